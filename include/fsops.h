@@ -281,6 +281,120 @@ fsops_status fsops_mxfp8_paged_decode_attention(const void* q_bf16, const uint8_
 size_t fsops_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int page_size, int max_pages);
 
 /* ------------------------------------------------------------------------
+ * What a decoder layer does around that cache: the position rotation (with the
+ * per-head norm of Qwen3-like layers) of q and k, the append of new keys and
+ * values, and the attention of a chunk of new tokens -- a prompt or a part of
+ * one, drafted tokens to verify, a single token -- over it.  The pages list
+ * MXFP8 FlashAttention with paged prefill ("extend") beside the paged decode
+ * (p2 "Ya esta disponible") and write none of this out; the definitions here
+ * are the standard ones.
+ *
+ * A batch of B sequences is described by
+ *   cu        [B + 1] int32: sequence b's new tokens are the rows cu[b] ..
+ *             cu[b + 1] - 1 of the row buffers (n_b of them, 0 allowed);
+ *             cu[0] >= 0, not decreasing, cu[B] <= T.  Rows outside
+ *             [cu[0], cu[B]) are padding: not read, not written.
+ *   seq_lens  [B] int32: the length WITH the new tokens; row cu[b] + i is token
+ *             seq_lens[b] - n_b + i.  n_b <= seq_lens[b] <= max_pages * P.
+ *   block_table [B, max_pages] int32 as above.
+ * All three are read on the device (a captured graph replays with new
+ * contents).  Metadata outside these limits, or a page id outside
+ * [0, num_pages) that would be used, is reported in the status word
+ * (fsops_read_kernel_status on the pointer that holds it, site 1 for lengths
+ * and offsets, 2 for a page id) and never followed; what belongs to the
+ * sequence concerned is unspecified.
+ *
+ * Rotation: the first rotary_dim dimensions of a head form pairs (u, w), the
+ * pair i being elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when
+ * interleaved; it becomes (u cos a - w sin a, w cos a + u sin a) with
+ * a = position * inv_freq[i], the angle exact to 2^-31 turns at any int32
+ * position.  The other dimensions stay.
+ *   inv_freq    device, [rotary_dim / 2] fp32, finite.
+ *   rotary_dim  0 (no rotation) .. D, a multiple of 32. */
+typedef struct {
+  const float* inv_freq;
+  int rotary_dim;
+  int interleaved;
+} fsops_rope;
+
+/* fsops_qk_norm_rope -- per-head RMSNorm and rotation of queries and keys, one
+ * launch: y = rotate(RMSNorm(x) * gamma) per head, in fp32, rounded once to
+ * bf16.
+ *   q, k        bf16 rows of Hq, Hkv heads of D elements, ldq, ldk elements
+ *               apart (parts of one projection's rows, for instance).  Either
+ *               may be NULL with its head count 0.
+ *   gamma_q, gamma_k  [D] bf16; NULL: no norm (nor eps) for q, for k.
+ *   positions   [T] int32.
+ *   rope        host struct; NULL: no rotation (positions may be NULL then).
+ *   q_out, k_out  bf16, rows ldq_out, ldk_out apart; may be q, k themselves
+ *               with the same row distance (any other overlap is not).
+ *   T >= 0, D a multiple of 16 up to 256, Hq, Hkv <= 65535, T * heads < 2^31,
+ *   row distances multiples of 8 and at least heads * D, eps >= 0.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
+fsops_status fsops_qk_norm_rope(const void* q_bf16, long long ldq, const void* k_bf16, long long ldk,
+                                const void* gamma_q_bf16, const void* gamma_k_bf16, float eps,
+                                const int32_t* positions, const fsops_rope* rope, void* q_out_bf16,
+                                long long ldq_out, void* k_out_bf16, long long ldk_out, int T, int Hq, int Hkv, int D,
+                                void* stream);
+
+/* fsops_mxfp8_kv_append -- the new tokens' keys and values into the paged cache
+ * that fsops_mxfp8_paged_decode_attention and
+ * fsops_mxfp8_paged_chunk_attention read, one launch: k through the per-head
+ * norm (gamma_k_bf16 [D], NULL: none) and the rotation (rope NULL: none), v as
+ * it is, both quantised from fp32 by the MXFP8 rule above along D and written
+ * to their slots.  Other slots of the pages stay as they are.
+ *   k, v        bf16 [T] rows of Hkv heads of D elements, ldk, ldv apart.
+ *   positions   [T] int32 for the rotation; NULL: the token's place in its
+ *               sequence.
+ *   k_codes, k_scales, v_codes, v_scales, num_pages: the cache (above).
+ *   status      device word (4-byte aligned) for the report above; an
+ *               attention workspace's first word serves.
+ *   Limits: D = 128; P in {16, 32, 64, 128}; B, Hkv <= 65535; T >= 0;
+ *   T * Hkv < 2^31; row distances as above.  Two rows of one call must not fall
+ *   into the same slot (which of them stays is unspecified).
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
+fsops_status fsops_mxfp8_kv_append(const void* k_bf16, long long ldk, const void* v_bf16, long long ldv,
+                                   const void* gamma_k_bf16, float eps, const int32_t* positions,
+                                   const fsops_rope* rope, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                                   uint8_t* v_scales, int num_pages, const int32_t* block_table, int max_pages,
+                                   const int32_t* cu, const int32_t* seq_lens, int T, int B, int Hkv, int D,
+                                   int page_size, uint32_t* status, void* stream);
+
+/* fsops_mxfp8_paged_chunk_attention -- causal attention of every new token over
+ * its sequence's cache (its own slot included: append first):
+ *   s[t] = sm_scale * q[i, h, :] . K^[t, h / G, :]  for the tokens t <= p and,
+ *   with window > 0, t > p - window, p the row's token (see cu above),
+ *   out[i, h, :] = bf16( sum_t softmax(s)[t] * V^[t, h / G, :] ).
+ * Scores, maxima and sums are fp32; the probabilities enter the second product
+ * rounded to bf16.
+ *   q           bf16 [T] rows of Hq heads of D, ldq elements apart.
+ *   out         bf16, rows ldo apart; must not overlap q.  Padding rows stay as
+ *               they are.
+ *   window      0: none; else >= 1.  Pages that no row of a call sees are not
+ *               read (their ids may be stale).
+ *   Limits: D = 128; P in {16, 32, 64, 128}; Hq / Hkv any whole number up to
+ *   64; B, Hkv <= 65535; T * Hq < 2^31; max_pages * P <= 2^24;
+ *   num_pages * Hkv * P < 2^31.  Pointers 16-byte aligned (block_table, cu,
+ *   seq_lens 4), row distances multiples of 8 and at least Hq * D.
+ *   workspace: 256-byte aligned, fsops_paged_chunk_attention_workspace_bytes()
+ *   of device memory, zero before its first use (the status word and counters;
+ *   each call leaves the counters zero).  One launch; graph-capture safe.
+ *   Calls sharing a workspace must be ordered (one stream, or events).
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
+fsops_status fsops_mxfp8_paged_chunk_attention(const void* q_bf16, long long ldq, const uint8_t* k_codes,
+                                               const uint8_t* k_scales, const uint8_t* v_codes,
+                                               const uint8_t* v_scales, int num_pages, const int32_t* block_table,
+                                               int max_pages, const int32_t* cu, const int32_t* seq_lens,
+                                               void* out_bf16, long long ldo, int T, int B, int Hq, int Hkv, int D,
+                                               int page_size, int window, float sm_scale, void* workspace,
+                                               size_t ws_bytes, void* stream);
+
+/* Workspace bytes of fsops_mxfp8_paged_chunk_attention for up to T rows on the
+ * current device (0 if the shape is unsupported).  A workspace serves every
+ * call whose own requirement is not larger. */
+size_t fsops_paged_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int page_size, int max_pages);
+
+/* ------------------------------------------------------------------------
  * FP8 with 128 x 128 block scales -- the second scale format the Fish Audio
  * post names beside mxfp8 ("bsgemm", X copy "Custom kernels for the shapes
  * TTS actually uses"; p2 "Estrategia de cuantizacion FP8").  The pages give

@@ -29,6 +29,8 @@ __all__ = [
     "fsops_blockscale_scale_count", "fsops_fp8_blockscale_gemm", "fsops_blockscale_gemm_workspace_bytes",
     "fsops_status_string", "fsops_version", "fsops_last_cuda_error", "fsops_rmsnorm_quantize_mxfp8",
     "fsops_mxfp8_swiglu_mlp_block", "fsops_mxfp8_paged_decode_attention", "fsops_paged_attention_workspace_bytes",
+    "fsops_qk_norm_rope", "fsops_mxfp8_kv_append", "fsops_mxfp8_paged_chunk_attention",
+    "fsops_paged_chunk_attention_workspace_bytes",
     "quantize_weight", "MLPWeights", "prepare_mlp_weights", "quantize_blockscale",
     "Workspace", "pair_gate_up",
 ]
@@ -53,6 +55,11 @@ class _MlpScales(ctypes.Structure):
     _fields_ = [("gateup", _vp), ("down", _vp)]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", _vp), ("rotary_dim", _i), ("interleaved", _i)]
+
+
+_ll = ctypes.c_longlong
 _SIGS = {
     "fsops_quantize_mxfp8": ([_vp, _i, _i, _i, _vp, _vp, _i, _vp], _i),
     "fsops_scale_bytes": ([_i, _i, _i], _sz),
@@ -74,6 +81,13 @@ _SIGS = {
     "fsops_mxfp8_paged_decode_attention": ([_vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
                                             ctypes.c_float, _vp, _sz, _vp], _i),
     "fsops_paged_attention_workspace_bytes": ([_i, _i, _i, _i, _i, _i], _sz),
+    "fsops_qk_norm_rope": ([_vp, _ll, _vp, _ll, _vp, _vp, ctypes.c_float, _vp, ctypes.POINTER(_Rope), _vp, _ll, _vp,
+                            _ll, _i, _i, _i, _i, _vp], _i),
+    "fsops_mxfp8_kv_append": ([_vp, _ll, _vp, _ll, _vp, ctypes.c_float, _vp, ctypes.POINTER(_Rope), _vp, _vp, _vp, _vp,
+                               _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp], _i),
+    "fsops_mxfp8_paged_chunk_attention": ([_vp, _ll, _vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _ll, _i, _i, _i,
+                                           _i, _i, _i, _i, ctypes.c_float, _vp, _sz, _vp], _i),
+    "fsops_paged_chunk_attention_workspace_bytes": ([_i, _i, _i, _i, _i, _i, _i], _sz),
     "fsops_mlp_workspace_bytes": ([_i, _i, _i], _sz),
     "fsops_set_workspace": ([_vp, _sz], _i),
     "fsops_read_kernel_status": ([_vp, ctypes.POINTER(_u32)], _i),
@@ -226,6 +240,63 @@ def fsops_mxfp8_paged_decode_attention(q, k_codes, k_scales, v_codes, v_scales, 
                                                   _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, page_size, sm_scale,
                                                   _ptr(workspace), ws_bytes, _stream(stream)),
            "fsops_mxfp8_paged_decode_attention")
+
+
+def _dev_ptr(t, where: str) -> Optional[int]:
+    """Pointer of a tensor of the current device (an address or None as it is)."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise FsopsError(ERR_INVALID_ARG, where + " (a tensor that is not on the GPU)")
+    return t.data_ptr()
+
+
+def _rope(rope, where: str):
+    if rope is None:
+        return None
+    inv_freq, rotary_dim, interleaved = rope
+    return ctypes.byref(_Rope(_dev_ptr(inv_freq, where), rotary_dim, 1 if interleaved else 0))
+
+
+def fsops_qk_norm_rope(q, ldq: int, k, ldk: int, gamma_q, gamma_k, eps: float, positions, rope, q_out, ldq_out: int,
+                       k_out, ldk_out: int, T: int, Hq: int, Hkv: int, D: int, stream=None) -> None:
+    """Per-head RMSNorm and rotation of q and k.  ``rope`` is (inv_freq,
+    rotary_dim, interleaved) or None."""
+    w = "fsops_qk_norm_rope"
+    _check(lib.fsops_qk_norm_rope(_dev_ptr(q, w), ldq, _dev_ptr(k, w), ldk, _dev_ptr(gamma_q, w), _dev_ptr(gamma_k, w),
+                                  eps, _dev_ptr(positions, w), _rope(rope, w), _dev_ptr(q_out, w), ldq_out,
+                                  _dev_ptr(k_out, w), ldk_out, T, Hq, Hkv, D, _stream(stream)), w)
+
+
+def fsops_mxfp8_kv_append(k, ldk: int, v, ldv: int, gamma_k, eps: float, positions, rope, k_codes, k_scales, v_codes,
+                          v_scales, num_pages: int, block_table, max_pages: int, cu, seq_lens, T: int, B: int,
+                          Hkv: int, D: int, page_size: int, status, stream=None) -> None:
+    """New keys (norm, rotation) and values into the paged MXFP8 cache (see fsops.h)."""
+    w = "fsops_mxfp8_kv_append"
+    _check(lib.fsops_mxfp8_kv_append(_dev_ptr(k, w), ldk, _dev_ptr(v, w), ldv, _dev_ptr(gamma_k, w), eps,
+                                     _dev_ptr(positions, w), _rope(rope, w), _dev_ptr(k_codes, w),
+                                     _dev_ptr(k_scales, w), _dev_ptr(v_codes, w), _dev_ptr(v_scales, w), num_pages,
+                                     _dev_ptr(block_table, w), max_pages, _dev_ptr(cu, w), _dev_ptr(seq_lens, w), T, B,
+                                     Hkv, D, page_size, _dev_ptr(status, w), _stream(stream)), w)
+
+
+def fsops_paged_chunk_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int, page_size: int,
+                                                max_pages: int) -> int:
+    return lib.fsops_paged_chunk_attention_workspace_bytes(T, B, Hq, Hkv, D, page_size, max_pages)
+
+
+def fsops_mxfp8_paged_chunk_attention(q, ldq: int, k_codes, k_scales, v_codes, v_scales, num_pages: int, block_table,
+                                      max_pages: int, cu, seq_lens, out, ldo: int, T: int, B: int, Hq: int, Hkv: int,
+                                      D: int, page_size: int, window: int, sm_scale: float, workspace, ws_bytes: int,
+                                      stream=None) -> None:
+    """Causal attention of each sequence's new tokens over the paged MXFP8 KV cache (see fsops.h)."""
+    w = "fsops_mxfp8_paged_chunk_attention"
+    _check(lib.fsops_mxfp8_paged_chunk_attention(_dev_ptr(q, w), ldq, _dev_ptr(k_codes, w), _dev_ptr(k_scales, w),
+                                                 _dev_ptr(v_codes, w), _dev_ptr(v_scales, w), num_pages,
+                                                 _dev_ptr(block_table, w), max_pages, _dev_ptr(cu, w),
+                                                 _dev_ptr(seq_lens, w), _dev_ptr(out, w), ldo, T, B, Hq, Hkv, D,
+                                                 page_size, window, sm_scale, _dev_ptr(workspace, w), ws_bytes,
+                                                 _stream(stream)), w)
 
 
 def fsops_mxfp8_swiglu_mlp_block(x_bf16, gamma_bf16, eps: float, residual: bool, w_gateup, w_down, scales, y_bf16,

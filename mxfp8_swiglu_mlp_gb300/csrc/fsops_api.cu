@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -18,6 +19,8 @@
 #include "mx_internal.h"
 #include "mx_tiled.h"
 #include "mx_attention.h"
+#include "mx_chunk.h"
+#include "mx_rope.h"
 #include "mx_slice.h"
 #include "mx_small.h"
 #include "mx_blockscale.h"
@@ -977,6 +980,229 @@ fsops_status fsops_mxfp8_paged_decode_attention(const void* q_bf16, const uint8_
 #endif
   const cudaError_t e = launch_paged_decode(aa, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FSOPS_OK : cuda_failed(e, "paged_decode_kernel launch");
+}
+
+}  // extern "C"
+
+namespace {
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// Rows of `heads` heads of D bf16 elements, ld elements apart.
+bool row_distance_ok(long long ld, int heads, int D) {
+  return ld % 8 == 0 && ld >= static_cast<long long>(heads) * D && ld < (1LL << 40);
+}
+// The rotation's description; a null one is no rotation.
+fsops_status rope_args(const fsops_rope* rope, int D, RopeArgs* r) {
+  r->inv_freq = nullptr;
+  r->R = 0;
+  r->interleaved = 0;
+  if (rope == nullptr || rope->rotary_dim == 0) return FSOPS_OK;
+  if (rope->rotary_dim < 0 || rope->rotary_dim > D || rope->rotary_dim % 32 != 0) return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  if (rope->inv_freq == nullptr || (rope->interleaved != 0 && rope->interleaved != 1)) return FSOPS_ERR_INVALID_ARG;
+  if (!aligned4(rope->inv_freq)) return FSOPS_ERR_MISALIGNED;
+  r->inv_freq = rope->inv_freq;
+  r->R = rope->rotary_dim;
+  r->interleaved = rope->interleaved;
+  return FSOPS_OK;
+}
+bool eps_ok(float eps) { return eps >= 0.0f && eps <= 1e30f; }  // also rejects NaN
+int log2_of(int v) {
+  int l = 0;
+  while ((1 << l) < v) ++l;
+  return l;
+}
+// Shape of a paged batch of new tokens (the append and the chunk attention).
+fsops_status paged_rows_shape(int T, int B, int heads, int Hkv, int D, int P, int num_pages, int max_pages) {
+  if (T < 0 || B < 1 || B > 65535 || Hkv < 1 || Hkv > 65535 || heads > 65535) return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  if (static_cast<long long>(T) * heads >= (1LL << 31)) return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  if (D != kChunkD || (P != 16 && P != 32 && P != 64 && P != 128)) return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  if (num_pages < 1 || max_pages < 1 || static_cast<long long>(max_pages) * P > (1LL << 24))
+    return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  if (static_cast<long long>(num_pages) * Hkv * P >= (1LL << 31)) return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  return FSOPS_OK;
+}
+fsops_status chunk_shape(int T, int B, int Hq, int Hkv, int D, int P, int num_pages, int max_pages) {
+  const fsops_status st = paged_rows_shape(T, B, Hq, Hkv, D, P, num_pages, max_pages);
+  if (st != FSOPS_OK) return st;
+  if (Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > kChunkMaxGroup) return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  return FSOPS_OK;
+}
+size_t chunk_rec_offset() { return kChunkHeaderBytes + kChunkMaxGroups * sizeof(uint32_t); }
+size_t chunk_ws_bytes(uint32_t rec_rows) {
+  return round_up(chunk_rec_offset() + static_cast<size_t>(rec_rows) * (kChunkD * sizeof(float) + sizeof(float2)), 256);
+}
+}  // namespace
+
+extern "C" {
+
+fsops_status fsops_qk_norm_rope(const void* q_bf16, long long ldq, const void* k_bf16, long long ldk,
+                                const void* gamma_q_bf16, const void* gamma_k_bf16, float eps,
+                                const int32_t* positions, const fsops_rope* rope, void* q_out_bf16,
+                                long long ldq_out, void* k_out_bf16, long long ldk_out, int T, int Hq, int Hkv, int D,
+                                void* stream) {
+  if (T < 0 || D < 16 || D > 256 || D % 16 != 0 || Hq < 0 || Hkv < 0 || Hq > 65535 || Hkv > 65535)
+    return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  if (static_cast<long long>(T) * (Hq + Hkv) >= (1LL << 31)) return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  if ((q_bf16 == nullptr) != (Hq == 0) || (k_bf16 == nullptr) != (Hkv == 0)) return FSOPS_ERR_INVALID_ARG;
+  if ((Hq > 0 && q_out_bf16 == nullptr) || (Hkv > 0 && k_out_bf16 == nullptr) || !eps_ok(eps))
+    return FSOPS_ERR_INVALID_ARG;
+  NormRopeArgs na;
+  std::memset(&na, 0, sizeof(na));
+  fsops_status st = rope_args(rope, D, &na.rope);
+  if (st != FSOPS_OK) return st;
+  if (na.rope.R > 0 && positions == nullptr) return FSOPS_ERR_INVALID_ARG;
+  if (Hq > 0 && (!row_distance_ok(ldq, Hq, D) || !row_distance_ok(ldq_out, Hq, D))) return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  if (Hkv > 0 && (!row_distance_ok(ldk, Hkv, D) || !row_distance_ok(ldk_out, Hkv, D)))
+    return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  if ((q_bf16 != nullptr && q_bf16 == q_out_bf16 && ldq != ldq_out) ||
+      (k_bf16 != nullptr && k_bf16 == k_out_bf16 && ldk != ldk_out))
+    return FSOPS_ERR_INVALID_ARG;
+  if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(gamma_q_bf16) || !aligned16(gamma_k_bf16) ||
+      !aligned16(q_out_bf16) || !aligned16(k_out_bf16) || !aligned4(positions))
+    return FSOPS_ERR_MISALIGNED;
+  if (T == 0 || Hq + Hkv == 0) return FSOPS_OK;
+  int dev;
+  const DeviceInfo* di;
+  st = current_device(&dev, &di);
+  if (st != FSOPS_OK) return st;
+  na.x[0] = static_cast<const uint16_t*>(q_bf16);
+  na.x[1] = static_cast<const uint16_t*>(k_bf16);
+  na.y[0] = static_cast<uint16_t*>(q_out_bf16);
+  na.y[1] = static_cast<uint16_t*>(k_out_bf16);
+  na.ldx[0] = ldq;
+  na.ldx[1] = ldk;
+  na.ldy[0] = ldq_out;
+  na.ldy[1] = ldk_out;
+  na.gamma[0] = static_cast<const uint16_t*>(gamma_q_bf16);
+  na.gamma[1] = static_cast<const uint16_t*>(gamma_k_bf16);
+  na.positions = positions;
+  na.eps = eps;
+  na.T = T;
+  na.H[0] = Hq;
+  na.H[1] = Hkv;
+  na.D = D;
+  const cudaError_t e = launch_norm_rope(na, di->sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FSOPS_OK : cuda_failed(e, "norm_rope_kernel launch");
+}
+
+fsops_status fsops_mxfp8_kv_append(const void* k_bf16, long long ldk, const void* v_bf16, long long ldv,
+                                   const void* gamma_k_bf16, float eps, const int32_t* positions,
+                                   const fsops_rope* rope, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                                   uint8_t* v_scales, int num_pages, const int32_t* block_table, int max_pages,
+                                   const int32_t* cu, const int32_t* seq_lens, int T, int B, int Hkv, int D,
+                                   int page_size, uint32_t* status, void* stream) {
+  fsops_status st = paged_rows_shape(T, B, Hkv, Hkv, D, page_size, num_pages, max_pages);
+  if (st != FSOPS_OK) return st;
+  if (k_bf16 == nullptr || v_bf16 == nullptr || k_codes == nullptr || k_scales == nullptr || v_codes == nullptr ||
+      v_scales == nullptr || block_table == nullptr || cu == nullptr || seq_lens == nullptr || status == nullptr ||
+      !eps_ok(eps))
+    return FSOPS_ERR_INVALID_ARG;
+  if (!row_distance_ok(ldk, Hkv, D) || !row_distance_ok(ldv, Hkv, D)) return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  KvAppendArgs ka;
+  std::memset(&ka, 0, sizeof(ka));
+  st = rope_args(rope, D, &ka.rope);
+  if (st != FSOPS_OK) return st;
+  if (!aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(gamma_k_bf16) || !aligned16(k_codes) ||
+      !aligned16(v_codes) || !aligned16(k_scales) || !aligned16(v_scales) || !aligned4(block_table) ||
+      !aligned4(cu) || !aligned4(seq_lens) || !aligned4(status) || !aligned4(positions))
+    return FSOPS_ERR_MISALIGNED;
+  if (T == 0) return FSOPS_OK;
+  int dev;
+  const DeviceInfo* di;
+  st = current_device(&dev, &di);
+  if (st != FSOPS_OK) return st;
+  ka.x[0] = static_cast<const uint16_t*>(k_bf16);
+  ka.x[1] = static_cast<const uint16_t*>(v_bf16);
+  ka.ldx[0] = ldk;
+  ka.ldx[1] = ldv;
+  ka.gamma = static_cast<const uint16_t*>(gamma_k_bf16);
+  ka.positions = positions;
+  ka.eps = eps;
+  ka.codes[0] = k_codes;
+  ka.codes[1] = v_codes;
+  ka.scales[0] = k_scales;
+  ka.scales[1] = v_scales;
+  ka.table = block_table;
+  ka.cu = cu;
+  ka.lens = seq_lens;
+  ka.status = status;
+  ka.T = T;
+  ka.B = B;
+  ka.Hkv = Hkv;
+  ka.log2P = log2_of(page_size);
+  ka.num_pages = num_pages;
+  ka.max_pages = max_pages;
+  const cudaError_t e = launch_kv_append(ka, di->sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FSOPS_OK : cuda_failed(e, "kv_append_kernel launch");
+}
+
+size_t fsops_paged_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int page_size,
+                                                   int max_pages) {
+  if (chunk_shape(T, B, Hq, Hkv, D, page_size, 1, max_pages) != FSOPS_OK) return 0;
+  int dev;
+  const DeviceInfo* di;
+  if (current_device(&dev, &di) != FSOPS_OK) return 0;
+  return chunk_ws_bytes(chunk_rec_rows(T, Hq, di->sms));
+}
+
+fsops_status fsops_mxfp8_paged_chunk_attention(const void* q_bf16, long long ldq, const uint8_t* k_codes,
+                                               const uint8_t* k_scales, const uint8_t* v_codes,
+                                               const uint8_t* v_scales, int num_pages, const int32_t* block_table,
+                                               int max_pages, const int32_t* cu, const int32_t* seq_lens,
+                                               void* out_bf16, long long ldo, int T, int B, int Hq, int Hkv, int D,
+                                               int page_size, int window, float sm_scale, void* workspace,
+                                               size_t ws_bytes, void* stream) {
+  fsops_status st = chunk_shape(T, B, Hq, Hkv, D, page_size, num_pages, max_pages);
+  if (st != FSOPS_OK) return st;
+  if (q_bf16 == nullptr || k_codes == nullptr || k_scales == nullptr || v_codes == nullptr || v_scales == nullptr ||
+      block_table == nullptr || cu == nullptr || seq_lens == nullptr || out_bf16 == nullptr || workspace == nullptr)
+    return FSOPS_ERR_INVALID_ARG;
+  if (window < 0 || !(sm_scale == sm_scale) || sm_scale > 1e30f || sm_scale < -1e30f) return FSOPS_ERR_INVALID_ARG;
+  if (!row_distance_ok(ldq, Hq, D) || !row_distance_ok(ldo, Hq, D)) return FSOPS_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(q_bf16) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) ||
+      !aligned16(v_scales) || !aligned16(out_bf16) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      !aligned4(block_table) || !aligned4(cu) || !aligned4(seq_lens))
+    return FSOPS_ERR_MISALIGNED;
+  if (q_bf16 == out_bf16) return FSOPS_ERR_INVALID_ARG;
+  if (T == 0) return FSOPS_OK;
+  int dev;
+  const DeviceInfo* di;
+  st = current_device(&dev, &di);
+  if (st != FSOPS_OK) return st;
+  ChunkArgs ca;
+  std::memset(&ca, 0, sizeof(ca));
+  ca.rec_rows = chunk_rec_rows(T, Hq, di->sms);
+  if (ws_bytes < chunk_ws_bytes(ca.rec_rows)) return FSOPS_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  ca.q = static_cast<const uint16_t*>(q_bf16);
+  ca.out = static_cast<uint16_t*>(out_bf16);
+  ca.ldq = ldq;
+  ca.ldo = ldo;
+  ca.kc = k_codes;
+  ca.ks = k_scales;
+  ca.vc = v_codes;
+  ca.vs = v_scales;
+  ca.table = block_table;
+  ca.cu = cu;
+  ca.lens = seq_lens;
+  ca.status = reinterpret_cast<uint32_t*>(ws);
+  ca.work = ca.status + 1;
+  ca.done = ca.status + 2;
+  ca.groups = reinterpret_cast<uint32_t*>(ws + kChunkHeaderBytes);
+  ca.rec = reinterpret_cast<float*>(ws + chunk_rec_offset());
+  ca.rec_ml = reinterpret_cast<float2*>(ca.rec + static_cast<size_t>(ca.rec_rows) * kChunkD);
+  ca.T = T;
+  ca.B = B;
+  ca.Hq = Hq;
+  ca.Hkv = Hkv;
+  ca.G = Hq / Hkv;
+  ca.log2P = log2_of(page_size);
+  ca.num_pages = num_pages;
+  ca.max_pages = max_pages;
+  ca.window = window;
+  ca.scale_log2 = sm_scale * 1.4426950408889634f;
+  ca.timeout_ns = g_timeout_ns.load();
+  const cudaError_t e = launch_chunk(ca, di->sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FSOPS_OK : cuda_failed(e, "chunk_kernel launch");
 }
 
 fsops_status fsops_rmsnorm_quantize_mxfp8(const void* x_bf16, const void* gamma_bf16, float eps, int rows, int K,

@@ -50,6 +50,12 @@ What it computes, step by step, and where the step comes from:
    the codes are defined bit for bit (``quantize_blockscale``); the GEMM
    (``gemm_blockscale``) is then exact up to float64 rounding.
 
+9. What a decoder layer does around that cache, by the standard definitions
+   (the pages list the paged prefill beside the paged decode and write none of
+   it out): the per-head RMSNorm with position rotation (``norm_rope``) and the
+   causal attention of a chunk of new tokens, optionally through a sliding
+   window (``paged_chunk_attention``), both in float64.
+
 Weight scales may be returned in the row-major layout or in the tiled layout
 the library consumes (``scales_rowmajor_to_tiled``): 128-row x 4-block tiles
 of 512 bytes, tile (rt, kg) at byte (rt * ceil(K/128) + kg) * 512, entry
@@ -304,6 +310,61 @@ def paged_decode_attention(q_bits: np.ndarray, k_codes: np.ndarray, k_scales: np
                 w = np.exp(s - s.max())
                 out[b, h] = (w / w.sum()) @ v
     return {"out": out, "out_bf16": round_bf16_bits(out)}
+
+
+def norm_rope(x: np.ndarray, gamma, eps: float, positions, inv_freq, rotary_dim: int, interleaved: bool) -> np.ndarray:
+    """x [T, H, D] (float64) through the per-head RMSNorm (gamma [D] float64 or
+    None) and the rotation of its first rotary_dim dimensions: the pairs
+    (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when interleaved, turned by
+    positions[t] * inv_freq[i]."""
+    x = np.array(x, np.float64)
+    if gamma is not None:
+        x = x / np.sqrt(np.mean(x * x, axis=-1, keepdims=True) + eps) * np.asarray(gamma, np.float64)
+    R = rotary_dim
+    if R:
+        a = np.asarray(positions, np.float64)[:, None] * np.asarray(inv_freq, np.float64)[None, :]
+        cos, sin = np.cos(a)[:, None, :], np.sin(a)[:, None, :]
+        first = slice(0, R, 2) if interleaved else slice(0, R // 2)
+        second = slice(1, R, 2) if interleaved else slice(R // 2, R)
+        u, w = x[..., first].copy(), x[..., second].copy()
+        x[..., first] = u * cos - w * sin
+        x[..., second] = w * cos + u * sin
+    return x
+
+
+def paged_chunk_attention(q: np.ndarray, k_codes: np.ndarray, k_scales: np.ndarray, v_codes: np.ndarray,
+                          v_scales: np.ndarray, block_table: np.ndarray, cu, seq_lens, window: int,
+                          sm_scale: float) -> Dict[str, np.ndarray]:
+    """Causal attention of each sequence's new tokens over the paged cache, in
+    float64: row cu[b] + i of q [T, Hq, D] is token seq_lens[b] - n_b + i and
+    sees the tokens up to itself (the last ``window`` of them for window > 0).
+    Returns out [T, Hq, D] (zero in rows of no sequence), absv (the softmax
+    average of |V|) and mag (the largest sm_scale sum_d |q_d K_d| a row sees)."""
+    T, Hq, D = q.shape
+    _, Hkv, P, _ = k_codes.shape
+    G = Hq // Hkv
+    out, absv, mag = np.zeros((T, Hq, D)), np.zeros((T, Hq, D)), np.zeros((T, Hq))
+    for b in range(len(seq_lens)):
+        c0, n, L = int(cu[b]), int(cu[b + 1] - cu[b]), int(seq_lens[b])
+        if n == 0:
+            continue
+        pos = np.arange(L - n, L)[:, None]
+        first = max(0, L - n - window + 1) if window else 0
+        t = np.arange(first, L)
+        seen = (t <= pos) & ((t > pos - window) if window else True)
+        page, slot = block_table[b, t // P], t % P
+        for hk in range(Hkv):
+            k = dequantize(k_codes[page, hk, slot], k_scales[page, hk, slot])
+            v = dequantize(v_codes[page, hk, slot], v_scales[page, hk, slot])
+            for h in range(hk * G, hk * G + G):
+                s = np.where(seen, sm_scale * (q[c0:c0 + n, h] @ k.T), -np.inf)
+                w = np.exp(s - s.max(axis=1, keepdims=True))
+                w /= w.sum(axis=1, keepdims=True)
+                out[c0:c0 + n, h] = w @ v
+                absv[c0:c0 + n, h] = w @ np.abs(v)
+                m = abs(sm_scale) * (np.abs(q[c0:c0 + n, h]) @ np.abs(k).T)
+                mag[c0:c0 + n, h] = np.where(seen, m, 0).max(axis=1)
+    return {"out": out, "absv": absv, "mag": mag}
 
 
 # ---------------------------------------------------------------- 128x128 block scales
