@@ -1026,9 +1026,10 @@ fsops_status chunk_shape(int T, int B, int Hq, int Hkv, int D, int P, int num_pa
   if (Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > kChunkMaxGroup) return FSOPS_ERR_UNSUPPORTED_SHAPE;
   return FSOPS_OK;
 }
-size_t chunk_rec_offset() { return kChunkHeaderBytes + kChunkMaxGroups * sizeof(uint32_t); }
-size_t chunk_ws_bytes(uint32_t rec_rows) {
-  return round_up(chunk_rec_offset() + static_cast<size_t>(rec_rows) * (kChunkD * sizeof(float) + sizeof(float2)), 256);
+size_t chunk_rec_offset() { return kChunkHeaderBytes + kChunkCounterBytes; }
+size_t chunk_ws_bytes(int sms, int slot_rows) {
+  const size_t rows = static_cast<size_t>(chunk_slots(sms)) * slot_rows;
+  return round_up(chunk_rec_offset() + rows * (kChunkD * sizeof(float) + sizeof(float2)), 256);
 }
 }  // namespace
 
@@ -1141,7 +1142,7 @@ size_t fsops_paged_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv
   int dev;
   const DeviceInfo* di;
   if (current_device(&dev, &di) != FSOPS_OK) return 0;
-  return chunk_ws_bytes(chunk_rec_rows(T, Hq, di->sms));
+  return chunk_ws_bytes(di->sms, chunk_slot_rows(T, Hq / Hkv, 256));
 }
 
 fsops_status fsops_mxfp8_paged_chunk_attention(const void* q_bf16, long long ldq, const uint8_t* k_codes,
@@ -1170,8 +1171,11 @@ fsops_status fsops_mxfp8_paged_chunk_attention(const void* q_bf16, long long ldq
   if (st != FSOPS_OK) return st;
   ChunkArgs ca;
   std::memset(&ca, 0, sizeof(ca));
-  ca.rec_rows = chunk_rec_rows(T, Hq, di->sms);
-  if (ws_bytes < chunk_ws_bytes(ca.rec_rows)) return FSOPS_ERR_INVALID_ARG;
+  ca.G = Hq / Hkv;
+  ca.tile_rows = chunk_tile_rows(T, B, ca.G);
+  ca.slot_rows = chunk_slot_rows(T, ca.G, ca.tile_rows);
+  ca.grid = di->sms;
+  if (ws_bytes < chunk_ws_bytes(di->sms, ca.slot_rows)) return FSOPS_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   ca.q = static_cast<const uint16_t*>(q_bf16);
   ca.out = static_cast<uint16_t*>(out_bf16);
@@ -1185,23 +1189,22 @@ fsops_status fsops_mxfp8_paged_chunk_attention(const void* q_bf16, long long ldq
   ca.cu = cu;
   ca.lens = seq_lens;
   ca.status = reinterpret_cast<uint32_t*>(ws);
-  ca.work = ca.status + 1;
-  ca.done = ca.status + 2;
-  ca.groups = reinterpret_cast<uint32_t*>(ws + kChunkHeaderBytes);
+  ca.count = reinterpret_cast<uint32_t*>(ws + kChunkHeaderBytes);
   ca.rec = reinterpret_cast<float*>(ws + chunk_rec_offset());
-  ca.rec_ml = reinterpret_cast<float2*>(ca.rec + static_cast<size_t>(ca.rec_rows) * kChunkD);
+  ca.rec_ml = reinterpret_cast<float2*>(ca.rec + static_cast<size_t>(chunk_slots(di->sms)) * ca.slot_rows * kChunkD);
   ca.T = T;
   ca.B = B;
   ca.Hq = Hq;
   ca.Hkv = Hkv;
-  ca.G = Hq / Hkv;
   ca.log2P = log2_of(page_size);
   ca.num_pages = num_pages;
   ca.max_pages = max_pages;
   ca.window = window;
-  ca.scale_log2 = sm_scale * 1.4426950408889634f;
+  // a scale of zero: so small a one that every exponent is zero, and the mask still -inf
+  ca.scale_log2 = std::fmax(std::fabs(sm_scale) * 1.4426950408889634f, 1e-37f);
+  ca.negate = sm_scale < 0.f ? 1 : 0;
   ca.timeout_ns = g_timeout_ns.load();
-  const cudaError_t e = launch_chunk(ca, di->sms, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_chunk(ca, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FSOPS_OK : cuda_failed(e, "chunk_kernel launch");
 }
 

@@ -3,22 +3,31 @@
 //
 //   out[i, h] = sum_t p[t] V^[t] / sum_t p[t],  p[t] = exp(sm_scale q[i, h] . K^[t] - m)
 //   over the tokens t <= pos(i) (and t > pos(i) - window),
-// with K^, V^ the dequantised cache and m the running maximum of the row: one
-// pass over the keys, the sums rescaled when m grows.
+// with K^, V^ the dequantised cache: one pass over the keys in tiles of 128,
+// with a running maximum m and sum a row.
 //
-//   chunk_kernel  items of 64 rows (tokens x query heads of a KV head) against
-//                 64 keys at a time: the block's threads turn the codes into
-//                 bf16 in shared memory (exact: an E4M3 value times a power of
-//                 two has four significant bits), each warp multiplies 16 rows
-//                 with mma.sync, softmax in registers.
+// One persistent block an SM; its share of the work is a range of key tiles of
+// consecutive query tiles (mx_chunk_plan.cuh).  Its warps:
+//   softmax   two groups of four warps, a thread a row: scores from tensor
+//             memory, exponentials, probabilities back as bf16;
+//   convert   E4M3 codes times their block's power of two to bf16 operand tiles
+//             in shared memory;
+//   mma       one thread issues the products (tcgen05, bf16, 128 x 128);
+//   load      walks the plan, copies pages of codes into a ring.
+// The two softmax groups ("streams") have score and output tiles of their own
+// in tensor memory (4 x 128 columns), so that the products of one run under the
+// exponentials of the other.  With more than 128 rows a stream is a half of the
+// query tile and both see every key tile; with fewer, the streams share the
+// rows and take the key tiles in turn, and their results are added at the end.
 //
-// p is rounded to bf16 for the second product (relative 2^-8 at most, the
-// size of the output's own rounding, and independent from token to token); the
-// sum of p that divides the result adds the same rounded values, so a row
-// that sees one token returns it exactly.  Scores, maxima and sums are fp32.
+// Exactness: an E4M3 value times a power of two has four significant bits, so
+// K^ and V^ are exact in bf16, as q is; scores are exact up to fp32 sums.  The
+// probabilities are rounded to bf16 for the second product (2^-8 at most, the
+// size of the output's own rounding, independent from token to token); maxima,
+// sums and outputs are fp32.  The maximum that scales a row is raised only when
+// it would grow by more than 2^8 (the bf16 probabilities keep their relative
+// precision up there), which spares nearly every rescaling of the outputs.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "mx_chunk.h"
 #include "mx_chunk_plan.cuh"
@@ -27,25 +36,98 @@ namespace fsops {
 
 namespace {
 
-constexpr int kTileRows = 64, kTileKeys = 64, kChunkThreads = 128;
-constexpr int kD = kChunkD;
+using chunk::Item;
+using chunk::kKeys;
 
-__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], const void* p) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(smem_u32(p))
-               : "memory");
+constexpr int kD = kChunkD;
+constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kBlock = 32 * (kLoadWarp + 3);          // warps come in groups of four
+constexpr uint32_t kCodes = kKeys * kD;               // bytes of a raw K or V tile
+constexpr uint32_t kScales = kKeys * kD / 32;
+constexpr uint32_t kOperand = kKeys * kD * 2;         // a bf16 tile: two halves of 64 dimensions,
+constexpr uint32_t kHalf = kOperand / 2;              // [128 rows][128 bytes], 128-byte swizzle
+constexpr int kSlots = 2;                             // bf16 K tiles, and V tiles
+constexpr float kGrow = 8.f;                          // in powers of two
+
+struct Ctl {
+  uint64_t raw_full[4], raw_empty[4];
+  uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
+  uint64_t s_full[2], p_full[2], o_done[2], q_full, fin;
+  uint64_t group[2], second, taken;  // barriers of a softmax group; the second stream's sums ready, and read
+  uint64_t it_full[2], it_empty[2];
+  Item item[2];
+  long long red[kBlock / 32];
+  uint32_t tmem, stop, last[2];
+};
+// Shared memory for MT halves of 128 rows of queries and a ring of NR raw tiles.
+template <int MT, int NR>
+struct Layout {
+  static constexpr uint32_t q = 0, k = MT * kOperand, v = k + kSlots * kOperand, raw = v + kSlots * kOperand,
+                            sc = raw + NR * kCodes, ctl = sc + NR * kScales, bytes = ctl + sizeof(Ctl);
+  static_assert(bytes <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
 }
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], const void* p) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(smem_u32(p))
-               : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
 }
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// kind::f16, fp32 sums, bf16 operands, M = N = 128; B K-major or (transposed) N-major.
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescBt = kIdesc | (1u << 16);
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+      "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
+      "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]),
+      "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, float a, float b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "f"(a), "f"(b) : "memory");
+}
+__device__ __forceinline__ void tmem_ld2(uint32_t taddr, float& a, float& b) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void bulk_load_plain(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   uint32_t r;
@@ -57,241 +139,647 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float scale_value(uint32_t s) {  // 2^(s - 127)
-  return s != 0 ? __uint_as_float(s << 23) : __uint_as_float(0x00400000u);
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
-// Four E4M3 codes times f as two words of bf16 pairs.
-__device__ __forceinline__ uint2 dequant4(uint32_t w, float f) {
-  const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3);
-  const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
-  const float2 x = __half22float2(__half2(lo)), y = __half22float2(__half2(hi));
-  return make_uint2(bf16x2_rn(x.x * f, x.y * f), bf16x2_rn(y.x * f, y.y * f));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
-// Byte offset of 16-byte piece c of row r in a [rows][128] bf16 tile.
-__device__ __forceinline__ int tile_ofs(int r, int c) { return r * 256 + ((c ^ (r & 7)) << 4); }
 
-// 64 tokens from `tok` of KV head hk into a bf16 tile; tokens outside
-// [lo, hi) become zeros (what the cache holds there is not read).
-__device__ __forceinline__ void load_tile(const ChunkArgs& a, const chunk::Item& w, const uint8_t* codes,
-                                          const uint8_t* scales, int tok, uint8_t* tile) {
-#pragma unroll
-  for (int i = 0; i < kTileKeys * 8 / kChunkThreads; ++i) {
-    const int r = (i * kChunkThreads + threadIdx.x) >> 3, c = threadIdx.x & 7;  // 16 codes: pieces 2 c, 2 c + 1
-    const int t = tok + r;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    float f = 0.f;
-    if (t >= w.lo && t < w.hi) {
-      const int page = __ldg(a.table + static_cast<long long>(w.b) * a.max_pages + (t >> a.log2P));
-      if (page >= 0 && page < a.num_pages) {
-        const long long row = ((static_cast<long long>(page) * a.Hkv + w.hk) << a.log2P) + (t & ((1 << a.log2P) - 1));
-        x = __ldg(reinterpret_cast<const uint4*>(codes + row * kD) + c);
-        f = scale_value(__ldg(scales + row * (kD / 32) + (c >> 1)));
-      } else {
-        atomicCAS(a.status, 0u, (1u << 24) | (2u << 16) | (static_cast<uint32_t>(w.b) & 0xFFFFu));
-      }
+struct Ctx {
+  const ChunkArgs& a;
+  Ctl* ctl;
+};
+// Bounded wait; false: the block gives up (the first reason is reported).
+__device__ __noinline__ bool wait_slow(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t site) {
+  const uint64_t t0 = globaltimer_ns();
+  volatile uint32_t* stop = &c.ctl->stop;
+  while (!mbar_try_wait(bar, parity)) {
+    if (*stop != 0u) return false;
+    if (globaltimer_ns() - t0 > c.a.timeout_ns) {
+      atomicCAS(c.a.status, 0u, (5u << 24) | (site << 16) | (blockIdx.x & 0xFFFFu));  // FSOPS_ERR_TIMEOUT
+      *stop = 1u;
+      return false;
     }
-    const uint2 p0 = dequant4(x.x, f), p1 = dequant4(x.y, f), p2 = dequant4(x.z, f), p3 = dequant4(x.w, f);
-    *reinterpret_cast<uint4*>(tile + tile_ofs(r, 2 * c)) = make_uint4(p0.x, p0.y, p1.x, p1.y);
-    *reinterpret_cast<uint4*>(tile + tile_ofs(r, 2 * c + 1)) = make_uint4(p2.x, p2.y, p3.x, p3.y);
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_one(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t site) {
+  return mbar_try_wait(bar, parity) || wait_slow(c, bar, parity, site);
+}
+// The same by a whole warp, whose lanes go on or give up together.
+__device__ __forceinline__ bool wait(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t site) {
+  return __all_sync(0xFFFFFFFFu, wait_one(c, bar, parity, site));
+}
+// A warp's arrival, after all its lanes' writes.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+// A position in a ring of n stages.
+template <int n>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == n) slot = 0, phase ^= 1u;
+  }
+};
+
+// Sixteen codes times m (a bf16 power of two, twice): four bf16 words for each
+// of the two 16-byte pieces.  A code s eeee mmm moved to s 0000eeee mmm0000 is
+// the bf16 2^-120 times its value (subnormal codes included), which m takes
+// back.  Within four codes the order is 0, 2, 1, 3: the queries are stored in
+// the same order, and the outputs' columns are put back at the end.
+__device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t m) {
+  const uint32_t even = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u);
+  const uint32_t odd = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
+  return make_uint2(mul_bf16x2(even, m), mul_bf16x2(odd, m));
+}
+
+// ---------------------------------------------------------------- load warp
+template <int NR>
+__device__ __forceinline__ bool load_tile(const Ctx& c, const Item& w, int tile, uint8_t* raw, uint8_t* sc,
+                                          Ring<NR>& ring, int lane) {
+  const ChunkArgs& a = c.a;
+  const int P = 1 << a.log2P, pages = kKeys >> a.log2P;
+  const int first = tile * kKeys + lane * P;  // first token of the lane's page
+  int pid = -1;
+  if (lane < pages && first < w.hi && first + P > w.lo) {
+    pid = __ldg(a.table + static_cast<long long>(w.b) * a.max_pages + (first >> a.log2P));
+    if (pid < 0 || pid >= a.num_pages) {
+      atomicCAS(a.status, 0u, (1u << 24) | (2u << 16) | (static_cast<uint32_t>(w.b) & 0xFFFFu));
+      pid = -1;
+    }
+  }
+  const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, pid >= 0)) * static_cast<uint32_t>(P) * kD;
+  // the scales of the lane's four tokens
+  const int sp = __shfl_sync(0xFFFFFFFFu, pid, (4 * lane) >> a.log2P);
+  uint4 ks = make_uint4(0u, 0u, 0u, 0u), vs = ks;
+  if (sp >= 0) {
+    const long long row = ((static_cast<long long>(sp) * a.Hkv + w.hk) << a.log2P) + ((4 * lane) & (P - 1));
+    ks = __ldg(reinterpret_cast<const uint4*>(a.ks + row * (kD / 32)));
+    vs = __ldg(reinterpret_cast<const uint4*>(a.vs + row * (kD / 32)));
+  }
+  const long long src = ((static_cast<long long>(max(pid, 0)) * a.Hkv + w.hk) << a.log2P) * kD;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    uint64_t* full = &c.ctl->raw_full[ring.slot];
+    if (!wait(c, &c.ctl->raw_empty[ring.slot], ring.phase ^ 1u, 3u)) return false;
+    fence_proxy_async_shared();
+    if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+    __syncwarp();
+    if (pid >= 0)
+      bulk_load_plain(raw + ring.slot * kCodes + lane * P * kD, (kv ? a.vc : a.kc) + src, P * kD, full);
+    reinterpret_cast<uint4*>(sc + ring.slot * kScales)[lane] = kv ? vs : ks;
+    mbar_arrive(full);
+    ring.step();
+  }
+  return true;
+}
+
+// ---------------------------------------------------------------- convert warps
+// A raw tile of tokens from tok0 to a bf16 tile; tokens outside [lo, hi) become
+// zeros whatever the ring holds there.
+__device__ __forceinline__ void convert_tile(const uint8_t* raw, const uint8_t* sc, uint8_t* out, int tok0, int lo, int hi,
+                                             int t) {
+  const int cpiece = t & 7, r0 = t >> 3;
+  const bool inside = tok0 >= lo && tok0 + kKeys <= hi;
+  uint8_t* half = out + (cpiece >> 2) * kHalf;
+  constexpr int kStep = 32 * kConvWarps / 8;  // rows of a pass
+#pragma unroll 4
+  for (int i = 0; i < kKeys / kStep; ++i) {
+    const int r = r0 + i * kStep;
+    const uint4 x = *reinterpret_cast<const uint4*>(raw + r * kD + 16 * cpiece);
+    const uint32_t s = sc[4 * r + (cpiece >> 1)];
+    const bool on = inside || (tok0 + r >= lo && tok0 + r < hi);
+    uint32_t m = on ? ((min(s, 134u) + 120u) << 7) * 0x10001u : 0u;  // 2^(s - 127 + 120)
+    uint2 p0 = widen4(x.x, m), p1 = widen4(x.y, m), p2 = widen4(x.z, m), p3 = widen4(x.w, m);
+    if (on && s > 134u) {  // 2^(s - 7) is beyond bf16: the rest of it
+      m = ((s - 134u + 127u) << 7) * 0x10001u;
+      p0 = make_uint2(mul_bf16x2(p0.x, m), mul_bf16x2(p0.y, m)), p1 = make_uint2(mul_bf16x2(p1.x, m), mul_bf16x2(p1.y, m));
+      p2 = make_uint2(mul_bf16x2(p2.x, m), mul_bf16x2(p2.y, m)), p3 = make_uint2(mul_bf16x2(p3.x, m), mul_bf16x2(p3.y, m));
+    }
+    // pieces 2 c and 2 c + 1 of the half's row; the lanes of the second half
+    // write theirs in the other order, so that eight lanes meet all banks
+    const int c0 = 2 * (cpiece & 3), odd = cpiece >> 2;
+    const uint4 a = make_uint4(p0.x, p0.y, p1.x, p1.y), b = make_uint4(p2.x, p2.y, p3.x, p3.y);
+    uint8_t* row = half + r * 128;
+    *reinterpret_cast<uint4*>(row + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? b : a;
+    *reinterpret_cast<uint4*>(row + (((c0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? a : b;
   }
 }
 
-__global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_constant__ ChunkArgs a) {
-  __shared__ __align__(128) uint8_t kt[kTileKeys * 256];
-  __shared__ __align__(128) uint8_t vt[kTileKeys * 256];
-  __shared__ unsigned long long red[kChunkThreads / 32];
-  __shared__ chunk::Item item;
-  __shared__ int flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
-  const int S = chunk::split_tiles(a, kTileRows, kTileKeys, 4, red);
-  chunk::Cursor cur;
-  if (warp == 0) cur.init(a, S, kTileRows, kTileKeys, lane);
+// ---------------------------------------------------------------- softmax warps
+// 128 rows of queries (rows from r0 of the sequence; the last one stands in
+// for rows past the end) into a bf16 tile, by `warps` warps.
+__device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item& w, int r0, uint8_t* tile, int first, int rows,
+                                             int warp, int lane) {
+  const int R = w.n * a.G;
+  const uint32_t flip = a.negate ? 0x80008000u : 0u;
+  const int c = lane & 15;  // 16-byte piece of the row
+  uint8_t* half = tile + (c >> 3) * kHalf;
+#pragma unroll 4
+  for (int i = warp * 2 + (lane >> 4); i < rows; i += 8) {
+    const int r = first + i, rr = min(r0 + r, R - 1), tok = rr / a.G;
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<long long>(w.c0 + tok) * a.ldq +
+                                                         (w.hk * a.G + rr - tok * a.G) * kD) + c);
+    uint4 y;
+    y.x = __byte_perm(x.x, x.y, 0x5410) ^ flip, y.y = __byte_perm(x.x, x.y, 0x7632) ^ flip;
+    y.z = __byte_perm(x.z, x.w, 0x5410) ^ flip, y.w = __byte_perm(x.z, x.w, 0x7632) ^ flip;
+    *reinterpret_cast<uint4*>(half + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = y;
+  }
+}
 
-  for (;;) {
-    __syncthreads();  // the previous item and its flag have been read
-    if (warp == 0) {
-      uint32_t it = 0;
-      if (lane == 0) it = atomicAdd(a.work, 1u);
-      it = __shfl_sync(0xFFFFFFFFu, it, 0);
-      chunk::Item w;
-      const bool some = cur.find(a, it, lane, w);
-      if (lane == 0) {
-        item = w;
-        flag = some;
-      }
+struct RowState {
+  float m, l;  // running maximum (base 2, scaled) and sum
+};
+// Scores of one key tile of the thread's row to probabilities.  from / upto:
+// the columns that the row sees are from <= column < upto.
+__device__ __forceinline__ void mask32(float (&s)[32], int col0, int from, int upto) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (col0 + i < from || col0 + i >= upto) s[i] = -INFINITY;
+}
+__device__ __forceinline__ float max32(const float (&s)[32], float m) {
+  float m1 = max3(s[0], s[1], m), m2 = max3(s[2], s[3], s[4]);
+#pragma unroll
+  for (int i = 5; i + 3 < 32; i += 4) {
+    m1 = max3(m1, s[i], s[i + 1]);
+    m2 = max3(m2, s[i + 2], s[i + 3]);
+  }
+  return max3(m1, m2, fmaxf(s[29], fmaxf(s[30], s[31])));
+}
+// p = 2^(s * scale - ms) as bf16 pairs; the sum of p joins `sum`.
+__device__ __forceinline__ void exp32(const float (&s)[32], float scale, float ms, float2& sum, uint32_t (&p)[16]) {
+  const float2 sc = make_float2(scale, scale), mm = make_float2(-ms, -ms);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), sc, mm);
+    x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
+    sum = __fadd2_rn(sum, x);
+    p[i] = bf16x2_rn(x.x, x.y);
+  }
+}
+__device__ __forceinline__ void softmax_tile(const ChunkArgs& a, uint32_t S, uint32_t O, bool masked, int from, int upto,
+                                             bool first, RowState& st) {
+  float x[32], y[32];
+  // columns 0..63 for the maximum only
+  tmem_ld32(S, x);
+  tmem_ld32(S + 32, y);
+  tmem_ld_wait();
+  if (masked) mask32(x, 0, from, upto), mask32(y, 32, from, upto);
+  float mx = max32(y, max32(x, -INFINITY));
+  // columns 64..127 stay in registers
+  tmem_ld32(S + 64, x);
+  tmem_ld32(S + 96, y);
+  tmem_ld_wait();
+  if (masked) mask32(x, 64, from, upto), mask32(y, 96, from, upto);
+  mx = max32(y, max32(x, mx)) * a.scale_log2;  // -inf * 0 is NaN, which fmaxf below drops
+  const bool grow = mx > st.m + kGrow || st.m == -INFINITY;
+  float al = 1.f;
+  if (grow) {
+    const float mn = fmaxf(st.m, mx);
+    al = mn == -INFINITY ? 1.f : exp2_fast(st.m - mn);
+    st.m = mn;
+  }
+  if (!first && __any_sync(0xFFFFFFFFu, al != 1.f)) {
+    // the outputs so far in the new unit (the scores' arrival says that their products are done)
+    float o[32];
+#pragma unroll 1
+    for (int c = 0; c < kD; c += 32) {
+      tmem_ld32(O + c, o);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] *= al;
+      tmem_st32(O + c, o);
     }
-    __syncthreads();
-    if (!flag) break;
-    const chunk::Item w = item;
-    if (w.t0 >= w.t1) continue;
-    const int R = w.n * a.G, r0 = w.j * kTileRows, nrows = min(kTileRows, R - r0);
-    // the lane's two rows and their last visible token
-    int tok[2], pos[2];
-    const uint16_t* qp[2];
-    bool mine[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 16 * warp + g + 8 * i;
-      mine[i] = r < nrows;
-      const int rr = r0 + min(r, nrows - 1);
-      tok[i] = rr / a.G;
-      pos[i] = w.len - w.n + tok[i];
-      qp[i] = a.q + static_cast<long long>(w.c0 + tok[i]) * a.ldq + (w.hk * a.G + rr % a.G) * kD;
-    }
-    uint32_t qf[8][4];
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        qf[kk][i] = __ldg(reinterpret_cast<const uint32_t*>(qp[i & 1] + 16 * kk + 8 * (i >> 1) + 2 * tq));
-    float o[16][4];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  }
+  const float ms = st.m == -INFINITY ? 0.f : st.m;
+  float2 sum = make_float2(0.f, 0.f);
+  // probabilities take the place of columns 64..127
+  uint32_t p[16];
+  exp32(x, a.scale_log2, ms, sum, p);
+  tmem_st16(S + 96, p);
+  exp32(y, a.scale_log2, ms, sum, p);
+  tmem_st16(S + 112, p);
+  tmem_ld32(S, x);
+  tmem_ld32(S + 32, y);
+  tmem_ld_wait();
+  if (masked) mask32(x, 0, from, upto), mask32(y, 32, from, upto);
+  exp32(x, a.scale_log2, ms, sum, p);
+  tmem_st16(S + 64, p);
+  exp32(y, a.scale_log2, ms, sum, p);
+  tmem_st16(S + 80, p);
+  st.l = fmaf(st.l, al, sum.x + sum.y);
+  tmem_st_wait();
+}
 
-    for (int kti = w.t0; kti < w.t1; ++kti) {
-      const int tok0 = kti * kTileKeys;
-      __syncthreads();
-      load_tile(a, w, a.kc, a.ks, tok0, kt);
-      load_tile(a, w, a.vc, a.vs, tok0, vt);
-      __syncthreads();
-      if (16 * warp >= nrows) continue;
-      float s[8][4];
+// Row `r` of the tile's parts added up by a warp: lane c of 32 takes part c for
+// the maximum and the sum, then the warp reads the outputs one part after
+// another, 4 columns a lane.
+__device__ __forceinline__ void merge_row(const ChunkArgs& a, const Item& w, const chunk::Ranges& rg, int r, int lane) {
+  float M = -INFINITY;
+  for (int c = w.first; c <= w.last; c += 32) {
+    const int slot = c + lane <= w.last ? chunk::part_slot(w, rg, c + lane) : -1;
+    float m = slot >= 0 ? __ldcg(&a.rec_ml[slot * a.slot_rows + r].x) : -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    M = fmaxf(M, m);
+  }
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.f;
+  for (int c = w.first; c <= w.last; c += 32) {
+    const int slot = c + lane <= w.last ? chunk::part_slot(w, rg, c + lane) : -1;
+    float f = 0.f, d = 0.f;
+    if (slot >= 0) {
+      const float2 ml = __ldcg(&a.rec_ml[slot * a.slot_rows + r]);
+      f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
+      d = f * ml.y;
+    }
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
+    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+    den += d;
+    const int n = min(32, w.last - c + 1);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const int sl = __shfl_sync(0xFFFFFFFFu, slot, i);
+      const float fi = __shfl_sync(0xFFFFFFFFu, f, i);
+      if (fi == 0.f) continue;
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.rec + (static_cast<size_t>(sl) * a.slot_rows + r) * kD) + lane);
+      num.x = fmaf(fi, v.x, num.x), num.y = fmaf(fi, v.y, num.y), num.z = fmaf(fi, v.z, num.z), num.w = fmaf(fi, v.w, num.w);
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const int rr = w.r0 + r, tok = rr / a.G;
+  uint16_t* y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
+  reinterpret_cast<uint2*>(y)[lane] = make_uint2(bf16x2_rn(num.x * inv, num.y * inv), bf16x2_rn(num.z * inv, num.w * inv));
+}
+
+template <int MT, int NR>
+__global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
+  using L = Layout<MT, NR>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + L::ctl);
+  const Ctx c{a, ctl};
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int qs = a.tile_rows / a.G, rs = a.tile_rows % a.G;
+  if (t == 0) {
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          uint32_t b[4];
-          ldmatrix_x4(b, kt + tile_ofs(nt * 16 + (lane >> 4) * 8 + (lane & 7), 2 * kk + ((lane >> 3) & 1)));
-          mma_bf16(s[2 * nt], qf[kk], b[0], b[1]);
-          mma_bf16(s[2 * nt + 1], qf[kk], b[2], b[3]);
-        }
-      // mask and online softmax; column of s[nt][e]: 8 nt + 2 tq + (e & 1)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int t = tok0 + 8 * nt + 2 * tq + e;
-            float& x = s[nt][2 * i + e];
-            const bool seen = t <= pos[i] && (a.window == 0 || t > pos[i] - a.window);
-            x = seen ? x * a.scale_log2 : -INFINITY;
-            mx = fmaxf(mx, x);
-          }
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-        const float mn = fmaxf(m[i], mx);
-        const float ms = mn == -INFINITY ? 0.f : mn;  // nothing seen so far
-        const float al = exp2_fast(m[i] - ms);
-        m[i] = mn;
-        float sum = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& x = s[nt][2 * i + e];
-            x = __bfloat162float(__float2bfloat16_rn(exp2_fast(x - ms)));
-            sum += x;
-          }
-        l[i] = fmaf(l[i], al, sum);
-#pragma unroll
-        for (int nd = 0; nd < 16; ++nd) {
-          o[nd][2 * i] *= al;
-          o[nd][2 * i + 1] *= al;
-        }
-      }
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint32_t p[4] = {bf16x2_rn(s[2 * kk][0], s[2 * kk][1]), bf16x2_rn(s[2 * kk][2], s[2 * kk][3]),
-                               bf16x2_rn(s[2 * kk + 1][0], s[2 * kk + 1][1]),
-                               bf16x2_rn(s[2 * kk + 1][2], s[2 * kk + 1][3])};
-#pragma unroll
-        for (int nd = 0; nd < 8; ++nd) {
-          uint32_t b[4];
-          ldmatrix_x4_trans(b, vt + tile_ofs(kk * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * nd + (lane >> 4)));
-          mma_bf16(o[2 * nd], p, b[0], b[1]);
-          mma_bf16(o[2 * nd + 1], p, b[2], b[3]);
-        }
-      }
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(&ctl->raw_full[i], 33);
+      mbar_init(&ctl->raw_empty[i], kConvWarps);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+      mbar_init(&ctl->k_full[i], kConvWarps);
+      mbar_init(&ctl->k_empty[i], 1);
+      mbar_init(&ctl->v_full[i], kConvWarps);
+      mbar_init(&ctl->v_empty[i], 1);
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->p_full[i], 4);
+      mbar_init(&ctl->o_done[i], 1);
+      mbar_init(&ctl->it_full[i], 32);
+      mbar_init(&ctl->it_empty[i], kSoftWarps + kConvWarps + 1);
     }
-    if (w.ns == 1) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (!mine[i]) continue;
-        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-        const int rr = r0 + 16 * warp + g + 8 * i;
-        uint16_t* y = a.out + static_cast<long long>(w.c0 + tok[i]) * a.ldo + (w.hk * a.G + rr % a.G) * kD + 2 * tq;
-#pragma unroll
-        for (int nd = 0; nd < 16; ++nd)
-          *reinterpret_cast<uint32_t*>(y + 8 * nd) = bf16x2_rn(o[nd][2 * i] * inv, o[nd][2 * i + 1] * inv);
-      }
-      continue;
+    mbar_init(&ctl->q_full, kSoftWarps);
+    mbar_init(&ctl->group[0], 4);
+    mbar_init(&ctl->group[1], 4);
+    mbar_init(&ctl->second, 4);
+    mbar_init(&ctl->taken, 4);
+    mbar_init(&ctl->fin, 1);
+    ctl->stop = 0u;
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&ctl->tmem, 512);
+    tmem_relinquish();
+  }
+  const long long units = chunk::all_units(a, qs, rs, ctl->red);  // a block-wide barrier inside
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  chunk::Ranges ranges;
+  ranges.make(units, a.grid);
+  // the shared memory starts on a swizzle atom (checked, as all offsets rely on it)
+  if ((smem_u32(smem) & 1023u) != 0u) {
+    if (t == 0) {
+      atomicCAS(a.status, 0u, (3u << 24) | (9u << 16));
+      ctl->stop = 1u;
     }
-    // ---- one of several splits: leave the partial result; the last split to
-    // arrive adds them up, always in the splits' order
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (!mine[i]) continue;
-      const uint32_t rec = w.rec + static_cast<uint32_t>(w.split * nrows + 16 * warp + g + 8 * i);
-      float* y = a.rec + static_cast<size_t>(rec) * kD + 2 * tq;
-#pragma unroll
-      for (int nd = 0; nd < 16; ++nd) *reinterpret_cast<float2*>(y + 8 * nd) = make_float2(o[nd][2 * i], o[nd][2 * i + 1]);
-      if (tq == 0) a.rec_ml[rec] = make_float2(m[i], l[i]);
-    }
-    __threadfence();
     __syncthreads();
-    if (tid == 0) {
-      const bool last = atomicAdd(a.groups + w.group, 1u) == static_cast<uint32_t>(w.ns) - 1u;
-      if (last) a.groups[w.group] = 0u;
-      flag = last;
-      __threadfence();
+  } else if (warp == kLoadWarp) {
+    // ---- the plan, and pages into the ring
+    chunk::Walk walk;
+    walk.init(a, ranges, blockIdx.x, qs, rs, lane);
+    Ring<2> it;
+    Ring<NR> ring;
+    for (bool some = true, ok = true; some && ok; it.step()) {
+      Item w;
+      w.t0 = w.t1 = 0;
+      some = walk.next(a, lane, w);
+      if (!some) w.t0 = w.t1 = 0;
+      if (!wait(c, &ctl->it_empty[it.slot], it.phase ^ 1u, 2u)) break;
+      if (lane == 0) ctl->item[it.slot] = w;
+      __syncwarp();
+      mbar_arrive(&ctl->it_full[it.slot]);
+      for (int k = w.t0; ok && k < w.t1; ++k) ok = load_tile<NR>(c, w, k, smem + L::raw, smem + L::sc, ring, lane);
     }
-    __syncthreads();
-    if (flag) {
-      for (int r = 0; r < nrows; ++r) {
-        float M = -INFINITY;
-        for (int sp = 0; sp < w.ns; ++sp) M = fmaxf(M, __ldcg(&a.rec_ml[w.rec + sp * nrows + r]).x);
-        float num = 0.f, den = 0.f;
-        for (int sp = 0; sp < w.ns; ++sp) {
-          const float2 ml = __ldcg(&a.rec_ml[w.rec + sp * nrows + r]);
-          if (ml.x == -INFINITY) continue;
-          const float f = exp2_fast(ml.x - M);
-          num = fmaf(f, __ldcg(a.rec + static_cast<size_t>(w.rec + sp * nrows + r) * kD + tid), num);
-          den = fmaf(f, ml.y, den);
+    // copies in flight land before the block ends
+    if (ctl->stop != 0u) {
+      for (int i = 0; i < NR; ++i) {
+        const uint64_t t0 = globaltimer_ns();
+        const uint32_t parity = (ring.phase ^ (i >= ring.slot ? 1u : 0u)) ^ 0u;
+        while (!mbar_try_wait(&ctl->raw_full[i], parity) && globaltimer_ns() - t0 < 20000000ull) {
         }
-        const int rr = r0 + r;
-        const __nv_bfloat16 y = __float2bfloat16_rn(den > 0.f ? num / den : 0.f);
-        a.out[static_cast<long long>(w.c0 + rr / a.G) * a.ldo + (w.hk * a.G + rr % a.G) * kD + tid] =
-            *reinterpret_cast<const uint16_t*>(&y);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      // ---- products
+      const uint32_t qa = smem_u32(smem + L::q), ka = smem_u32(smem + L::k), va = smem_u32(smem + L::v);
+      Ring<2> it;
+      Ring<kSlots> kr, vr;
+      uint32_t q_phase = 0, p_phase[2] = {0, 0};
+      bool issued = false;
+      for (;; it.step()) {
+        if (!wait_one(c, &ctl->it_full[it.slot], it.phase, 4u)) break;
+        const int tiles = ctl->item[it.slot].t1 - ctl->item[it.slot].t0;
+        const bool pair = ctl->item[it.slot].rows > 128;
+        mbar_arrive(&ctl->it_empty[it.slot]);
+        if (tiles == 0) break;
+        issued = true;
+        if (!wait_one(c, &ctl->q_full, q_phase, 5u)) break;
+        q_phase ^= 1u;
+        tc_fence_after();
+        const int steps = pair ? 2 * tiles : tiles;
+        // step i: stream i % 2; with a pair two steps share a key tile
+        auto scores = [&](int i) -> bool {
+          const int m = i & 1;
+          if (!pair || m == 0)
+            if (!wait_one(c, &ctl->k_full[kr.slot], kr.phase, 6u)) return false;
+          tc_fence_after();
+          const uint32_t qb = qa + (pair && m ? kOperand : 0u), kb = ka + kr.slot * kOperand;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t o = (k >> 2) * kHalf + (k & 3) * 32;
+            mma_ss(tmem + m * 128, smem_desc(qb + o, 16, 1024, kSwizzle128B), smem_desc(kb + o, 16, 1024, kSwizzle128B),
+                   kIdesc, k > 0);
+          }
+          tc_commit(&ctl->s_full[m]);
+          if (!pair || m == 1) {
+            tc_commit(&ctl->k_empty[kr.slot]);
+            kr.step();
+          }
+          return true;
+        };
+        bool ok = scores(0);
+        if (ok && steps > 1) ok = scores(1);
+        for (int i = 0; ok && i < steps; ++i) {
+          const int m = i & 1;
+          if (!pair || m == 0) ok = wait_one(c, &ctl->v_full[vr.slot], vr.phase, 7u);
+          ok = ok && wait_one(c, &ctl->p_full[m], p_phase[m], 8u);
+          if (!ok) break;
+          p_phase[m] ^= 1u;
+          tc_fence_after();
+          const uint32_t vb = va + vr.slot * kOperand;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ts(tmem + 256 + m * 128, tmem + m * 128 + 64 + 8 * k, smem_desc(vb + k * 2048, kHalf, 1024, kSwizzle128B),
+                   kIdescBt, (i >= 2 || k > 0) ? 1u : 0u);
+          if (!pair || m == 1) {
+            tc_commit(&ctl->v_empty[vr.slot]);
+            vr.step();
+          }
+          if (i + 2 >= steps) tc_commit(&ctl->o_done[m]);
+          if (i + 2 < steps) ok = scores(i + 2);
+        }
+        if (!ok) break;
+      }
+      if (issued && ctl->stop != 0u) {  // products in flight end before tensor memory is given back
+        tc_commit(&ctl->fin);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&ctl->fin, 0) && globaltimer_ns() - t0 < 20000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kSoftWarps && warp < kMmaWarp) {
+    // ---- codes to bf16
+    const int ct = t - 32 * kSoftWarps;
+    Ring<2> it;
+    Ring<NR> ring;
+    Ring<kSlots> kv;
+    for (bool ok = true; ok; it.step()) {
+      if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) break;
+      const int t0 = ctl->item[it.slot].t0, t1 = ctl->item[it.slot].t1, lo = ctl->item[it.slot].lo,
+                hi = ctl->item[it.slot].hi;
+      warp_arrive(&ctl->it_empty[it.slot], lane);
+      if (t0 == t1) break;
+      for (int k = t0; ok && k < t1; ++k) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          uint64_t* full = v ? ctl->v_full : ctl->k_full;
+          uint64_t* empty = v ? ctl->v_empty : ctl->k_empty;
+          ok = ok && wait(c, &ctl->raw_full[ring.slot], ring.phase, 3u) &&
+               wait(c, &empty[kv.slot], kv.phase ^ 1u, 6u);
+          if (!ok) break;
+          convert_tile(smem + L::raw + ring.slot * kCodes, smem + L::sc + ring.slot * kScales,
+                       smem + (v ? L::v : L::k) + kv.slot * kOperand, k * kKeys, lo, hi, ct);
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full[kv.slot]);
+            mbar_arrive(&ctl->raw_empty[ring.slot]);
+          }
+          ring.step();
+        }
+        kv.step();
+      }
+    }
+  } else if (warp < kSoftWarps) {
+    // ---- softmax: stream m, a thread a row
+    const int m = warp >> 2, wl = warp & 3, row = t & 127;
+    const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
+    const uint32_t S = tmem + lanes + m * 128, O = tmem + lanes + 256 + m * 128;
+    Ring<2> it;
+    uint32_t s_phase = 0, o_phase = 0, g_phase = 0, x_phase = 0;
+    for (bool ok = true; ok; it.step()) {
+      if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) break;
+      const Item w = ctl->item[it.slot];
+      warp_arrive(&ctl->it_empty[it.slot], lane);
+      if (w.t0 == w.t1) break;
+      const bool pair = w.rows > 128;
+      const int tr = (pair ? 128 * m : 0) + row;  // row in the tile
+      if (pair)
+        load_queries(a, w, w.r0 + 128 * m, smem + L::q + m * kOperand, 0, 128, wl, lane);
+      else
+        load_queries(a, w, w.r0, smem + L::q, 64 * m, 64, wl, lane);
+      fence_proxy_async_shared();
+      warp_arrive(&ctl->q_full, lane);
+      const int rr = w.r0 + min(tr, w.rows - 1), tok = rr / a.G;
+      const int pos = w.len - w.n + tok;
+      const bool busy = (pair ? 128 * m : 0) + 32 * wl < w.rows;  // the warp has a row
+      // the warp's rows see all of a tile between these tokens
+      const int see_lo = a.window > 0 ? __reduce_max_sync(0xFFFFFFFFu, pos) - a.window + 1 : 0;
+      const int see_hi = __reduce_min_sync(0xFFFFFFFFu, pos) + 1;
+      const int mine = a.window > 0 ? pos - a.window + 1 : 0;
+      RowState st{-INFINITY, 0.f};
+      const int step = pair ? 1 : 2;
+      int k = w.t0 + (pair ? 0 : m);
+      const bool any = k < w.t1;
+      for (bool first = true; k < w.t1; k += step, first = false) {
+        ok = wait(c, &ctl->s_full[m], s_phase, 10u);
+        if (!ok) break;
+        s_phase ^= 1u;
+        tc_fence_after();
+        const int tok0 = k * kKeys;
+        if (busy) {
+          if (tok0 >= see_lo && tok0 + kKeys <= see_hi)
+            softmax_tile(a, S, O, false, 0, kKeys, first, st);
+          else
+            softmax_tile(a, S, O, true, mine - tok0, pos + 1 - tok0, first, st);
+        }
+        tc_fence_before();
+        warp_arrive(&ctl->p_full[m], lane);
+      }
+      if (!ok) break;
+      if (any) {
+        ok = wait(c, &ctl->o_done[m], o_phase, 11u);
+        if (!ok) break;
+        o_phase ^= 1u;
+        tc_fence_after();
+      }
+      float f0 = 1.f, f1 = 0.f;  // the streams' shares of the row's output
+      if (!pair) {
+        // the second stream's sums through tensor memory to the first, which adds both up
+        if (m == 1) {
+          tmem_st2(S, st.m, any ? st.l : 0.f);
+          tmem_st_wait();
+          tc_fence_before();
+          warp_arrive(&ctl->second, lane);
+        } else {
+          ok = wait(c, &ctl->second, x_phase, 12u);
+          if (!ok) break;
+          tc_fence_after();
+          float m1, l1;
+          tmem_ld2(S + 128, m1, l1);
+          tmem_ld_wait();
+          const float M = fmaxf(st.m, m1);
+          f0 = st.m == -INFINITY ? 0.f : exp2_fast(st.m - M);
+          f1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - M);
+          st.l = f0 * st.l + f1 * l1;
+          st.m = M;
+        }
+      }
+      if (pair || m == 0) {
+        const bool two = !pair && w.t1 - w.t0 > 1;
+        const bool write = tr < w.rows;
+        const int slot = w.whole ? 0 : chunk::part_slot(w, ranges, blockIdx.x);
+        if (w.whole) {
+          const float inv = st.l > 0.f ? 1.f / st.l : 0.f;
+          f0 *= inv, f1 *= inv;
+        }
+        uint16_t* y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
+        const size_t rec = static_cast<size_t>(slot) * a.slot_rows + min(tr, w.rows - 1);
+        if (busy) {
+#pragma unroll 1
+          for (int col = 0; col < kD; col += 32) {
+            float o[32];
+            tmem_ld32(O + col, o);
+            tmem_ld_wait();
+            if (two) {
+              float o1[32];
+              tmem_ld32(O + 128 + col, o1);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = (f0 != 0.f ? f0 * o[i] : 0.f) + (f1 != 0.f ? f1 * o1[i] : 0.f);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = f0 != 0.f ? f0 * o[i] : 0.f;
+            }
+            if (write) {
+              if (w.whole) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8)
+                  *reinterpret_cast<uint4*>(y + col + i) =
+                      make_uint4(bf16x2_rn(o[i], o[i + 2]), bf16x2_rn(o[i + 1], o[i + 3]),
+                                 bf16x2_rn(o[i + 4], o[i + 6]), bf16x2_rn(o[i + 5], o[i + 7]));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                  *reinterpret_cast<float4*>(a.rec + rec * kD + col + i) = make_float4(o[i], o[i + 2], o[i + 1], o[i + 3]);
+              }
+            }
+          }
+          if (!w.whole && write) a.rec_ml[rec] = make_float2(st.m, st.l);
+        }
+        tc_fence_before();
+        if (!w.whole) {
+          // the last part to arrive adds them up, in the blocks' order
+          __threadfence();
+          warp_arrive(&ctl->group[m], lane);
+          ok = wait(c, &ctl->group[m], g_phase, 13u);
+          if (!ok) break;
+          g_phase ^= 1u;
+          if (row == 0) {
+            uint32_t* count = a.count + 2 * w.first + m;
+            const bool last = atomicAdd(count, 1u) == static_cast<uint32_t>(w.parts) - 1u;
+            if (last) *count = 0u;
+            ctl->last[m] = last;
+            __threadfence();
+          }
+          warp_arrive(&ctl->group[m], lane);
+          ok = wait(c, &ctl->group[m], g_phase, 13u);
+          if (!ok) break;
+          g_phase ^= 1u;
+          if (ctl->last[m]) {
+            const int base = pair ? 128 * m : 0, rows = min(128, w.rows - base);
+            for (int r = wl; r < rows; r += 4) merge_row(a, w, ranges, base + r, lane);
+          }
+        }
+      }
+      if (!pair) {  // the second stream goes on when its tiles have been read
+        if (m == 0) {
+          warp_arrive(&ctl->taken, lane);
+        } else {
+          ok = wait(c, &ctl->taken, x_phase, 14u);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        x_phase ^= 1u;
       }
     }
   }
-  if (tid == 0) chunk::leave(a);
+  // ---- the end: every role is here, and nothing is in flight
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
 
-uint32_t chunk_rec_rows(int T, int Hq, int sms) {
-  // few rows: every row in up to two splits for each block of the GPU; many
-  // rows: as many splits as 64 K rows of partial results hold (34 MB)
-  const long long most = static_cast<long long>(T) * Hq * 2 * sms;
-  return static_cast<uint32_t>(most < 65536 ? most : 65536);
+int chunk_tile_rows(int T, int B, int G) {
+  return static_cast<long long>(T) * G > 128LL * B ? 256 : 128;
 }
 
-cudaError_t launch_chunk(const ChunkArgs& args, int sms, cudaStream_t stream) {
-  ChunkArgs a = args;
-  a.grid = 2 * sms;
-  chunk_kernel<<<a.grid, kChunkThreads, 0, stream>>>(a);
+namespace {
+template <int MT, int NR>
+cudaError_t launch_as(const ChunkArgs& a, cudaStream_t stream) {
+  const int bytes = static_cast<int>(Layout<MT, NR>::bytes);
+  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<MT, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  chunk_kernel<MT, NR><<<a.grid, kBlock, bytes, stream>>>(a);
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream) {
+  return a.tile_rows == 256 ? launch_as<2, 2>(a, stream) : launch_as<1, 3>(a, stream);
 }
 
 }  // namespace fsops

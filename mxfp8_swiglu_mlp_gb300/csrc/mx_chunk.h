@@ -10,7 +10,7 @@ namespace fsops {
 constexpr int kChunkD = 128;            // head dimension
 constexpr int kChunkMaxGroup = 64;      // query heads per KV head
 constexpr size_t kChunkHeaderBytes = 256;
-constexpr uint32_t kChunkMaxGroups = 16384;  // (sequence, query tile, KV head) triples that may be split
+constexpr size_t kChunkCounterBytes = 4096;  // two counters a block, blocks <= 256
 
 struct ChunkArgs {
   const uint16_t* q;          // row t, head h at t * ldq + h * 128
@@ -21,20 +21,26 @@ struct ChunkArgs {
   const int32_t* cu;          // [B + 1]
   const int32_t* lens;        // [B]
   uint32_t* status;           // first error (status << 24 | site << 16 | sequence)
-  uint32_t* work;             // items handed out (zero between calls)
-  uint32_t* done;             // blocks that have left (zero between calls)
-  uint32_t* groups;           // [kChunkMaxGroups] splits finished (zero between calls)
-  float* rec;                 // [rec_rows][128] unnormalised outputs of split rows
-  float2* rec_ml;             // [rec_rows] running maximum (base 2) and sum
-  uint32_t rec_rows;
+  uint32_t* count;            // [2 * grid] parts of a query tile that have arrived (zero between calls)
+  float* rec;                 // [2 * grid][slot_rows][128] unnormalised outputs of parts
+  float2* rec_ml;             // [2 * grid][slot_rows] running maximum (base 2) and sum
+  int slot_rows;
   int T, B, Hq, Hkv, G, log2P, num_pages, max_pages, window;
-  float scale_log2;           // sm_scale * log2(e)
+  float scale_log2;           // |sm_scale| * log2(e)
+  int negate;                 // sm_scale < 0: q enters with its sign turned
+  int tile_rows;              // rows of a query tile: 128 or 256
   int grid;
   uint64_t timeout_ns;
 };
 
-// Rows of partial results a call may need (a row is one query token and head).
-uint32_t chunk_rec_rows(int T, int Hq, int sms);
-cudaError_t launch_chunk(const ChunkArgs& a, int sms, cudaStream_t stream);
+// Rows of a query tile for T rows of B sequences in groups of G heads.
+int chunk_tile_rows(int T, int B, int G);
+// Partial-result slots of a call and their rows.
+inline int chunk_slots(int sms) { return 2 * sms; }
+inline int chunk_slot_rows(int T, int G, int tile_rows) {
+  const long long r = static_cast<long long>(T) * G;
+  return r < tile_rows ? static_cast<int>(r) : tile_rows;
+}
+cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream);
 
 }  // namespace fsops

@@ -1,15 +1,16 @@
-// mx_chunk_plan.cuh -- how the chunk attention's work is cut and handed out.
+// mx_chunk_plan.cuh -- how the chunk attention's work is cut and shared out.
 // The lengths are device data, so every block derives the same plan from them.
 //
 // A sequence's new tokens times the G query heads of a KV head are its rows
-// (row r: token r / G, head r % G); `rows` consecutive ones make a query
-// tile, which sees the key tiles [lo, hi) of `kt` tokens that its mask
-// reaches.  An item is (sequence, query tile, split, KV head), a split being S
-// key tiles of the query tile.  S is one for the whole call: about half of a
-// block's even share of the work, so that few rows over a long cache spread
-// over the GPU and many rows are not split at all, doubled until the partial
-// results fit the workspace.  Items are handed out by a counter, the query
-// tiles of a sequence from its end, where a causal mask leaves most keys.
+// (row r: token r / G, head r % G); tile_rows consecutive ones make a query
+// tile, which sees the key tiles of 128 tokens that its mask reaches.  All
+// query tiles in a row (sequence, KV head, query tile), each worth
+//   kTileCost + its key tiles * (kPairCost above 128 rows, else kHalfCost)
+// units, are cut into `blocks` equal ranges of units, one a block.  A block so
+// does the end of one query tile, some whole ones and the beginning of
+// another: the work is even whatever the lengths are, a long cache with few
+// rows spreads over the whole GPU, and a block leaves at most two partial
+// results, however many rows there are.
 #pragma once
 #include "mx_chunk.h"
 #include "mx_device.cuh"
@@ -17,170 +18,222 @@
 namespace fsops {
 namespace chunk {
 
+constexpr int kKeys = 128;     // tokens of a key tile
+constexpr int kTileCost = 10;  // what a query tile costs besides its keys (queries in, outputs out)
+constexpr int kPairCost = 8;   // a key tile against two halves of 128 rows
+constexpr int kHalfCost = 5;   // a key tile against one
+constexpr int kLeastUnits = 10;  // of a block: what a part costs to merge is worth about two key tiles
+
 struct Seq {
-  int n, len;   // new tokens, length with them (n = 0: nothing to do or not valid)
-  int nq;       // query tiles
-  int tiles;    // key tiles of a query tile at most
+  int n, len;  // new tokens, length with them (n = 0: nothing to do or not valid)
   bool bad;
 };
-__device__ __forceinline__ Seq load_seq(const ChunkArgs& a, int b, int rows, int kt) {
+__device__ __forceinline__ Seq load_seq(const ChunkArgs& a, int b) {
   Seq s;
   const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
   s.len = __ldg(a.lens + b);
   s.n = c1 - c0;
   s.bad = c0 < 0 || c1 < c0 || c1 > a.T ||
           (s.n > 0 && (s.len < s.n || static_cast<long long>(s.len) > (static_cast<long long>(a.max_pages) << a.log2P)));
-  if (s.bad || s.n <= 0) {
-    s.n = s.nq = s.tiles = 0;
-    return s;
-  }
-  s.nq = (s.n * a.G + rows - 1) / rows;
-  s.tiles = (s.len + kt - 1) / kt;
-  if (a.window > 0) {
-    const int span = min(a.window, s.len) + min(s.n, rows / a.G + 2);  // tokens a query tile can reach
-    s.tiles = min(s.tiles, (span + kt - 1) / kt + 1);
-  }
+  if (s.bad) s.n = 0;
   return s;
 }
 
-// One item.
-struct Item {
-  int b, j, split, hk;   // sequence, query tile, split, KV head
-  int n, len, c0;        // new tokens, length, first row of the sequence
-  int t0, t1;            // key tiles [t0, t1) of this split
-  int ns;                // splits of the query tile that have keys
-  int lo, hi;            // tokens some row of the tile sees
-  uint32_t rec, group;   // first partial-result row and counter of the tile (ns > 1)
+// A sequence's query tiles one after another, without divisions.
+struct Tiles {
+  int j, R;            // tile, rows of the sequence
+  int f, fr;           // first row = f * G + fr
+  int qs, rs;          // tile_rows / G and the rest
+  int base;            // len - n: token of row 0
+  int n;
+  __device__ __forceinline__ void start(const ChunkArgs& a, const Seq& s, int qs_, int rs_) {
+    j = f = fr = 0;
+    qs = qs_, rs = rs_;
+    R = s.n * a.G;
+    n = s.n;
+    base = s.len - s.n;
+  }
+  __device__ __forceinline__ bool more(const ChunkArgs& a) const { return j * a.tile_rows < R; }
+  // tokens [lo, hi) seen, key tiles from tb, nt of them, rows of the tile
+  __device__ __forceinline__ void get(const ChunkArgs& a, int& lo, int& hi, int& tb, int& nt, int& rows) const {
+    int nf = f + qs, nr = fr + rs;
+    if (nr >= a.G) nr -= a.G, ++nf;
+    const int last = min(n - 1, nr == 0 ? nf - 1 : nf);
+    rows = min(a.tile_rows, R - j * a.tile_rows);
+    hi = base + last + 1;
+    lo = a.window > 0 ? max(0, base + f - a.window + 1) : 0;
+    tb = lo / kKeys;
+    nt = (hi + kKeys - 1) / kKeys - tb;
+  }
+  __device__ __forceinline__ void next(const ChunkArgs& a) {
+    f += qs, fr += rs;
+    if (fr >= a.G) fr -= a.G, ++f;
+    ++j;
+  }
+};
+__device__ __forceinline__ int key_cost(int rows) { return rows > 128 ? kPairCost : kHalfCost; }
+// Units of one KV head of a sequence.
+__device__ __forceinline__ long long seq_units(const ChunkArgs& a, const Seq& s, int qs, int rs) {
+  long long u = 0;
+  Tiles t;
+  for (t.start(a, s, qs, rs); t.more(a); t.next(a)) {
+    int lo, hi, tb, nt, rows;
+    t.get(a, lo, hi, tb, nt, rows);
+    u += kTileCost + static_cast<long long>(nt) * key_cost(rows);
+  }
+  return u;
+}
+// Key tiles of a query tile (nt of them, cost w each) that lie before unit y of it.
+__device__ __forceinline__ int tiles_before(long long y, int nt, int w) {
+  if (y <= kTileCost) return 0;
+  const long long t = (y - kTileCost + w - 1) / w;
+  return t < nt ? static_cast<int>(t) : nt;
+}
+
+// The ranges of the blocks: block c has units [start(c), start(c + 1)).
+struct Ranges {
+  long long each;
+  int more, blocks;  // the first `more` blocks have one unit more
+  __device__ __forceinline__ void make(long long units, int grid) {
+    long long b = units / kLeastUnits;
+    blocks = b < 1 ? 1 : b < grid ? static_cast<int>(b) : grid;
+    each = units / blocks;
+    more = static_cast<int>(units - each * blocks);
+  }
+  __device__ __forceinline__ long long start(int c) const { return each * c + min(c, more); }
+  __device__ __forceinline__ int block_of(long long x) const {
+    const long long cut = (each + 1) * more;
+    return x < cut ? static_cast<int>(x / (each + 1)) : more + static_cast<int>((x - cut) / each);
+  }
 };
 
-// Block-wide: the tiles of a split.  `red` holds one value a warp.
-__device__ inline int split_tiles(const ChunkArgs& a, int rows, int kt, int smin, unsigned long long* red) {
-  const int nt = blockDim.x, t = threadIdx.x;
-  auto total = [&](unsigned long long v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    __syncthreads();
-    if ((t & 31) == 0) red[t >> 5] = v;
-    __syncthreads();
-    unsigned long long s = 0;
-    for (int w = 0; w < nt / 32; ++w) s += red[w];
-    return s;
-  };
-  unsigned long long cost = 0;
-  for (int b = t; b < a.B; b += nt) {
-    const Seq s = load_seq(a, b, rows, kt);
-    // a causal chunk's query tiles see half of the chunk's own keys on average
-    const int avg = a.window > 0 ? s.tiles : max(1, s.tiles - s.n / (2 * kt));
-    cost += static_cast<unsigned long long>(s.nq) * avg;
+// One block's part of a query tile.
+struct Item {
+  int b, hk, n, len, c0;  // sequence, KV head, new tokens, length, first row of the sequence in q and out
+  int r0, rows;           // first row of the tile, its rows
+  int lo, hi;             // tokens some row of the tile sees
+  int t0, t1;             // key tiles of this part (t0 == t1: no more work)
+  int whole;              // the part is the whole tile
+  int tb, nt;             // key tiles of the tile
+  int first, last;        // blocks that have a share of the tile
+  int parts;              // how many of them have a key tile
+  long long x;            // unit at which the tile begins
+};
+// Block c's part of the tile: its slot, or -1 when it has no key tile.
+__device__ __forceinline__ int part_slot(const Item& w, const Ranges& r, int c) {
+  const long long s = r.start(c), e = r.start(c + 1);
+  const int kc = key_cost(w.rows);
+  if (tiles_before(e - w.x, w.nt, kc) <= tiles_before(s - w.x, w.nt, kc)) return -1;
+  return 2 * c + (s >= w.x ? 0 : 1);  // the tile that a block begins with, else the one it ends with
+}
+
+// Block-wide: all units; reports sequences that are not valid.
+__device__ inline long long all_units(const ChunkArgs& a, int qs, int rs, long long* red) {
+  const int t = threadIdx.x;
+  long long u = 0;
+  for (int b = t; b < a.B; b += blockDim.x) {
+    const Seq s = load_seq(a, b);
+    u += seq_units(a, s, qs, rs);
     if (s.bad) atomicCAS(a.status, 0u, (1u << 24) | (1u << 16) | (static_cast<uint32_t>(b) & 0xFFFFu));
   }
-  cost = total(cost) * a.Hkv;
-  long long S = static_cast<long long>((cost + 2ull * a.grid - 1) / (2ull * a.grid));
-  if (S < smin) S = smin;
-  for (;;) {
-    // rows of partial results in the low 40 bits' place, counters above
-    unsigned long long need = 0, groups = 0;
-    for (int b = t; b < a.B; b += nt) {
-      const Seq s = load_seq(a, b, rows, kt);
-      const long long ns = (s.tiles + S - 1) / S;
-      if (ns > 1) {
-        need += static_cast<unsigned long long>(ns) * s.n * a.Hq;
-        groups += static_cast<unsigned long long>(s.nq) * a.Hkv;
-      }
-    }
-    need = total(need);
-    groups = total(groups);
-    if (need <= a.rec_rows && groups <= kChunkMaxGroups) break;
-    S *= 2;
-  }
-  return static_cast<int>(S > (1 << 28) ? (1 << 28) : S);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+  if ((t & 31) == 0) red[t >> 5] = u;
+  __syncthreads();
+  long long s = 0;
+  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) s += red[w];
+  return s * a.Hkv;
 }
 
-// A warp's way through the items, which it meets in increasing order: the
-// sequences [base, base + 32), one a lane, with the sums of what lies before.
-struct Cursor {
-  int S, rows, kt;
-  int base;
-  long long items0;           // items of the sequences before `base`
-  uint32_t rec0, group0;
-  Seq s;                      // the lane's sequence
-  long long incl;             // items up to and with the lane's sequence, from base
-  uint32_t rincl, gincl;
+// A warp's way through its block's range.
+struct Walk {
+  Ranges r;
+  int qs, rs;
+  long long x, end;      // where it is, where the range ends
+  long long head;        // unit at which the current KV head began (the tile's units follow)
+  long long at;          // unit at which the current query tile begins
+  int b, hk, c0;
+  Seq s;
+  Tiles t;
 
-  __device__ __forceinline__ void load(const ChunkArgs& a, int lane) {
-    const int b = base + lane;
-    s.n = s.nq = s.tiles = s.len = 0;
-    if (b < a.B) s = load_seq(a, b, rows, kt);
-    const int ns = (s.tiles + S - 1) / S;
-    incl = static_cast<long long>(s.nq) * ns * a.Hkv;
-    rincl = ns > 1 ? static_cast<uint32_t>(ns) * s.n * a.Hq : 0u;
-    gincl = ns > 1 ? static_cast<uint32_t>(s.nq) * a.Hkv : 0u;
+  __device__ inline void init(const ChunkArgs& a, const Ranges& rr, int block, int qs_, int rs_, int lane) {
+    r = rr, qs = qs_, rs = rs_;
+    b = a.B;
+    x = end = 0;
+    if (block >= r.blocks) return;
+    x = r.start(block), end = r.start(block + 1);
+    if (x >= end) return;
+    // the sequence that holds x: 32 at a time
+    long long before = 0;
+    for (int base = 0; base < a.B; base += 32) {
+      Seq ls;
+      ls.n = ls.len = 0;
+      if (base + lane < a.B) ls = load_seq(a, base + lane);
+      const long long mine = seq_units(a, ls, qs, rs);
+      long long incl = mine * a.Hkv;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      const uint32_t r = __shfl_up_sync(0xFFFFFFFFu, rincl, o), g = __shfl_up_sync(0xFFFFFFFFu, gincl, o);
-      if (lane >= o) incl += v, rincl += r, gincl += g;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned past = __ballot_sync(0xFFFFFFFFu, before + incl > x);
+      if (past != 0) {
+        const int k = __ffs(static_cast<int>(past)) - 1;
+        b = base + k;
+        s.n = __shfl_sync(0xFFFFFFFFu, ls.n, k);
+        s.len = __shfl_sync(0xFFFFFFFFu, ls.len, k);
+        const long long u = __shfl_sync(0xFFFFFFFFu, mine, k);
+        head = before + __shfl_sync(0xFFFFFFFFu, incl, k) - u * a.Hkv;
+        hk = static_cast<int>((x - head) / u);
+        head += hk * u;
+        c0 = __ldg(a.cu + b);
+        t.start(a, s, qs, rs);
+        at = head;
+        return;
+      }
+      before += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
   }
-  __device__ __forceinline__ void init(const ChunkArgs& a, int S_, int rows_, int kt_, int lane) {
-    S = S_, rows = rows_, kt = kt_;
-    base = 0, items0 = 0, rec0 = 0, group0 = 0;
-    load(a, lane);
-  }
-  // Item number `it` (not below an earlier one); false: none left.  Empty
-  // splits give t0 == t1.
-  __device__ __forceinline__ bool find(const ChunkArgs& a, long long it, int lane, Item& w) {
-    for (;;) {
-      const long long all = __shfl_sync(0xFFFFFFFFu, incl, 31);
-      if (it < items0 + all) break;
-      if (base + 32 >= a.B) return false;
-      items0 += all;
-      rec0 += __shfl_sync(0xFFFFFFFFu, rincl, 31);
-      group0 += __shfl_sync(0xFFFFFFFFu, gincl, 31);
-      base += 32;
-      load(a, lane);
+  // The next part with key tiles; false: the range is done.
+  __device__ inline bool next(const ChunkArgs& a, int lane, Item& w) {
+    while (x < end && b < a.B) {
+      if (!t.more(a)) {  // the next KV head or sequence
+        if (++hk == a.Hkv || s.n == 0) {
+          hk = 0;
+          if (++b >= a.B) return false;
+          s = load_seq(a, b);
+          c0 = __ldg(a.cu + b);
+        }
+        t.start(a, s, qs, rs);
+        continue;
+      }
+      t.get(a, w.lo, w.hi, w.tb, w.nt, w.rows);
+      const int kc = key_cost(w.rows), j = t.j;
+      const long long stop = at + kTileCost + static_cast<long long>(w.nt) * kc;
+      t.next(a);
+      w.x = at;
+      at = stop;
+      if (stop <= x) continue;  // before the range
+      const long long to = min(stop, end);
+      const int p0 = tiles_before(x - w.x, w.nt, kc), p1 = tiles_before(to - w.x, w.nt, kc);
+      x = to;
+      if (p0 == p1) continue;
+      w.b = b, w.hk = hk, w.n = s.n, w.len = s.len, w.c0 = c0;
+      w.r0 = j * a.tile_rows;
+      w.t0 = w.tb + p0, w.t1 = w.tb + p1;
+      w.whole = p0 == 0 && p1 == w.nt;
+      w.parts = 1;
+      if (!w.whole) {
+        w.first = r.block_of(w.x), w.last = r.block_of(stop - 1);
+        w.parts = 0;
+        for (int c = w.first; c <= w.last; c += 32)
+          w.parts += __popc(__ballot_sync(0xFFFFFFFFu, c + lane <= w.last && part_slot(w, r, c + lane) >= 0));
+      }
+      return true;
     }
-    const unsigned after = __ballot_sync(0xFFFFFFFFu, it < items0 + incl);
-    const int k = __ffs(static_cast<int>(after)) - 1;
-    const int before = max(k - 1, 0);
-    const long long ib = __shfl_sync(0xFFFFFFFFu, incl, before);
-    const uint32_t rb = __shfl_sync(0xFFFFFFFFu, rincl, before), gb = __shfl_sync(0xFFFFFFFFu, gincl, before);
-    w.b = base + k;
-    w.n = __shfl_sync(0xFFFFFFFFu, s.n, k);
-    w.len = __shfl_sync(0xFFFFFFFFu, s.len, k);
-    const int nq = __shfl_sync(0xFFFFFFFFu, s.nq, k), tiles = __shfl_sync(0xFFFFFFFFu, s.tiles, k);
-    const int nsb = (tiles + S - 1) / S;
-    int i = static_cast<int>(it - items0 - (k ? ib : 0));
-    w.hk = i % a.Hkv;
-    i /= a.Hkv;
-    w.split = i % nsb;
-    w.j = nq - 1 - i / nsb;
-    w.c0 = __ldg(a.cu + w.b);
-    // the tokens that the tile's rows see
-    const int R = w.n * a.G, first = w.j * rows / a.G, last = (min(R, (w.j + 1) * rows) - 1) / a.G;
-    const int p0 = w.len - w.n + first;
-    w.hi = w.len - w.n + last + 1;
-    w.lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-    const int tb = w.lo / kt, te = (w.hi + kt - 1) / kt;
-    w.ns = (te - tb + S - 1) / S;
-    w.t0 = min(te, tb + w.split * S);
-    w.t1 = min(te, w.t0 + S);
-    // a sequence's partial results: [query tile][KV head][split][rows of the tile]
-    const int tr = min(rows, R - w.j * rows);
-    w.rec = rec0 + (k ? rb : 0u) +
-            (static_cast<uint32_t>(w.j) * rows * a.Hkv + static_cast<uint32_t>(w.hk) * tr) * static_cast<uint32_t>(nsb);
-    w.group = group0 + (k ? gb : 0u) + static_cast<uint32_t>(w.j) * a.Hkv + w.hk;
-    return true;
+    return false;
   }
 };
-
-// A block leaves: the last one hands the counters back at zero.
-__device__ __forceinline__ void leave(const ChunkArgs& a) {
-  if (atomicAdd(a.done, 1u) == static_cast<uint32_t>(a.grid) - 1u) {
-    *a.work = 0u;
-    *a.done = 0u;
-  }
-}
 
 }  // namespace chunk
 }  // namespace fsops
