@@ -40,9 +40,12 @@ using chunk::Item;
 using chunk::kKeys;
 
 constexpr int kD = kChunkD;
-constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kSoftWarps = 8, kConvWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kBlock = 32 * (kLoadWarp + 3);          // warps come in groups of four
+constexpr int kBlock = 32 * (kMmaWarp + 4);            // warps come in groups of four
+// Registers: every thread starts with 96 (20 warps); the groups share them as
+// they need, 2 x 152 + 2 x 64 + 48 = 5 x 96.
+constexpr int kSoftRegs = 152, kConvRegs = 64, kRestRegs = 48;
 constexpr uint32_t kCodes = kKeys * kD;               // bytes of a raw K or V tile
 constexpr uint32_t kScales = kKeys * kD / 32;
 constexpr uint32_t kOperand = kKeys * kD * 2;         // a bf16 tile: two halves of 64 dimensions,
@@ -144,6 +147,20 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// One lane of the warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+template <int n>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n));
+}
+template <int n>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -155,7 +172,7 @@ struct Ctx {
   Ctl* ctl;
 };
 // Bounded wait; false: the block gives up (the first reason is reported).
-__device__ __noinline__ bool wait_slow(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t site) {
+__device__ __forceinline__ bool wait_slow(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t site) {
   const uint64_t t0 = globaltimer_ns();
   volatile uint32_t* stop = &c.ctl->stop;
   while (!mbar_try_wait(bar, parity)) {
@@ -250,27 +267,33 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, const uint8_t* 
   const int cpiece = t & 7, r0 = t >> 3;
   const bool inside = tok0 >= lo && tok0 + kKeys <= hi;
   uint8_t* half = out + (cpiece >> 2) * kHalf;
-  constexpr int kStep = 32 * kConvWarps / 8;  // rows of a pass
-#pragma unroll 4
-  for (int i = 0; i < kKeys / kStep; ++i) {
+  constexpr int kStep = 32 * kConvWarps / 8, kPasses = kKeys / kStep;  // rows of a pass
+  uint4 x[kPasses];
+  uint32_t s[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
     const int r = r0 + i * kStep;
-    const uint4 x = *reinterpret_cast<const uint4*>(raw + r * kD + 16 * cpiece);
-    const uint32_t s = sc[4 * r + (cpiece >> 1)];
+    x[i] = *reinterpret_cast<const uint4*>(raw + r * kD + 16 * cpiece);
+    s[i] = sc[4 * r + (cpiece >> 1)];
+  }
+  // pieces 2 c and 2 c + 1 of the half's row; the lanes of the second half
+  // write theirs in the other order, so that eight lanes meet all banks
+  const int odd = cpiece >> 2, first = ((2 * (cpiece & 3) + odd) ^ (r0 & 7)) << 4, second = first ^ 16;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = r0 + i * kStep;
     const bool on = inside || (tok0 + r >= lo && tok0 + r < hi);
-    uint32_t m = on ? ((min(s, 134u) + 120u) << 7) * 0x10001u : 0u;  // 2^(s - 127 + 120)
-    uint2 p0 = widen4(x.x, m), p1 = widen4(x.y, m), p2 = widen4(x.z, m), p3 = widen4(x.w, m);
-    if (on && s > 134u) {  // 2^(s - 7) is beyond bf16: the rest of it
-      m = ((s - 134u + 127u) << 7) * 0x10001u;
+    uint32_t m = on ? ((min(s[i], 134u) + 120u) << 7) * 0x10001u : 0u;  // 2^(s - 127 + 120)
+    uint2 p0 = widen4(x[i].x, m), p1 = widen4(x[i].y, m), p2 = widen4(x[i].z, m), p3 = widen4(x[i].w, m);
+    if (on && s[i] > 134u) {  // 2^(s - 7) is beyond bf16: the rest of it
+      m = ((s[i] - 134u + 127u) << 7) * 0x10001u;
       p0 = make_uint2(mul_bf16x2(p0.x, m), mul_bf16x2(p0.y, m)), p1 = make_uint2(mul_bf16x2(p1.x, m), mul_bf16x2(p1.y, m));
       p2 = make_uint2(mul_bf16x2(p2.x, m), mul_bf16x2(p2.y, m)), p3 = make_uint2(mul_bf16x2(p3.x, m), mul_bf16x2(p3.y, m));
     }
-    // pieces 2 c and 2 c + 1 of the half's row; the lanes of the second half
-    // write theirs in the other order, so that eight lanes meet all banks
-    const int c0 = 2 * (cpiece & 3), odd = cpiece >> 2;
-    const uint4 a = make_uint4(p0.x, p0.y, p1.x, p1.y), b = make_uint4(p2.x, p2.y, p3.x, p3.y);
+    const uint4 lo8 = make_uint4(p0.x, p0.y, p1.x, p1.y), hi8 = make_uint4(p2.x, p2.y, p3.x, p3.y);
     uint8_t* row = half + r * 128;
-    *reinterpret_cast<uint4*>(row + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? b : a;
-    *reinterpret_cast<uint4*>(row + (((c0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? a : b;
+    *reinterpret_cast<uint4*>(row + first) = odd ? hi8 : lo8;
+    *reinterpret_cast<uint4*>(row + second) = odd ? lo8 : hi8;
   }
 }
 
@@ -379,45 +402,76 @@ __device__ __forceinline__ void softmax_tile(const ChunkArgs& a, uint32_t S, uin
   tmem_st_wait();
 }
 
-// Row `r` of the tile's parts added up by a warp: lane c of 32 takes part c for
-// the maximum and the sum, then the warp reads the outputs one part after
-// another, 4 columns a lane.
-__device__ __forceinline__ void merge_row(const ChunkArgs& a, const Item& w, const chunk::Ranges& rg, int r, int lane) {
+// The parts of rows base + 32 wl .. (32 of them, below `rows`) added up by a
+// warp, always in the blocks' order: lane = row for the maxima, sums and
+// factors (kept in `f`, [32 parts][32 rows]), then eight rows at a time, four
+// columns a lane.
+__device__ __forceinline__ void merge_rows(const ChunkArgs& a, const Item& w, const chunk::Ranges& rg, int row0, int rows,
+                                           float* f, int lane) {
+  const int own = row0 + min(lane, rows - 1);
+  const int blocks = w.last - w.first + 1;
+  int slots = lane < blocks ? chunk::part_slot(w, rg, w.first + lane) : -1;
+  auto slots_from = [&](int p0) {
+    if (blocks > 32) slots = p0 + lane < blocks ? chunk::part_slot(w, rg, w.first + p0 + lane) : -1;
+  };
   float M = -INFINITY;
-  for (int c = w.first; c <= w.last; c += 32) {
-    const int slot = c + lane <= w.last ? chunk::part_slot(w, rg, c + lane) : -1;
-    float m = slot >= 0 ? __ldcg(&a.rec_ml[slot * a.slot_rows + r].x) : -INFINITY;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    M = fmaxf(M, m);
-  }
-  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-  float den = 0.f;
-  for (int c = w.first; c <= w.last; c += 32) {
-    const int slot = c + lane <= w.last ? chunk::part_slot(w, rg, c + lane) : -1;
-    float f = 0.f, d = 0.f;
-    if (slot >= 0) {
-      const float2 ml = __ldcg(&a.rec_ml[slot * a.slot_rows + r]);
-      f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
-      d = f * ml.y;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-    den += d;
-    const int n = min(32, w.last - c + 1);
+  for (int p0 = 0; p0 < blocks; p0 += 32) {
+    slots_from(p0);
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const int sl = __shfl_sync(0xFFFFFFFFu, slot, i);
-      const float fi = __shfl_sync(0xFFFFFFFFu, f, i);
-      if (fi == 0.f) continue;
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.rec + (static_cast<size_t>(sl) * a.slot_rows + r) * kD) + lane);
-      num.x = fmaf(fi, v.x, num.x), num.y = fmaf(fi, v.y, num.y), num.z = fmaf(fi, v.z, num.z), num.w = fmaf(fi, v.w, num.w);
+    for (int p = 0; p < min(32, blocks - p0); ++p) {
+      const int sl = __shfl_sync(0xFFFFFFFFu, slots, p);
+      if (sl >= 0) M = fmaxf(M, __ldcg(&a.rec_ml[static_cast<size_t>(sl) * a.slot_rows + own].x));
     }
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  const int rr = w.r0 + r, tok = rr / a.G;
-  uint16_t* y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
-  reinterpret_cast<uint2*>(y)[lane] = make_uint2(bf16x2_rn(num.x * inv, num.y * inv), bf16x2_rn(num.z * inv, num.w * inv));
+  float den = 0.f;
+  for (int g = 0; g < rows; g += 8) {
+    float4 acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < blocks; p0 += 32) {
+      slots_from(p0);
+      const int n = min(32, blocks - p0);
+      if (g == 0 || blocks > 32) {
+        __syncwarp();
+#pragma unroll 4
+        for (int p = 0; p < n; ++p) {
+          const int sl = __shfl_sync(0xFFFFFFFFu, slots, p);
+          float2 ml = make_float2(-INFINITY, 0.f);
+          if (sl >= 0) ml = __ldcg(&a.rec_ml[static_cast<size_t>(sl) * a.slot_rows + own]);
+          const float x = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
+          f[32 * p + lane] = x;
+          if (g == 0) den = fmaf(x, ml.y, den);
+        }
+        __syncwarp();
+      }
+#pragma unroll 2
+      for (int p = 0; p < n; ++p) {
+        const int sl = __shfl_sync(0xFFFFFFFFu, slots, p);
+        if (sl < 0) continue;
+        const float4* src = reinterpret_cast<const float4*>(a.rec + (static_cast<size_t>(sl) * a.slot_rows + row0 + g) * kD) + lane;
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (g + i < rows) v[i] = __ldcg(src + i * (kD / 4));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (g + i < rows) {
+            const float x = f[32 * p + g + i];
+            acc[i].x = fmaf(x, v[i].x, acc[i].x), acc[i].y = fmaf(x, v[i].y, acc[i].y);
+            acc[i].z = fmaf(x, v[i].z, acc[i].z), acc[i].w = fmaf(x, v[i].w, acc[i].w);
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (g + i >= rows) break;
+      const float d = __shfl_sync(0xFFFFFFFFu, den, g + i), inv = d > 0.f ? 1.f / d : 0.f;
+      const int rr = w.r0 + row0 + g + i, tok = rr / a.G;
+      uint16_t* y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
+      reinterpret_cast<uint2*>(y)[lane] =
+          make_uint2(bf16x2_rn(acc[i].x * inv, acc[i].y * inv), bf16x2_rn(acc[i].z * inv, acc[i].w * inv));
+    }
+  }
 }
 
 template <int MT, int NR>
@@ -473,7 +527,9 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       ctl->stop = 1u;
     }
     __syncthreads();
-  } else if (warp == kLoadWarp) {
+  } else if (warp >= kMmaWarp) {
+   reg_dec<kRestRegs>();
+   if (warp == kLoadWarp) {
     // ---- the plan, and pages into the ring
     chunk::Walk walk;
     walk.init(a, ranges, blockIdx.x, qs, rs, lane);
@@ -499,78 +555,84 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         }
       }
     }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      // ---- products
-      const uint32_t qa = smem_u32(smem + L::q), ka = smem_u32(smem + L::k), va = smem_u32(smem + L::v);
-      Ring<2> it;
-      Ring<kSlots> kr, vr;
-      uint32_t q_phase = 0, p_phase[2] = {0, 0};
-      bool issued = false;
-      for (;; it.step()) {
-        if (!wait_one(c, &ctl->it_full[it.slot], it.phase, 4u)) break;
-        const int tiles = ctl->item[it.slot].t1 - ctl->item[it.slot].t0;
-        const bool pair = ctl->item[it.slot].rows > 128;
-        mbar_arrive(&ctl->it_empty[it.slot]);
-        if (tiles == 0) break;
-        issued = true;
-        if (!wait_one(c, &ctl->q_full, q_phase, 5u)) break;
-        q_phase ^= 1u;
+   } else if (warp == kMmaWarp) {
+    // ---- products: the warp walks together, one lane issues
+    const uint64_t dq = smem_desc(smem_u32(smem + L::q), 16, 1024, kSwizzle128B);
+    const uint64_t dk = smem_desc(smem_u32(smem + L::k), 16, 1024, kSwizzle128B);
+    const uint64_t dv = smem_desc(smem_u32(smem + L::v), kHalf, 1024, kSwizzle128B);
+    Ring<2> it;
+    Ring<kSlots> kr, vr;
+    uint32_t q_phase = 0, p_phase[2] = {0, 0};
+    bool issued = false;
+    for (;; it.step()) {
+      if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) break;
+      const int tiles = __shfl_sync(0xFFFFFFFFu, ctl->item[it.slot].t1 - ctl->item[it.slot].t0, 0);
+      const bool pair = __shfl_sync(0xFFFFFFFFu, ctl->item[it.slot].rows, 0) > 128;
+      warp_arrive(&ctl->it_empty[it.slot], lane);
+      if (tiles == 0) break;
+      issued = true;
+      if (!wait(c, &ctl->q_full, q_phase, 5u)) break;
+      q_phase ^= 1u;
+      tc_fence_after();
+      const int steps = pair ? 2 * tiles : tiles;
+      // step i: stream i % 2; with a pair two steps share a key tile
+      auto scores = [&](int i) -> bool {
+        const int m = i & 1;
+        if (!pair || m == 0)
+          if (!wait(c, &ctl->k_full[kr.slot], kr.phase, 6u)) return false;
         tc_fence_after();
-        const int steps = pair ? 2 * tiles : tiles;
-        // step i: stream i % 2; with a pair two steps share a key tile
-        auto scores = [&](int i) -> bool {
-          const int m = i & 1;
-          if (!pair || m == 0)
-            if (!wait_one(c, &ctl->k_full[kr.slot], kr.phase, 6u)) return false;
-          tc_fence_after();
-          const uint32_t qb = qa + (pair && m ? kOperand : 0u), kb = ka + kr.slot * kOperand;
+        const uint64_t q = dq + (pair && m ? kOperand >> 4 : 0u), k0 = dk + kr.slot * (kOperand >> 4);
+        const uint32_t d = tmem + m * 128;
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint32_t o = (k >> 2) * kHalf + (k & 3) * 32;
-            mma_ss(tmem + m * 128, smem_desc(qb + o, 16, 1024, kSwizzle128B), smem_desc(kb + o, 16, 1024, kSwizzle128B),
-                   kIdesc, k > 0);
+            const uint32_t o = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+            mma_ss(d, q + o, k0 + o, kIdesc, k > 0);
           }
           tc_commit(&ctl->s_full[m]);
-          if (!pair || m == 1) {
-            tc_commit(&ctl->k_empty[kr.slot]);
-            kr.step();
-          }
-          return true;
-        };
-        bool ok = scores(0);
-        if (ok && steps > 1) ok = scores(1);
-        for (int i = 0; ok && i < steps; ++i) {
-          const int m = i & 1;
-          if (!pair || m == 0) ok = wait_one(c, &ctl->v_full[vr.slot], vr.phase, 7u);
-          ok = ok && wait_one(c, &ctl->p_full[m], p_phase[m], 8u);
-          if (!ok) break;
-          p_phase[m] ^= 1u;
-          tc_fence_after();
-          const uint32_t vb = va + vr.slot * kOperand;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ts(tmem + 256 + m * 128, tmem + m * 128 + 64 + 8 * k, smem_desc(vb + k * 2048, kHalf, 1024, kSwizzle128B),
-                   kIdescBt, (i >= 2 || k > 0) ? 1u : 0u);
-          if (!pair || m == 1) {
-            tc_commit(&ctl->v_empty[vr.slot]);
-            vr.step();
-          }
-          if (i + 2 >= steps) tc_commit(&ctl->o_done[m]);
-          if (i + 2 < steps) ok = scores(i + 2);
+          if (!pair || m == 1) tc_commit(&ctl->k_empty[kr.slot]);
         }
+        __syncwarp();
+        if (!pair || m == 1) kr.step();
+        return true;
+      };
+      bool ok = scores(0);
+      if (ok && steps > 1) ok = scores(1);
+      for (int i = 0; ok && i < steps; ++i) {
+        const int m = i & 1;
+        if (!pair || m == 0) ok = wait(c, &ctl->v_full[vr.slot], vr.phase, 7u);
+        ok = ok && wait(c, &ctl->p_full[m], m ? p_phase[1] : p_phase[0], 8u);
         if (!ok) break;
-      }
-      if (issued && ctl->stop != 0u) {  // products in flight end before tensor memory is given back
-        tc_commit(&ctl->fin);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(&ctl->fin, 0) && globaltimer_ns() - t0 < 20000000ull) {
+        if (m)
+          p_phase[1] ^= 1u;
+        else
+          p_phase[0] ^= 1u;
+        tc_fence_after();
+        const uint64_t v0 = dv + vr.slot * (kOperand >> 4);
+        const uint32_t d = tmem + 256 + m * 128, p = tmem + m * 128 + 64;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mma_ts(d, p + 8 * k, v0 + k * (2048 >> 4), kIdescBt, (i >= 2 || k > 0) ? 1u : 0u);
+          if (!pair || m == 1) tc_commit(&ctl->v_empty[vr.slot]);
+          if (i + 2 >= steps) tc_commit(&ctl->o_done[m]);
         }
+        __syncwarp();
+        if (!pair || m == 1) vr.step();
+        if (i + 2 < steps) ok = scores(i + 2);
+      }
+      if (!ok) break;
+    }
+    if (issued && ctl->stop != 0u) {  // products in flight end before tensor memory is given back
+      if (lane == 0) tc_commit(&ctl->fin);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(&ctl->fin, 0) && globaltimer_ns() - t0 < 20000000ull) {
       }
     }
     __syncwarp();
-  } else if (warp >= kSoftWarps && warp < kMmaWarp) {
+   }
+  } else if (warp >= kSoftWarps) {
     // ---- codes to bf16
+    reg_dec<kConvRegs>();
     const int ct = t - 32 * kSoftWarps;
     Ring<2> it;
     Ring<NR> ring;
@@ -602,8 +664,9 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         kv.step();
       }
     }
-  } else if (warp < kSoftWarps) {
+  } else {
     // ---- softmax: stream m, a thread a row
+    reg_inc<kSoftRegs>();
     const int m = warp >> 2, wl = warp & 3, row = t & 127;
     const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
     const uint32_t S = tmem + lanes + m * 128, O = tmem + lanes + 256 + m * 128;
@@ -611,8 +674,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     uint32_t s_phase = 0, o_phase = 0, g_phase = 0, x_phase = 0;
     for (bool ok = true; ok; it.step()) {
       if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) break;
-      const Item w = ctl->item[it.slot];
-      warp_arrive(&ctl->it_empty[it.slot], lane);
+      const Item& w = ctl->item[it.slot];  // given back at the item's end
       if (w.t0 == w.t1) break;
       const bool pair = w.rows > 128;
       const int tr = (pair ? 128 * m : 0) + row;  // row in the tile
@@ -739,8 +801,14 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
           if (!ok) break;
           g_phase ^= 1u;
           if (ctl->last[m]) {
-            const int base = pair ? 128 * m : 0, rows = min(128, w.rows - base);
-            for (int r = wl; r < rows; r += 4) merge_row(a, w, ranges, base + r, lane);
+            // the factors lie where the group's queries were (their products are done);
+            // few rows are spread over the four warps
+            const int base = pair ? 128 * m : 0, rows = min(128, w.rows - base), each = (rows + 3) / 4;
+            const int mine_rows = min(each, rows - wl * each);
+            if (mine_rows > 0)
+              merge_rows(a, w, ranges, base + wl * each, mine_rows,
+                         reinterpret_cast<float*>(smem + L::q + (pair ? m * kOperand : 0u)) + 1024 * wl, lane);
+            fence_proxy_async_shared();
           }
         }
       }
@@ -754,6 +822,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         }
         x_phase ^= 1u;
       }
+      warp_arrive(&ctl->it_empty[it.slot], lane);
     }
   }
   // ---- the end: every role is here, and nothing is in flight
