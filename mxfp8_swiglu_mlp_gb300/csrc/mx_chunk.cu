@@ -10,23 +10,34 @@
 // consecutive query tiles (mx_chunk_plan.cuh).  Its warps:
 //   softmax   two groups of four warps, a thread a row: scores from tensor
 //             memory, exponentials, probabilities back as bf16;
-//   convert   E4M3 codes times their block's power of two to bf16 operand tiles
+//   convert   V's codes times their block's power of two to bf16 operand tiles
 //             in shared memory;
-//   mma       one thread issues the products (tcgen05, bf16, 128 x 128);
-//   load      walks the plan, copies pages of codes into a ring.
+//   mma       issues the products (tcgen05);
+//   load      walks the plan, copies pages of codes into two rings by TMA.
 // The two softmax groups ("streams") have score and output tiles of their own
-// in tensor memory (4 x 128 columns), so that the products of one run under the
-// exponentials of the other.  With more than 128 rows a stream is a half of the
-// query tile and both see every key tile; with fewer, the streams share the
-// rows and take the key tiles in turn, and their results are added at the end.
+// in tensor memory, so that the products of one run under the exponentials of
+// the other.  With more than 128 rows a stream is a half of the query tile and
+// both see every key tile; with fewer, the streams share the rows and take the
+// key tiles in turn, and their results are added at the end.
 //
-// Exactness: an E4M3 value times a power of two has four significant bits, so
-// K^ and V^ are exact in bf16, as q is; scores are exact up to fp32 sums.  The
-// probabilities are rounded to bf16 for the second product (2^-8 at most, the
-// size of the output's own rounding, independent from token to token); maxima,
-// sums and outputs are fp32.  The maximum that scales a row is raised only when
-// it would grow by more than 2^8 (the bf16 probabilities keep their relative
-// precision up there), which spares nearly every rescaling of the outputs.
+// Scores.  K stays as it is in the cache: its codes and scales (one per 32
+// dimensions, the depth of one block-scaled MMA step) are an operand of
+// tcgen05.mma kind::mxf8f6f4.  A query (bf16, 8 significant bits) is the sum of
+// two E4M3 numbers (4 bits each), its rounding and the rest, each with its own
+// block scales, so two such products give q . K^: exact for elements down to
+// 2^-14 of their block's largest, to 2^-22 of it below.  At twice the bf16 rate
+// they cost what one bf16 product would, and K needs no conversion.
+// Outputs.  V's scales vary along the summed dimension, so V is widened to
+// bf16 (exact: four significant bits) by the convert warps, once a key tile,
+// and multiplied by the probabilities from tensor memory.
+// A key tile is 112 tokens: two score tiles, two outputs of 128 columns and the
+// scale factors then share the 512 columns of tensor memory.
+//
+// The probabilities are rounded to bf16 (2^-8 at most, the size of the output's
+// own rounding, independent from token to token); maxima, sums and outputs are
+// fp32.  The maximum that scales a row is raised only when it would grow by
+// more than 2^8 (bf16 keeps its relative precision up there), which spares
+// nearly every rescaling of the outputs.
 #include <cuda_bf16.h>
 
 #include "mx_chunk.h"
@@ -40,44 +51,43 @@ using chunk::Item;
 using chunk::kKeys;
 
 constexpr int kD = kChunkD;
-constexpr int kSoftWarps = 8, kConvWarps = 8;
+constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 1;
 constexpr int kBlock = 32 * (kMmaWarp + 4);            // warps come in groups of four
-// Registers: every thread starts with 96 (20 warps); the groups share them as
-// they need, 2 x 152 + 2 x 64 + 48 = 5 x 96.
-constexpr int kSoftRegs = 152, kConvRegs = 64, kRestRegs = 48;
-constexpr uint32_t kCodes = kKeys * kD;               // bytes of a raw K or V tile
-constexpr uint32_t kScales = kKeys * kD / 32;
-constexpr uint32_t kOperand = kKeys * kD * 2;         // a bf16 tile: two halves of 64 dimensions,
-constexpr uint32_t kHalf = kOperand / 2;              // [128 rows][128 bytes], 128-byte swizzle
-constexpr int kSlots = 2;                             // bf16 K tiles, and V tiles
+// Registers: every thread starts with 128 (16 warps); the groups share them as
+// they need, 2 x 176 + 80 + 80 = 4 x 128.
+constexpr int kSoftRegs = 176, kConvRegs = 80, kRestRegs = 80;
+constexpr uint32_t kCodes = kKeys * kD;               // bytes of a K or V tile of codes
+constexpr uint32_t kQCodes = 128 * kD;                // bytes of one term of a query tile's half
+constexpr uint32_t kScales = 512;                     // bytes kept for a tile's scales
+constexpr uint32_t kOperand = kKeys * kD * 2;         // V as bf16: two halves of 64 dimensions,
+constexpr uint32_t kHalf = kOperand / 2;              // [tokens][128 bytes], 128-byte swizzle
+constexpr int kSlots = 2;                             // bf16 V tiles
 constexpr float kGrow = 8.f;                          // in powers of two
+static_assert(kKeys % 16 == 0 && kCodes % 1024 == 0, "16-token groups, whole swizzle atoms");
+// Columns of tensor memory: scores and (in their place) probabilities of the
+// streams, outputs, scale factors of the queries (stream, term) and of K.
+constexpr uint32_t kColS = 128, kColO = 256, kColSfq = 112, kColSfk = 240;
 
 struct Ctl {
-  uint64_t raw_full[4], raw_empty[4];
-  uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
-  uint64_t s_full[2], p_full[2], o_done[2], q_full, fin;
+  uint64_t k_full[5], k_empty[5], r_full[4], r_empty[4];  // rings of K and V codes
+  uint64_t v_full[kSlots], v_empty[kSlots];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], q_full, fin;
   uint64_t group[2], second, taken;  // barriers of a softmax group; the second stream's sums ready, and read
   uint64_t it_full[2], it_empty[2];
   Item item[2];
   long long red[kBlock / 32];
   uint32_t tmem, stop, last[2];
 };
-// Shared memory for MT halves of 128 rows of queries and a ring of NR raw tiles.
-template <int MT, int NR>
+// Shared memory for MT halves of 128 rows of queries, NK tiles of K and NV of V in flight.
+template <int MT, int NK, int NV>
 struct Layout {
-  static constexpr uint32_t q = 0, k = MT * kOperand, v = k + kSlots * kOperand, raw = v + kSlots * kOperand,
-                            sc = raw + NR * kCodes, ctl = sc + NR * kScales, bytes = ctl + sizeof(Ctl);
-  static_assert(bytes <= 232448, "shared memory");
+  static constexpr uint32_t q = 0, v = MT * 2 * kQCodes, k = v + kSlots * kOperand, raw = k + NK * kCodes,
+                            sfk = raw + NV * kCodes, sv = sfk + NK * kScales, sfq = sv + NV * kScales,
+                            ctl = sfq + MT * 2 * kScales, bytes = ctl + sizeof(Ctl);
+  static_assert(bytes <= 232448 && NK <= 5 && NV <= 4, "shared memory");
 };
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -85,9 +95,8 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// kind::f16, fp32 sums, bf16 operands, M = N = 128; B K-major or (transposed) N-major.
-constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr uint32_t kIdescBt = kIdesc | (1u << 16);
+// kind::f16, fp32 sums, bf16 operands, M = N = 128, B N-major (bit 16).
+constexpr uint32_t kIdescPv = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
   asm volatile(
@@ -101,23 +110,33 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
-      "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
-      "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]),
-      "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
       "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_plain(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void tmem_st2(uint32_t taddr, float a, float b) {
@@ -219,70 +238,99 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t m) {
 }
 
 // ---------------------------------------------------------------- load warp
-template <int NR>
-__device__ __forceinline__ bool load_tile(const Ctx& c, const Item& w, int tile, uint8_t* raw, uint8_t* sc,
-                                          Ring<NR>& ring, int lane) {
-  const ChunkArgs& a = c.a;
-  const int P = 1 << a.log2P, pages = kKeys >> a.log2P;
-  const int first = tile * kKeys + lane * P;  // first token of the lane's page
-  int pid = -1;
-  if (lane < pages && first < w.hi && first + P > w.lo) {
-    pid = __ldg(a.table + static_cast<long long>(w.b) * a.max_pages + (first >> a.log2P));
-    if (pid < 0 || pid >= a.num_pages) {
+// Copies tiles of codes into the rings, 16 tokens a copy (a page holds whole
+// groups of 16), and their scales through registers: K's in the order that
+// tcgen05.cp wants, V's token by token.  A tile's scales are on their way
+// while its successor's copies are issued.
+template <int NK, int NV>
+struct Loader {
+  uint8_t *k, *raw, *sfk, *sv;
+  Ring<NK> kr;
+  Ring<NV> vr;
+  bool open = false;      // the last tile's scales are still in registers
+  uint4 ks, vs;
+  int kslot, vslot;
+
+  // page of the lane's 16 tokens of a tile, -1 when no row sees them
+  __device__ __forceinline__ int page(const ChunkArgs& a, const Item& w, int tile, int lane) const {
+    const int tok = tile * kKeys + 16 * lane;
+    if (lane >= kKeys / 16 || tok >= w.hi || tok + 16 <= w.lo) return -1;
+    return __ldg(a.table + static_cast<long long>(w.b) * a.max_pages + (tok >> a.log2P));
+  }
+  __device__ __forceinline__ void flush(const Ctx& c, int lane) {
+    if (!open) return;
+    if (lane < kKeys / 4) {
+      // token 4 lane + i: row % 32 times 16 bytes, row / 32 times 4
+      uint32_t* d = reinterpret_cast<uint32_t*>(sfk + kslot * kScales + ((4 * lane) & 31) * 16 + ((4 * lane) >> 5) * 4);
+      d[0] = ks.x, d[4] = ks.y, d[8] = ks.z, d[12] = ks.w;
+      reinterpret_cast<uint4*>(sv + vslot * kScales)[lane] = vs;
+    }
+    fence_proxy_async_shared();
+    mbar_arrive(&c.ctl->k_full[kslot]);
+    mbar_arrive(&c.ctl->r_full[vslot]);
+    open = false;
+  }
+  __device__ __forceinline__ bool tile(const Ctx& c, const Item& w, int tile, int pid, int lane) {
+    const ChunkArgs& a = c.a;
+    const int tok = tile * kKeys + 16 * lane;
+    if (pid >= a.num_pages || (pid < 0 && lane < kKeys / 16 && tok < w.hi && tok + 16 > w.lo)) {
       atomicCAS(a.status, 0u, (1u << 24) | (2u << 16) | (static_cast<uint32_t>(w.b) & 0xFFFFu));
       pid = -1;
     }
-  }
-  const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, pid >= 0)) * static_cast<uint32_t>(P) * kD;
-  // the scales of the lane's four tokens
-  const int sp = __shfl_sync(0xFFFFFFFFu, pid, (4 * lane) >> a.log2P);
-  uint4 ks = make_uint4(0u, 0u, 0u, 0u), vs = ks;
-  if (sp >= 0) {
-    const long long row = ((static_cast<long long>(sp) * a.Hkv + w.hk) << a.log2P) + ((4 * lane) & (P - 1));
-    ks = __ldg(reinterpret_cast<const uint4*>(a.ks + row * (kD / 32)));
-    vs = __ldg(reinterpret_cast<const uint4*>(a.vs + row * (kD / 32)));
-  }
-  const long long src = ((static_cast<long long>(max(pid, 0)) * a.Hkv + w.hk) << a.log2P) * kD;
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    uint64_t* full = &c.ctl->raw_full[ring.slot];
-    if (!wait(c, &c.ctl->raw_empty[ring.slot], ring.phase ^ 1u, 3u)) return false;
+    // first cache row of the lane's group (rows are below 2^31)
+    const int row = ((pid * a.Hkv + w.hk) << a.log2P) + (tok & ((1 << a.log2P) - 1));
+    const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, pid >= 0)) * 16u * kD;
+    // the scales of the lane's four tokens
+    const int spid = __shfl_sync(0xFFFFFFFFu, pid, lane >> 2), srow = __shfl_sync(0xFFFFFFFFu, row, lane >> 2) + 4 * (lane & 3);
+    uint4 nk = make_uint4(0u, 0u, 0u, 0u), nv = nk;
+    if (lane < kKeys / 4 && spid >= 0) {
+      nk = __ldg(reinterpret_cast<const uint4*>(a.ks) + (srow >> 2));
+      nv = __ldg(reinterpret_cast<const uint4*>(a.vs) + (srow >> 2));
+    }
+    if (!wait(c, &c.ctl->k_empty[kr.slot], kr.phase ^ 1u, 3u)) return false;
     fence_proxy_async_shared();
-    if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+    if (lane == 0) mbar_arrive_expect_tx(&c.ctl->k_full[kr.slot], bytes);
+    __syncwarp();
+    if (pid >= 0) tma_load_plain(k + kr.slot * kCodes + lane * 16 * kD, &a.tm_k, &c.ctl->k_full[kr.slot], 0, row);
+    if (!wait(c, &c.ctl->r_empty[vr.slot], vr.phase ^ 1u, 3u)) return false;
+    if (lane == 0) mbar_arrive_expect_tx(&c.ctl->r_full[vr.slot], bytes);
     __syncwarp();
     if (pid >= 0)
-      bulk_load_plain(raw + ring.slot * kCodes + lane * P * kD, (kv ? a.vc : a.kc) + src, P * kD, full);
-    reinterpret_cast<uint4*>(sc + ring.slot * kScales)[lane] = kv ? vs : ks;
-    mbar_arrive(full);
-    ring.step();
+      bulk_load_plain(raw + vr.slot * kCodes + lane * 16 * kD, a.vc + static_cast<size_t>(row) * kD, 16 * kD,
+                      &c.ctl->r_full[vr.slot]);
+    flush(c, lane);
+    open = true;
+    ks = nk, vs = nv, kslot = kr.slot, vslot = vr.slot;
+    kr.step();
+    vr.step();
+    return true;
   }
-  return true;
-}
+};
 
 // ---------------------------------------------------------------- convert warps
-// A raw tile of tokens from tok0 to a bf16 tile; tokens outside [lo, hi) become
+// V's codes of tokens from tok0 to a bf16 tile; tokens outside [lo, hi) become
 // zeros whatever the ring holds there.
 __device__ __forceinline__ void convert_tile(const uint8_t* raw, const uint8_t* sc, uint8_t* out, int tok0, int lo, int hi,
                                              int t) {
-  const int cpiece = t & 7, r0 = t >> 3;
+  const int piece = t & 7, r0 = t >> 3;
   const bool inside = tok0 >= lo && tok0 + kKeys <= hi;
-  uint8_t* half = out + (cpiece >> 2) * kHalf;
   constexpr int kStep = 32 * kConvWarps / 8, kPasses = kKeys / kStep;  // rows of a pass
   uint4 x[kPasses];
   uint32_t s[kPasses];
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int r = r0 + i * kStep;
-    x[i] = *reinterpret_cast<const uint4*>(raw + r * kD + 16 * cpiece);
-    s[i] = sc[4 * r + (cpiece >> 1)];
+    x[i] = *reinterpret_cast<const uint4*>(raw + r * kD + 16 * piece);
+    s[i] = sc[4 * r + (piece >> 1)];
   }
-  // pieces 2 c and 2 c + 1 of the half's row; the lanes of the second half
-  // write theirs in the other order, so that eight lanes meet all banks
-  const int odd = cpiece >> 2, first = ((2 * (cpiece & 3) + odd) ^ (r0 & 7)) << 4, second = first ^ 16;
+  // the lanes of the second half write their two pieces in the other order, so
+  // that eight lanes meet all banks
+  const int odd = piece >> 2, first = ((2 * (piece & 3) + odd) ^ (r0 & 7)) << 4, second = first ^ 16;
+  uint8_t* half = out + odd * kHalf + r0 * 128;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
-    const int r = r0 + i * kStep;
-    const bool on = inside || (tok0 + r >= lo && tok0 + r < hi);
+    const int tok = tok0 + r0 + i * kStep;
+    const bool on = inside || (tok >= lo && tok < hi);
     uint32_t m = on ? ((min(s[i], 134u) + 120u) << 7) * 0x10001u : 0u;  // 2^(s - 127 + 120)
     uint2 p0 = widen4(x[i].x, m), p1 = widen4(x[i].y, m), p2 = widen4(x[i].z, m), p3 = widen4(x[i].w, m);
     if (on && s[i] > 134u) {  // 2^(s - 7) is beyond bf16: the rest of it
@@ -291,30 +339,57 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, const uint8_t* 
       p2 = make_uint2(mul_bf16x2(p2.x, m), mul_bf16x2(p2.y, m)), p3 = make_uint2(mul_bf16x2(p3.x, m), mul_bf16x2(p3.y, m));
     }
     const uint4 lo8 = make_uint4(p0.x, p0.y, p1.x, p1.y), hi8 = make_uint4(p2.x, p2.y, p3.x, p3.y);
-    uint8_t* row = half + r * 128;
+    uint8_t* row = half + i * kStep * 128;
     *reinterpret_cast<uint4*>(row + first) = odd ? hi8 : lo8;
     *reinterpret_cast<uint4*>(row + second) = odd ? lo8 : hi8;
   }
 }
 
 // ---------------------------------------------------------------- softmax warps
-// 128 rows of queries (rows from r0 of the sequence; the last one stands in
-// for rows past the end) into a bf16 tile, by `warps` warps.
-__device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item& w, int r0, uint8_t* tile, int first, int rows,
-                                             int warp, int lane) {
+// Rows first .. first + rows - 1 of a query tile's half (row i is row r0 + i of
+// the sequence; the last one stands in for rows past the end) as two E4M3
+// terms with their scales.  Four lanes hold a block of 32 dimensions.
+__device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item& w, int r0, uint8_t* codes, uint8_t* sf, int first,
+                                             int rows, int warp, int lane) {
   const int R = w.n * a.G;
   const uint32_t flip = a.negate ? 0x80008000u : 0u;
-  const int c = lane & 15;  // 16-byte piece of the row
-  uint8_t* half = tile + (c >> 3) * kHalf;
+  const int c = lane & 15;  // the lane's 8 dimensions
 #pragma unroll 4
   for (int i = warp * 2 + (lane >> 4); i < rows; i += 8) {
     const int r = first + i, rr = min(r0 + r, R - 1), tok = rr / a.G;
     const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<long long>(w.c0 + tok) * a.ldq +
                                                          (w.hk * a.G + rr - tok * a.G) * kD) + c);
-    uint4 y;
-    y.x = __byte_perm(x.x, x.y, 0x5410) ^ flip, y.y = __byte_perm(x.x, x.y, 0x7632) ^ flip;
-    y.z = __byte_perm(x.z, x.w, 0x5410) ^ flip, y.w = __byte_perm(x.z, x.w, 0x7632) ^ flip;
-    *reinterpret_cast<uint4*>(half + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = y;
+    const uint32_t u[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
+    uint32_t am = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) am = __vmaxu2(am, u[k] & 0x7FFF7FFFu);
+    am = max(am & 0xFFFFu, am >> 16);
+    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+    // the largest below 2^8 in units of the first scale: nothing saturates, and
+    // the rest is at most 2^3 of them, four bits again
+    const int e = static_cast<int>(am >> 7);
+    const uint32_t s0 = static_cast<uint32_t>(max(e - 7, 0)), s1 = static_cast<uint32_t>(max(e - 11, 0));
+    const float i0 = inv_scale_from_ue8m0(s0), i1 = inv_scale_from_ue8m0(s1);
+    const float back = s0 != 0 ? __uint_as_float(s0 << 23) : __uint_as_float(0x00400000u);
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float v0 = bf16_lo(u[2 * k]), v1 = bf16_hi(u[2 * k]), v2 = bf16_lo(u[2 * k + 1]), v3 = bf16_hi(u[2 * k + 1]);
+      h[k] = e4m3x4_code(v0 * i0, v1 * i0, v2 * i0, v3 * i0);
+      const __nv_fp8x4_e4m3* hc = reinterpret_cast<const __nv_fp8x4_e4m3*>(&h[k]);
+      const float4 hv = static_cast<float4>(*hc);
+      l[k] = e4m3x4_code(fmaf(-hv.x, back, v0) * i1, fmaf(-hv.y, back, v1) * i1, fmaf(-hv.z, back, v2) * i1,
+                         fmaf(-hv.w, back, v3) * i1);
+    }
+    uint8_t* d = codes + r * 128 + ((((c >> 1) ^ (r & 7)) << 4) | ((c & 1) << 3));
+    *reinterpret_cast<uint2*>(d) = make_uint2(h[0], h[1]);
+    *reinterpret_cast<uint2*>(d + kQCodes) = make_uint2(l[0], l[1]);
+    if ((c & 3) == 0) {
+      uint8_t* q = sf + (r & 31) * 16 + (r >> 5) * 4 + (c >> 2);
+      q[0] = static_cast<uint8_t>(s0);
+      q[kScales] = static_cast<uint8_t>(s1);
+    }
   }
 }
 
@@ -323,46 +398,49 @@ struct RowState {
 };
 // Scores of one key tile of the thread's row to probabilities.  from / upto:
 // the columns that the row sees are from <= column < upto.
-__device__ __forceinline__ void mask32(float (&s)[32], int col0, int from, int upto) {
+template <int n>
+__device__ __forceinline__ void mask_cols(float (&s)[n], int col0, int from, int upto) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
+  for (int i = 0; i < n; ++i)
     if (col0 + i < from || col0 + i >= upto) s[i] = -INFINITY;
 }
-__device__ __forceinline__ float max32(const float (&s)[32], float m) {
+template <int n>
+__device__ __forceinline__ float max_cols(const float (&s)[n], float m) {
   float m1 = max3(s[0], s[1], m), m2 = max3(s[2], s[3], s[4]);
 #pragma unroll
-  for (int i = 5; i + 3 < 32; i += 4) {
+  for (int i = 5; i + 3 < n; i += 4) {
     m1 = max3(m1, s[i], s[i + 1]);
     m2 = max3(m2, s[i + 2], s[i + 3]);
   }
-  return max3(m1, m2, fmaxf(s[29], fmaxf(s[30], s[31])));
+  return max3(m1, m2, fmaxf(s[n - 3], fmaxf(s[n - 2], s[n - 1])));
 }
 // p = 2^(s * scale - ms) as bf16 pairs; the sum of p joins `sum`.
-__device__ __forceinline__ void exp32(const float (&s)[32], float scale, float ms, float2& sum, uint32_t (&p)[16]) {
+template <int n>
+__device__ __forceinline__ void exp_cols(const float (&s)[n], float scale, float ms, float2& sum, uint32_t (&p)[n / 2]) {
   const float2 sc = make_float2(scale, scale), mm = make_float2(-ms, -ms);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < n / 2; ++i) {
     float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), sc, mm);
     x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
     sum = __fadd2_rn(sum, x);
     p[i] = bf16x2_rn(x.x, x.y);
   }
 }
+// `half` and `full`: the barriers that hand the first 64 and the other
+// probabilities to the products.
 __device__ __forceinline__ void softmax_tile(const ChunkArgs& a, uint32_t S, uint32_t O, bool masked, int from, int upto,
-                                             bool first, RowState& st) {
-  float x[32], y[32];
-  // columns 0..63 for the maximum only
-  tmem_ld32(S, x);
-  tmem_ld32(S + 32, y);
+                                             bool first, RowState& st, uint64_t* half, int lane) {
+  float x0[32], x1[32], x2[32], x3[16];
+  tmem_ld32(S, x0);
+  tmem_ld32(S + 32, x1);
+  tmem_ld32(S + 64, x2);
+  tmem_ld16f(S + 96, x3);
   tmem_ld_wait();
-  if (masked) mask32(x, 0, from, upto), mask32(y, 32, from, upto);
-  float mx = max32(y, max32(x, -INFINITY));
-  // columns 64..127 stay in registers
-  tmem_ld32(S + 64, x);
-  tmem_ld32(S + 96, y);
-  tmem_ld_wait();
-  if (masked) mask32(x, 64, from, upto), mask32(y, 96, from, upto);
-  mx = max32(y, max32(x, mx)) * a.scale_log2;  // -inf * 0 is NaN, which fmaxf below drops
+  if (masked) {
+    mask_cols(x0, 0, from, upto), mask_cols(x1, 32, from, upto);
+    mask_cols(x2, 64, from, upto), mask_cols(x3, 96, from, upto);
+  }
+  const float mx = max_cols(x3, max_cols(x2, fmaxf(max_cols(x0, -INFINITY), max_cols(x1, -INFINITY)))) * a.scale_log2;
   const bool grow = mx > st.m + kGrow || st.m == -INFINITY;
   float al = 1.f;
   if (grow) {
@@ -372,32 +450,33 @@ __device__ __forceinline__ void softmax_tile(const ChunkArgs& a, uint32_t S, uin
   }
   if (!first && __any_sync(0xFFFFFFFFu, al != 1.f)) {
     // the outputs so far in the new unit (the scores' arrival says that their products are done)
-    float o[32];
+    float o[16];
 #pragma unroll 1
-    for (int c = 0; c < kD; c += 32) {
-      tmem_ld32(O + c, o);
+    for (int c = 0; c < kD; c += 16) {
+      tmem_ld16f(O + c, o);
       tmem_ld_wait();
+      uint32_t u[16];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] *= al;
-      tmem_st32(O + c, o);
+      for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * al);
+      tmem_st16(O + c, u);
     }
   }
   const float ms = st.m == -INFINITY ? 0.f : st.m;
   float2 sum = make_float2(0.f, 0.f);
-  // probabilities take the place of columns 64..127
+  // the probabilities take the scores' place (all of them are in registers)
   uint32_t p[16];
-  exp32(x, a.scale_log2, ms, sum, p);
-  tmem_st16(S + 96, p);
-  exp32(y, a.scale_log2, ms, sum, p);
-  tmem_st16(S + 112, p);
-  tmem_ld32(S, x);
-  tmem_ld32(S + 32, y);
-  tmem_ld_wait();
-  if (masked) mask32(x, 0, from, upto), mask32(y, 32, from, upto);
-  exp32(x, a.scale_log2, ms, sum, p);
-  tmem_st16(S + 64, p);
-  exp32(y, a.scale_log2, ms, sum, p);
-  tmem_st16(S + 80, p);
+  exp_cols(x0, a.scale_log2, ms, sum, p);
+  tmem_st16(S, p);
+  exp_cols(x1, a.scale_log2, ms, sum, p);
+  tmem_st16(S + 16, p);
+  tmem_st_wait();
+  tc_fence_before();
+  warp_arrive(half, lane);
+  exp_cols(x2, a.scale_log2, ms, sum, p);
+  tmem_st16(S + 32, p);
+  uint32_t p3[8];
+  exp_cols(x3, a.scale_log2, ms, sum, p3);
+  tmem_st8(S + 48, p3);
   st.l = fmaf(st.l, al, sum.x + sum.y);
   tmem_st_wait();
 }
@@ -474,9 +553,9 @@ __device__ __forceinline__ void merge_rows(const ChunkArgs& a, const Item& w, co
   }
 }
 
-template <int MT, int NR>
+template <int MT, int NK, int NV>
 __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
-  using L = Layout<MT, NR>;
+  using L = Layout<MT, NK, NV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + L::ctl);
   const Ctx c{a, ctl};
@@ -484,17 +563,21 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
   const int qs = a.tile_rows / a.G, rs = a.tile_rows % a.G;
   if (t == 0) {
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      mbar_init(&ctl->raw_full[i], 33);
-      mbar_init(&ctl->raw_empty[i], kConvWarps);
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(&ctl->k_full[i], 33);
+      mbar_init(&ctl->k_empty[i], 1);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(&ctl->r_full[i], 33);
+      mbar_init(&ctl->r_empty[i], kConvWarps);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->k_full[i], kConvWarps);
-      mbar_init(&ctl->k_empty[i], 1);
       mbar_init(&ctl->v_full[i], kConvWarps);
       mbar_init(&ctl->v_empty[i], 1);
       mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->p_half[i], 4);
       mbar_init(&ctl->p_full[i], 4);
       mbar_init(&ctl->o_done[i], 1);
       mbar_init(&ctl->it_full[i], 32);
@@ -530,39 +613,53 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
   } else if (warp >= kMmaWarp) {
    reg_dec<kRestRegs>();
    if (warp == kLoadWarp) {
-    // ---- the plan, and pages into the ring
+    // ---- the plan, and pages into the rings
+    if (lane == 0) tma_prefetch_desc(&a.tm_k);
     chunk::Walk walk;
     walk.init(a, ranges, blockIdx.x, qs, rs, lane);
     Ring<2> it;
-    Ring<NR> ring;
+    Loader<NK, NV> ld;
+    ld.k = smem + L::k, ld.raw = smem + L::raw, ld.sfk = smem + L::sfk, ld.sv = smem + L::sv;
     for (bool some = true, ok = true; some && ok; it.step()) {
       Item w;
-      w.t0 = w.t1 = 0;
       some = walk.next(a, lane, w);
       if (!some) w.t0 = w.t1 = 0;
+      int pid = some ? ld.page(a, w, w.t0, lane) : -1;
       if (!wait(c, &ctl->it_empty[it.slot], it.phase ^ 1u, 2u)) break;
       if (lane == 0) ctl->item[it.slot] = w;
       __syncwarp();
       mbar_arrive(&ctl->it_full[it.slot]);
-      for (int k = w.t0; ok && k < w.t1; ++k) ok = load_tile<NR>(c, w, k, smem + L::raw, smem + L::sc, ring, lane);
+      for (int k = w.t0; ok && k < w.t1; ++k) {
+        const int next = k + 1 < w.t1 ? ld.page(a, w, k + 1, lane) : -1;
+        ok = ld.tile(c, w, k, pid, lane);
+        pid = next;
+      }
+      ld.flush(c, lane);
     }
     // copies in flight land before the block ends
     if (ctl->stop != 0u) {
-      for (int i = 0; i < NR; ++i) {
-        const uint64_t t0 = globaltimer_ns();
-        const uint32_t parity = (ring.phase ^ (i >= ring.slot ? 1u : 0u)) ^ 0u;
-        while (!mbar_try_wait(&ctl->raw_full[i], parity) && globaltimer_ns() - t0 < 20000000ull) {
+      ld.flush(c, lane);
+      const uint64_t t0 = globaltimer_ns();
+      for (int i = 0; i < NK; ++i)
+        while (!mbar_try_wait(&ctl->k_full[i], ld.kr.phase ^ (i >= ld.kr.slot ? 1u : 0u)) &&
+               globaltimer_ns() - t0 < 20000000ull) {
         }
-      }
+      for (int i = 0; i < NV; ++i)
+        while (!mbar_try_wait(&ctl->r_full[i], ld.vr.phase ^ (i >= ld.vr.slot ? 1u : 0u)) &&
+               globaltimer_ns() - t0 < 20000000ull) {
+        }
     }
    } else if (warp == kMmaWarp) {
     // ---- products: the warp walks together, one lane issues
     const uint64_t dq = smem_desc(smem_u32(smem + L::q), 16, 1024, kSwizzle128B);
     const uint64_t dk = smem_desc(smem_u32(smem + L::k), 16, 1024, kSwizzle128B);
     const uint64_t dv = smem_desc(smem_u32(smem + L::v), kHalf, 1024, kSwizzle128B);
+    const uint64_t dsq = smem_desc(smem_u32(smem + L::sfq), 0, 128, kSwizzleNone);
+    const uint64_t dsk = smem_desc(smem_u32(smem + L::sfk), 0, 128, kSwizzleNone);
     Ring<2> it;
-    Ring<kSlots> kr, vr;
-    uint32_t q_phase = 0, p_phase[2] = {0, 0};
+    Ring<NK> kr;
+    Ring<kSlots> vr;
+    uint32_t q_phase = 0, p_phase[2] = {0, 0}, odd_tile = 0;
     bool issued = false;
     for (;; it.step()) {
       if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) break;
@@ -575,25 +672,35 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       q_phase ^= 1u;
       tc_fence_after();
       const int steps = pair ? 2 * tiles : tiles;
+      if (elect_one()) {  // the queries' scales: stream, term
+        for (int i = 0; i < (pair ? 4 : 2); ++i) tc_cp_32x128b_warpx4(tmem + kColSfq + 4 * i, dsq + i * (kScales >> 4));
+      }
+      __syncwarp();
       // step i: stream i % 2; with a pair two steps share a key tile
       auto scores = [&](int i) -> bool {
         const int m = i & 1;
         if (!pair || m == 0)
           if (!wait(c, &ctl->k_full[kr.slot], kr.phase, 6u)) return false;
         tc_fence_after();
-        const uint64_t q = dq + (pair && m ? kOperand >> 4 : 0u), k0 = dk + kr.slot * (kOperand >> 4);
-        const uint32_t d = tmem + m * 128;
+        const uint64_t q = dq + (pair && m ? 2 * kQCodes >> 4 : 0u), k0 = dk + kr.slot * (kCodes >> 4);
+        const uint32_t d = tmem + m * kColS, sfk = tmem + kColSfk + 4 * odd_tile,
+                       sfq = tmem + kColSfq + (pair && m ? 8 : 0);
         if (elect_one()) {
+          if (!pair || m == 0) tc_cp_32x128b_warpx4(sfk, dsk + kr.slot * (kScales >> 4));
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t o = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-            mma_ss(d, q + o, k0 + o, kIdesc, k > 0);
+          for (int k = 0; k < 8; ++k) {  // step k / 2 of 32 dimensions, term k % 2
+            const uint32_t o = (32 * (k >> 1)) >> 4;
+            tc_mma_mxf8(d, q + (k & 1) * (kQCodes >> 4) + o, k0 + o, idesc_mxf8_e4m3(kKeys, k >> 1, k >> 1),
+                        sfq + 4 * (k & 1), sfk, k > 0);
           }
           tc_commit(&ctl->s_full[m]);
           if (!pair || m == 1) tc_commit(&ctl->k_empty[kr.slot]);
         }
         __syncwarp();
-        if (!pair || m == 1) kr.step();
+        if (!pair || m == 1) {
+          kr.step();
+          odd_tile ^= 1u;
+        }
         return true;
       };
       bool ok = scores(0);
@@ -601,18 +708,27 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       for (int i = 0; ok && i < steps; ++i) {
         const int m = i & 1;
         if (!pair || m == 0) ok = wait(c, &ctl->v_full[vr.slot], vr.phase, 7u);
-        ok = ok && wait(c, &ctl->p_full[m], m ? p_phase[1] : p_phase[0], 8u);
+        const uint32_t ph = m ? p_phase[1] : p_phase[0];
+        ok = ok && wait(c, &ctl->p_half[m], ph, 8u);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t v0 = dv + vr.slot * (kOperand >> 4);
+        const uint32_t d = tmem + kColO + m * 128, p = tmem + m * kColS;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_ts(d, p + 8 * k, v0 + k * (2048 >> 4), kIdescPv, (i >= 2 || k > 0) ? 1u : 0u);
+        }
+        __syncwarp();
+        ok = wait(c, &ctl->p_full[m], ph, 8u);
         if (!ok) break;
         if (m)
           p_phase[1] ^= 1u;
         else
           p_phase[0] ^= 1u;
         tc_fence_after();
-        const uint64_t v0 = dv + vr.slot * (kOperand >> 4);
-        const uint32_t d = tmem + 256 + m * 128, p = tmem + m * 128 + 64;
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mma_ts(d, p + 8 * k, v0 + k * (2048 >> 4), kIdescBt, (i >= 2 || k > 0) ? 1u : 0u);
+          for (int k = 4; k < kKeys / 16; ++k) mma_ts(d, p + 8 * k, v0 + k * (2048 >> 4), kIdescPv, 1u);
           if (!pair || m == 1) tc_commit(&ctl->v_empty[vr.slot]);
           if (i + 2 >= steps) tc_commit(&ctl->o_done[m]);
         }
@@ -635,33 +751,27 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     reg_dec<kConvRegs>();
     const int ct = t - 32 * kSoftWarps;
     Ring<2> it;
-    Ring<NR> ring;
-    Ring<kSlots> kv;
+    Ring<NV> ring;
+    Ring<kSlots> vr;
     for (bool ok = true; ok; it.step()) {
       if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) break;
       const int t0 = ctl->item[it.slot].t0, t1 = ctl->item[it.slot].t1, lo = ctl->item[it.slot].lo,
                 hi = ctl->item[it.slot].hi;
       warp_arrive(&ctl->it_empty[it.slot], lane);
       if (t0 == t1) break;
-      for (int k = t0; ok && k < t1; ++k) {
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          uint64_t* full = v ? ctl->v_full : ctl->k_full;
-          uint64_t* empty = v ? ctl->v_empty : ctl->k_empty;
-          ok = ok && wait(c, &ctl->raw_full[ring.slot], ring.phase, 3u) &&
-               wait(c, &empty[kv.slot], kv.phase ^ 1u, 6u);
-          if (!ok) break;
-          convert_tile(smem + L::raw + ring.slot * kCodes, smem + L::sc + ring.slot * kScales,
-                       smem + (v ? L::v : L::k) + kv.slot * kOperand, k * kKeys, lo, hi, ct);
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&full[kv.slot]);
-            mbar_arrive(&ctl->raw_empty[ring.slot]);
-          }
-          ring.step();
+      for (int k = t0; k < t1; ++k) {
+        ok = wait(c, &ctl->r_full[ring.slot], ring.phase, 3u) && wait(c, &ctl->v_empty[vr.slot], vr.phase ^ 1u, 6u);
+        if (!ok) break;
+        convert_tile(smem + L::raw + ring.slot * kCodes, smem + L::sv + ring.slot * kScales,
+                     smem + L::v + vr.slot * kOperand, k * kKeys, lo, hi, ct);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ctl->v_full[vr.slot]);
+          mbar_arrive(&ctl->r_empty[ring.slot]);
         }
-        kv.step();
+        ring.step();
+        vr.step();
       }
     }
   } else {
@@ -669,7 +779,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     reg_inc<kSoftRegs>();
     const int m = warp >> 2, wl = warp & 3, row = t & 127;
     const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
-    const uint32_t S = tmem + lanes + m * 128, O = tmem + lanes + 256 + m * 128;
+    const uint32_t S = tmem + lanes + m * kColS, O = tmem + lanes + kColO + m * 128;
     Ring<2> it;
     uint32_t s_phase = 0, o_phase = 0, g_phase = 0, x_phase = 0;
     for (bool ok = true; ok; it.step()) {
@@ -679,9 +789,9 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       const bool pair = w.rows > 128;
       const int tr = (pair ? 128 * m : 0) + row;  // row in the tile
       if (pair)
-        load_queries(a, w, w.r0 + 128 * m, smem + L::q + m * kOperand, 0, 128, wl, lane);
+        load_queries(a, w, w.r0 + 128 * m, smem + L::q + m * 2 * kQCodes, smem + L::sfq + m * 2 * kScales, 0, 128, wl, lane);
       else
-        load_queries(a, w, w.r0, smem + L::q, 64 * m, 64, wl, lane);
+        load_queries(a, w, w.r0, smem + L::q, smem + L::sfq, 64 * m, 64, wl, lane);
       fence_proxy_async_shared();
       warp_arrive(&ctl->q_full, lane);
       const int rr = w.r0 + min(tr, w.rows - 1), tok = rr / a.G;
@@ -701,12 +811,11 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         s_phase ^= 1u;
         tc_fence_after();
         const int tok0 = k * kKeys;
-        if (busy) {
-          if (tok0 >= see_lo && tok0 + kKeys <= see_hi)
-            softmax_tile(a, S, O, false, 0, kKeys, first, st);
-          else
-            softmax_tile(a, S, O, true, mine - tok0, pos + 1 - tok0, first, st);
-        }
+        if (busy)
+          softmax_tile(a, S, O, tok0 < see_lo || tok0 + kKeys > see_hi, mine - tok0, pos + 1 - tok0, first, st,
+                       &ctl->p_half[m], lane);
+        else
+          warp_arrive(&ctl->p_half[m], lane);
         tc_fence_before();
         warp_arrive(&ctl->p_full[m], lane);
       }
@@ -730,7 +839,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
           if (!ok) break;
           tc_fence_after();
           float m1, l1;
-          tmem_ld2(S + 128, m1, l1);
+          tmem_ld2(S + kColS, m1, l1);
           tmem_ld_wait();
           const float M = fmaxf(st.m, m1);
           f0 = st.m == -INFINITY ? 0.f : exp2_fast(st.m - M);
@@ -807,7 +916,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
             const int mine_rows = min(each, rows - wl * each);
             if (mine_rows > 0)
               merge_rows(a, w, ranges, base + wl * each, mine_rows,
-                         reinterpret_cast<float*>(smem + L::q + (pair ? m * kOperand : 0u)) + 1024 * wl, lane);
+                         reinterpret_cast<float*>(smem + L::q + (pair ? m * 2 * kQCodes : 0u)) + 1024 * wl, lane);
             fence_proxy_async_shared();
           }
         }
@@ -837,18 +946,18 @@ int chunk_tile_rows(int T, int B, int G) {
 }
 
 namespace {
-template <int MT, int NR>
+template <int MT, int NK, int NV>
 cudaError_t launch_as(const ChunkArgs& a, cudaStream_t stream) {
-  const int bytes = static_cast<int>(Layout<MT, NR>::bytes);
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<MT, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const int bytes = static_cast<int>(Layout<MT, NK, NV>::bytes);
+  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<MT, NK, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  chunk_kernel<MT, NR><<<a.grid, kBlock, bytes, stream>>>(a);
+  chunk_kernel<MT, NK, NV><<<a.grid, kBlock, bytes, stream>>>(a);
   return cudaGetLastError();
 }
 }  // namespace
 
 cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream) {
-  return a.tile_rows == 256 ? launch_as<2, 2>(a, stream) : launch_as<1, 3>(a, stream);
+  return a.tile_rows == 256 ? launch_as<2, 4, 3>(a, stream) : launch_as<1, 5, 4>(a, stream);
 }
 
 }  // namespace fsops

@@ -13,6 +13,7 @@ constexpr size_t kChunkHeaderBytes = 256;
 constexpr size_t kChunkCounterBytes = 4096;  // two counters a block, blocks <= 256
 
 struct ChunkArgs {
+  CUtensorMap tm_k;           // K codes as [num_pages * Hkv * P, 128] bytes, boxes of 16 rows, 128-byte swizzle
   const uint16_t* q;          // row t, head h at t * ldq + h * 128
   uint16_t* out;
   long long ldq, ldo;

@@ -3,7 +3,7 @@
 //
 // A sequence's new tokens times the G query heads of a KV head are its rows
 // (row r: token r / G, head r % G); tile_rows consecutive ones make a query
-// tile, which sees the key tiles of 128 tokens that its mask reaches.  All
+// tile, which sees the key tiles of kKeys tokens that its mask reaches.  All
 // query tiles in a row (sequence, KV head, query tile), each worth
 //   kTileCost + its key tiles * (kPairCost above 128 rows, else kHalfCost)
 // units, are cut into `blocks` equal ranges of units, one a block.  A block so
@@ -18,7 +18,7 @@
 namespace fsops {
 namespace chunk {
 
-constexpr int kKeys = 128;     // tokens of a key tile
+constexpr int kKeys = 112;     // tokens of a key tile
 constexpr int kTileCost = 10;  // what a query tile costs besides its keys (queries in, outputs out)
 constexpr int kPairCost = 8;   // a key tile against two halves of 128 rows
 constexpr int kHalfCost = 5;   // a key tile against one
