@@ -12,8 +12,9 @@
 //             memory, exponentials, probabilities back as bf16;
 //   convert   V's codes times their block's power of two to bf16 operand tiles
 //             in shared memory;
-//   mma       issues the products (tcgen05);
-//   load      walks the plan, copies pages of codes into two rings by TMA.
+//   mma       two warps, one a stream, issue the products (tcgen05);
+//   load      two warps copy pages of codes into a ring for K and one for V by
+//             TMA, and their scales; one of them walks the plan.
 // The two softmax groups ("streams") have score and output tiles of their own
 // in tensor memory, so that the products of one run under the exponentials of
 // the other.  With more than 128 rows a stream is a half of the query tile and
@@ -52,7 +53,7 @@ using chunk::kKeys;
 
 constexpr int kD = kChunkD;
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 2;  // two warps each
 constexpr int kBlock = 32 * (kMmaWarp + 4);            // warps come in groups of four
 // Registers: every thread starts with 128 (16 warps); the groups share them as
 // they need, 2 x 176 + 80 + 80 = 4 x 128.
@@ -66,16 +67,18 @@ constexpr int kSlots = 2;                             // bf16 V tiles
 constexpr float kGrow = 8.f;                          // in powers of two
 static_assert(kKeys % 16 == 0 && kCodes % 1024 == 0, "16-token groups, whole swizzle atoms");
 // Columns of tensor memory: scores and (in their place) probabilities of the
-// streams, outputs, scale factors of the queries (stream, term) and of K.
+// streams, outputs, scale factors of the queries (stream, term) and of K
+// (stream, tile parity).
 constexpr uint32_t kColS = 128, kColO = 256, kColSfq = 112, kColSfk = 240;
 
 struct Ctl {
   uint64_t k_full[5], k_empty[5], r_full[4], r_empty[4];  // rings of K and V codes
   uint64_t v_full[kSlots], v_empty[kSlots];
-  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], q_full, fin;
-  uint64_t group[2], second, taken;  // barriers of a softmax group; the second stream's sums ready, and read
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], q_full, q_free, fin[2];
+  uint64_t group[2], second, taken;  // a stream's warps; the second stream's sums ready, and read
   uint64_t it_full[2], it_empty[2];
   Item item[2];
+  float2 ml[128];                    // maxima and sums of the second stream's rows
   long long red[kBlock / 32];
   uint32_t tmem, stop, last[2];
 };
@@ -139,12 +142,6 @@ __device__ __forceinline__ void tma_load_plain(void* dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void tmem_st2(uint32_t taddr, float a, float b) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "f"(a), "f"(b) : "memory");
-}
-__device__ __forceinline__ void tmem_ld2(uint32_t taddr, float& a, float& b) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(taddr) : "memory");
-}
 __device__ __forceinline__ void bulk_load_plain(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    smem_u32(dst)),
@@ -189,27 +186,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 struct Ctx {
   const ChunkArgs& a;
   Ctl* ctl;
+  volatile uint32_t* stop;  // the site of a wait that ran out
+  uint32_t tries;
 };
-// Bounded wait; false: the block gives up (the first reason is reported).
-__device__ __forceinline__ bool wait_slow(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t site) {
-  const uint64_t t0 = globaltimer_ns();
-  volatile uint32_t* stop = &c.ctl->stop;
-  while (!mbar_try_wait(bar, parity)) {
-    if (*stop != 0u) return false;
-    if (globaltimer_ns() - t0 > c.a.timeout_ns) {
-      atomicCAS(c.a.status, 0u, (5u << 24) | (site << 16) | (blockIdx.x & 0xFFFFu));  // FSOPS_ERR_TIMEOUT
-      *stop = 1u;
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool wait_one(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t site) {
-  return mbar_try_wait(bar, parity) || wait_slow(c, bar, parity, site);
-}
-// The same by a whole warp, whose lanes go on or give up together.
+// Bounded wait by a whole warp, whose lanes go on or give up together.  Every
+// wait is for another warp of the block, so thousandths of a second at most;
+// a failed try sleeps for microseconds, so the limit is a number of tries.
+// Where one runs out the block stops, and says so at its end.  (The code is
+// kept this short on purpose: the roles' loops together have to stay in the
+// instruction cache, and there are some thirty waits.)
 __device__ __forceinline__ bool wait(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t site) {
-  return __all_sync(0xFFFFFFFFu, wait_one(c, bar, parity, site));
+  bool ok = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xFFFFFFFFu, ok)) {
+#pragma unroll 1
+    for (uint32_t n = c.tries; !(ok = mbar_try_wait(bar, parity)); --n) {
+      if (n == 0) *c.stop = site;
+      if (*c.stop != 0u) break;
+    }
+    ok = __all_sync(0xFFFFFFFFu, ok);
+  }
+  return ok;
 }
 // A warp's arrival, after all its lanes' writes.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
@@ -237,73 +233,98 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t m) {
   return make_uint2(mul_bf16x2(even, m), mul_bf16x2(odd, m));
 }
 
-// ---------------------------------------------------------------- load warp
-// Copies tiles of codes into the rings, 16 tokens a copy (a page holds whole
-// groups of 16), and their scales through registers: K's in the order that
-// tcgen05.cp wants, V's token by token.  A tile's scales are on their way
-// while its successor's copies are issued.
-template <int NK, int NV>
+// ---------------------------------------------------------------- load warps
+// One of them copies K's key tiles into its ring (boxes of 16 tokens, swizzled
+// as the products read them; a page holds whole groups of 16), the other V's
+// (a page's tokens a copy), and their scales: K's in the order that tcgen05.cp
+// wants, V's token by token.  A copy costs its warp about 50 cycles to issue,
+// which is why there are two; page ids are fetched a tile ahead.
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The thread's arrival on `bar` when its copies so far have landed.
+__device__ __forceinline__ void copy_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 struct Loader {
-  uint8_t *k, *raw, *sfk, *sv;
-  Ring<NK> kr;
-  Ring<NV> vr;
-  bool open = false;      // the last tile's scales are still in registers
-  uint4 ks, vs;
-  int kslot, vslot;
+  bool v;
+  int stages;
+  uint8_t *codes, *sf;
+  const uint8_t* scales;
+  uint64_t *full, *empty;
+  int slot = 0;
+  uint32_t phase = 0;
 
-  // page of the lane's 16 tokens of a tile, -1 when no row sees them
-  __device__ __forceinline__ int page(const ChunkArgs& a, const Item& w, int tile, int lane) const {
-    const int tok = tile * kKeys + 16 * lane;
-    if (lane >= kKeys / 16 || tok >= w.hi || tok + 16 <= w.lo) return -1;
+  __device__ __forceinline__ int page(const ChunkArgs& a, const Item& w, int tok) const {
+    tok = min(max(tok, w.lo), w.hi - 1);  // (the same page where the tokens' group is seen at all)
     return __ldg(a.table + static_cast<long long>(w.b) * a.max_pages + (tok >> a.log2P));
   }
-  __device__ __forceinline__ void flush(const Ctx& c, int lane) {
-    if (!open) return;
-    if (lane < kKeys / 4) {
-      // token 4 lane + i: row % 32 times 16 bytes, row / 32 times 4
-      uint32_t* d = reinterpret_cast<uint32_t*>(sfk + kslot * kScales + ((4 * lane) & 31) * 16 + ((4 * lane) >> 5) * 4);
-      d[0] = ks.x, d[4] = ks.y, d[8] = ks.z, d[12] = ks.w;
-      reinterpret_cast<uint4*>(sv + vslot * kScales)[lane] = vs;
-    }
-    fence_proxy_async_shared();
-    mbar_arrive(&c.ctl->k_full[kslot]);
-    mbar_arrive(&c.ctl->r_full[vslot]);
-    open = false;
-  }
-  __device__ __forceinline__ bool tile(const Ctx& c, const Item& w, int tile, int pid, int lane) {
-    const ChunkArgs& a = c.a;
-    const int tok = tile * kKeys + 16 * lane;
-    if (pid >= a.num_pages || (pid < 0 && lane < kKeys / 16 && tok < w.hi && tok + 16 > w.lo)) {
+  // first row of token tok's place on a page; a bad page id is reported and page 0 read instead
+  __device__ __forceinline__ int row(const ChunkArgs& a, const Item& w, int pid, int tok) const {
+    if (pid < 0 || pid >= a.num_pages) {
       atomicCAS(a.status, 0u, (1u << 24) | (2u << 16) | (static_cast<uint32_t>(w.b) & 0xFFFFu));
-      pid = -1;
+      pid = 0;
     }
-    // first cache row of the lane's group (rows are below 2^31)
-    const int row = ((pid * a.Hkv + w.hk) << a.log2P) + (tok & ((1 << a.log2P) - 1));
-    const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, pid >= 0)) * 16u * kD;
-    // the scales of the lane's four tokens
-    const int spid = __shfl_sync(0xFFFFFFFFu, pid, lane >> 2), srow = __shfl_sync(0xFFFFFFFFu, row, lane >> 2) + 4 * (lane & 3);
-    uint4 nk = make_uint4(0u, 0u, 0u, 0u), nv = nk;
-    if (lane < kKeys / 4 && spid >= 0) {
-      nk = __ldg(reinterpret_cast<const uint4*>(a.ks) + (srow >> 2));
-      nv = __ldg(reinterpret_cast<const uint4*>(a.vs) + (srow >> 2));
+    return ((pid * a.Hkv + w.hk) << a.log2P) + (tok & ((1 << a.log2P) - 1));  // below 2^31
+  }
+  __device__ __forceinline__ bool item(const Ctx& c, const Item& w, int lane) {
+    const ChunkArgs& a = c.a;
+    const int each = v ? 1 << a.log2P : 16;  // tokens of a copy
+    const int t1 = w.t1, lo16 = w.lo & ~15, hi16 = (w.hi + 15) & ~15;
+    int copy_page = 0, scale_page = 0, tok = 0, n = 0;
+    auto look = [&](int tile) {  // the lane's copy of a tile, and the pages
+      const int from = max(tile * kKeys, lo16), at = (v ? from & -each : tile * kKeys) + lane * each;
+      tok = max(at, from);
+      n = min(at + each, min((tile + 1) * kKeys, hi16)) - tok;
+      copy_page = page(a, w, tok);
+      scale_page = page(a, w, tile * kKeys + 4 * lane);
+    };
+    if (w.t0 < t1) look(w.t0);
+#pragma unroll 1
+    for (int k = w.t0; k < t1; ++k) {
+      const int t4 = k * kKeys + 4 * lane;
+      const bool scaled = lane < kKeys / 4 && t4 < w.hi && t4 + 4 > w.lo;
+      const size_t r = n > 0 ? row(a, w, copy_page, tok) : 0;
+      const uint8_t* s = scales + (scaled ? static_cast<size_t>(row(a, w, scale_page, t4)) * (kD / 32) : 0);
+      const int bytes = n * kD;
+      uint8_t* d = codes + slot * kCodes + (tok - k * kKeys) * kD;
+      if (k + 1 < t1) look(k + 1);
+      if (!wait(c, empty + slot, phase ^ 1u, 3u)) return false;
+      uint64_t* bar = full + slot;
+      fence_proxy_async_shared();
+      if (lane == 0)
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(min((k + 1) * kKeys, hi16) - max(k * kKeys, lo16)) * kD);
+      __syncwarp();
+      if (bytes > 0) {
+        if (v)
+          bulk_load_plain(d, a.vc + r * kD, bytes, bar);
+        else
+          tma_load_plain(d, &a.tm_k, bar, 0, static_cast<int>(r));
+      }
+      if (scaled) {
+        // K: token 4 lane + i at row % 32 times 16 bytes, row / 32 times 4
+        const uint32_t f = smem_u32(sf + slot * kScales) + (v ? 16 * lane : ((4 * lane) & 31) * 16 + ((4 * lane) >> 5) * 4);
+        if (v) {
+          copy_async16(f, s);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) copy_async4(f + 16 * i, s + 4 * i);
+        }
+      }
+      copy_async_arrive(bar);
+      if (++slot == stages) slot = 0, phase ^= 1u;
     }
-    if (!wait(c, &c.ctl->k_empty[kr.slot], kr.phase ^ 1u, 3u)) return false;
-    fence_proxy_async_shared();
-    if (lane == 0) mbar_arrive_expect_tx(&c.ctl->k_full[kr.slot], bytes);
-    __syncwarp();
-    if (pid >= 0) tma_load_plain(k + kr.slot * kCodes + lane * 16 * kD, &a.tm_k, &c.ctl->k_full[kr.slot], 0, row);
-    if (!wait(c, &c.ctl->r_empty[vr.slot], vr.phase ^ 1u, 3u)) return false;
-    if (lane == 0) mbar_arrive_expect_tx(&c.ctl->r_full[vr.slot], bytes);
-    __syncwarp();
-    if (pid >= 0)
-      bulk_load_plain(raw + vr.slot * kCodes + lane * 16 * kD, a.vc + static_cast<size_t>(row) * kD, 16 * kD,
-                      &c.ctl->r_full[vr.slot]);
-    flush(c, lane);
-    open = true;
-    ks = nk, vs = nv, kslot = kr.slot, vslot = vr.slot;
-    kr.step();
-    vr.step();
     return true;
+  }
+  // copies in flight land before the block ends (only after a wait ran out)
+  __device__ __forceinline__ void drain() {
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = 0; i < stages; ++i)
+      while (!mbar_try_wait(full + i, phase ^ (i >= slot ? 1u : 0u)) && globaltimer_ns() - t0 < 20000000ull) {
+      }
   }
 };
 
@@ -315,50 +336,61 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, const uint8_t* 
   const int piece = t & 7, r0 = t >> 3;
   const bool inside = tok0 >= lo && tok0 + kKeys <= hi;
   constexpr int kStep = 32 * kConvWarps / 8, kPasses = kKeys / kStep;  // rows of a pass
-  uint4 x[kPasses];
-  uint32_t s[kPasses];
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int r = r0 + i * kStep;
-    x[i] = *reinterpret_cast<const uint4*>(raw + r * kD + 16 * piece);
-    s[i] = sc[4 * r + (piece >> 1)];
-  }
   // the lanes of the second half write their two pieces in the other order, so
   // that eight lanes meet all banks
   const int odd = piece >> 2, first = ((2 * (piece & 3) + odd) ^ (r0 & 7)) << 4, second = first ^ 16;
-  uint8_t* half = out + odd * kHalf + r0 * 128;
-#pragma unroll
+  uint8_t* row = out + odd * kHalf + r0 * 128;
+  raw += r0 * kD + 16 * piece, sc += 4 * r0 + (piece >> 1);
+  uint4 next = *reinterpret_cast<const uint4*>(raw);
+  uint32_t snext = *sc;
+#pragma unroll 1
   for (int i = 0; i < kPasses; ++i) {
+    const uint4 x = next;
+    const uint32_t s = snext;
+    if (i + 1 < kPasses) {
+      raw += kStep * kD, sc += kStep * 4;
+      next = *reinterpret_cast<const uint4*>(raw);
+      snext = *sc;
+    }
     const int tok = tok0 + r0 + i * kStep;
     const bool on = inside || (tok >= lo && tok < hi);
-    uint32_t m = on ? ((min(s[i], 134u) + 120u) << 7) * 0x10001u : 0u;  // 2^(s - 127 + 120)
-    uint2 p0 = widen4(x[i].x, m), p1 = widen4(x[i].y, m), p2 = widen4(x[i].z, m), p3 = widen4(x[i].w, m);
-    if (on && s[i] > 134u) {  // 2^(s - 7) is beyond bf16: the rest of it
-      m = ((s[i] - 134u + 127u) << 7) * 0x10001u;
+    uint32_t m = on ? ((min(s, 134u) + 120u) << 7) * 0x10001u : 0u;  // 2^(s - 127 + 120)
+    uint2 p0 = widen4(x.x, m), p1 = widen4(x.y, m), p2 = widen4(x.z, m), p3 = widen4(x.w, m);
+    if (on && s > 134u) {  // 2^(s - 7) is beyond bf16: the rest of it
+      m = ((s - 134u + 127u) << 7) * 0x10001u;
       p0 = make_uint2(mul_bf16x2(p0.x, m), mul_bf16x2(p0.y, m)), p1 = make_uint2(mul_bf16x2(p1.x, m), mul_bf16x2(p1.y, m));
       p2 = make_uint2(mul_bf16x2(p2.x, m), mul_bf16x2(p2.y, m)), p3 = make_uint2(mul_bf16x2(p3.x, m), mul_bf16x2(p3.y, m));
     }
     const uint4 lo8 = make_uint4(p0.x, p0.y, p1.x, p1.y), hi8 = make_uint4(p2.x, p2.y, p3.x, p3.y);
-    uint8_t* row = half + i * kStep * 128;
     *reinterpret_cast<uint4*>(row + first) = odd ? hi8 : lo8;
     *reinterpret_cast<uint4*>(row + second) = odd ? lo8 : hi8;
+    row += kStep * 128;
   }
 }
 
 // ---------------------------------------------------------------- softmax warps
 // Rows first .. first + rows - 1 of a query tile's half (row i is row r0 + i of
 // the sequence; the last one stands in for rows past the end) as two E4M3
-// terms with their scales.  Four lanes hold a block of 32 dimensions.
+// terms with their scales, by four warps (rows a multiple of 64).  Four lanes
+// hold a block of 32 dimensions.
 __device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item& w, int r0, uint8_t* codes, uint8_t* sf, int first,
                                              int rows, int warp, int lane) {
   const int R = w.n * a.G;
   const uint32_t flip = a.negate ? 0x80008000u : 0u;
   const int c = lane & 15;  // the lane's 8 dimensions
-#pragma unroll 4
-  for (int i = warp * 2 + (lane >> 4); i < rows; i += 8) {
-    const int r = first + i, rr = min(r0 + r, R - 1), tok = rr / a.G;
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<long long>(w.c0 + tok) * a.ldq +
-                                                         (w.hk * a.G + rr - tok * a.G) * kD) + c);
+#pragma unroll 1
+  for (int i0 = warp * 2 + (lane >> 4); i0 < rows; i0 += 32) {
+   uint4 xs[4];
+#pragma unroll
+   for (int k = 0; k < 4; ++k) {
+    const int rr = min(r0 + first + i0 + 8 * k, R - 1), tok = rr / a.G;
+    xs[k] = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<long long>(w.c0 + tok) * a.ldq +
+                                                 (w.hk * a.G + rr - tok * a.G) * kD) + c);
+   }
+#pragma unroll
+   for (int k0 = 0; k0 < 4; ++k0) {
+    const int r = first + i0 + 8 * k0;
+    const uint4 x = xs[k0];
     const uint32_t u[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
     uint32_t am = 0;
 #pragma unroll
@@ -390,6 +422,7 @@ __device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item& w, 
       q[0] = static_cast<uint8_t>(s0);
       q[kScales] = static_cast<uint8_t>(s1);
     }
+   }
   }
 }
 
@@ -426,8 +459,9 @@ __device__ __forceinline__ void exp_cols(const float (&s)[n], float scale, float
     p[i] = bf16x2_rn(x.x, x.y);
   }
 }
-// `half` and `full`: the barriers that hand the first 64 and the other
-// probabilities to the products.
+// One key tile of the thread's row; from / upto: the tile's columns that it
+// sees.  `half`: the barrier that hands the first 64 probabilities to the
+// products, before the others are computed.
 __device__ __forceinline__ void softmax_tile(const ChunkArgs& a, uint32_t S, uint32_t O, bool masked, int from, int upto,
                                              bool first, RowState& st, uint64_t* half, int lane) {
   float x0[32], x1[32], x2[32], x3[16];
@@ -440,10 +474,10 @@ __device__ __forceinline__ void softmax_tile(const ChunkArgs& a, uint32_t S, uin
     mask_cols(x0, 0, from, upto), mask_cols(x1, 32, from, upto);
     mask_cols(x2, 64, from, upto), mask_cols(x3, 96, from, upto);
   }
-  const float mx = max_cols(x3, max_cols(x2, fmaxf(max_cols(x0, -INFINITY), max_cols(x1, -INFINITY)))) * a.scale_log2;
-  const bool grow = mx > st.m + kGrow || st.m == -INFINITY;
+  const float mx = fmaxf(max3(max_cols(x0, -INFINITY), max_cols(x1, -INFINITY), max_cols(x2, -INFINITY)),
+                         max_cols(x3, -INFINITY)) * a.scale_log2;
   float al = 1.f;
-  if (grow) {
+  if (mx > st.m + kGrow || st.m == -INFINITY) {
     const float mn = fmaxf(st.m, mx);
     al = mn == -INFINITY ? 1.f : exp2_fast(st.m - mn);
     st.m = mn;
@@ -462,12 +496,12 @@ __device__ __forceinline__ void softmax_tile(const ChunkArgs& a, uint32_t S, uin
     }
   }
   const float ms = st.m == -INFINITY ? 0.f : st.m;
-  float2 sum = make_float2(0.f, 0.f);
+  float2 sum = make_float2(0.f, 0.f), sum1 = sum;
   // the probabilities take the scores' place (all of them are in registers)
   uint32_t p[16];
   exp_cols(x0, a.scale_log2, ms, sum, p);
   tmem_st16(S, p);
-  exp_cols(x1, a.scale_log2, ms, sum, p);
+  exp_cols(x1, a.scale_log2, ms, sum1, p);
   tmem_st16(S + 16, p);
   tmem_st_wait();
   tc_fence_before();
@@ -475,71 +509,56 @@ __device__ __forceinline__ void softmax_tile(const ChunkArgs& a, uint32_t S, uin
   exp_cols(x2, a.scale_log2, ms, sum, p);
   tmem_st16(S + 32, p);
   uint32_t p3[8];
-  exp_cols(x3, a.scale_log2, ms, sum, p3);
+  exp_cols(x3, a.scale_log2, ms, sum1, p3);
   tmem_st8(S + 48, p3);
-  st.l = fmaf(st.l, al, sum.x + sum.y);
+  st.l = fmaf(st.l, al, (sum.x + sum.y) + (sum1.x + sum1.y));
   tmem_st_wait();
 }
 
-// The parts of rows base + 32 wl .. (32 of them, below `rows`) added up by a
+// The parts of `rows` (at most 32) rows of the tile from row0 on added up by a
 // warp, always in the blocks' order: lane = row for the maxima, sums and
-// factors (kept in `f`, [32 parts][32 rows]), then eight rows at a time, four
-// columns a lane.
+// factors, then eight rows at a time, four columns a lane.
 __device__ __forceinline__ void merge_rows(const ChunkArgs& a, const Item& w, const chunk::Ranges& rg, int row0, int rows,
-                                           float* f, int lane) {
+                                           int lane) {
   const int own = row0 + min(lane, rows - 1);
   const int blocks = w.last - w.first + 1;
-  int slots = lane < blocks ? chunk::part_slot(w, rg, w.first + lane) : -1;
-  auto slots_from = [&](int p0) {
-    if (blocks > 32) slots = p0 + lane < blocks ? chunk::part_slot(w, rg, w.first + p0 + lane) : -1;
+  int slots = -1, from = -32;  // slots of the parts from .. from + 31, one a lane
+  auto slot_of = [&](int p) {
+    if (p >= from + 32 || p < from) {
+      from = p & ~31;
+      slots = from + lane < blocks ? chunk::part_slot(w, rg, w.first + from + lane) : -1;
+    }
+    return __shfl_sync(0xFFFFFFFFu, slots, p & 31);
   };
   float M = -INFINITY;
-  for (int p0 = 0; p0 < blocks; p0 += 32) {
-    slots_from(p0);
-#pragma unroll 4
-    for (int p = 0; p < min(32, blocks - p0); ++p) {
-      const int sl = __shfl_sync(0xFFFFFFFFu, slots, p);
-      if (sl >= 0) M = fmaxf(M, __ldcg(&a.rec_ml[static_cast<size_t>(sl) * a.slot_rows + own].x));
-    }
+  for (int p = 0; p < blocks; ++p) {
+    const int sl = slot_of(p);
+    if (sl >= 0) M = fmaxf(M, __ldcg(&a.rec_ml[static_cast<size_t>(sl) * a.slot_rows + own].x));
   }
   float den = 0.f;
   for (int g = 0; g < rows; g += 8) {
     float4 acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < blocks; p0 += 32) {
-      slots_from(p0);
-      const int n = min(32, blocks - p0);
-      if (g == 0 || blocks > 32) {
-        __syncwarp();
-#pragma unroll 4
-        for (int p = 0; p < n; ++p) {
-          const int sl = __shfl_sync(0xFFFFFFFFu, slots, p);
-          float2 ml = make_float2(-INFINITY, 0.f);
-          if (sl >= 0) ml = __ldcg(&a.rec_ml[static_cast<size_t>(sl) * a.slot_rows + own]);
-          const float x = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
-          f[32 * p + lane] = x;
-          if (g == 0) den = fmaf(x, ml.y, den);
-        }
-        __syncwarp();
-      }
 #pragma unroll 2
-      for (int p = 0; p < n; ++p) {
-        const int sl = __shfl_sync(0xFFFFFFFFu, slots, p);
-        if (sl < 0) continue;
-        const float4* src = reinterpret_cast<const float4*>(a.rec + (static_cast<size_t>(sl) * a.slot_rows + row0 + g) * kD) + lane;
-        float4 v[8];
+    for (int p = 0; p < blocks; ++p) {
+      const int sl = slot_of(p);
+      if (sl < 0) continue;
+      const float2 ml = __ldcg(&a.rec_ml[static_cast<size_t>(sl) * a.slot_rows + own]);
+      const float4* src = reinterpret_cast<const float4*>(a.rec + (static_cast<size_t>(sl) * a.slot_rows + row0 + g) * kD) + lane;
+      float4 v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (g + i < rows) v[i] = __ldcg(src + i * (kD / 4));
+      for (int i = 0; i < 8; ++i)
+        if (g + i < rows) v[i] = __ldcg(src + i * (kD / 4));
+      const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
+      if (g == 0) den = fmaf(f, ml.y, den);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (g + i < rows) {
-            const float x = f[32 * p + g + i];
-            acc[i].x = fmaf(x, v[i].x, acc[i].x), acc[i].y = fmaf(x, v[i].y, acc[i].y);
-            acc[i].z = fmaf(x, v[i].z, acc[i].z), acc[i].w = fmaf(x, v[i].w, acc[i].w);
-          }
-      }
+      for (int i = 0; i < 8; ++i)
+        if (g + i < rows) {
+          const float x = __shfl_sync(0xFFFFFFFFu, f, g + i);
+          acc[i].x = fmaf(x, v[i].x, acc[i].x), acc[i].y = fmaf(x, v[i].y, acc[i].y);
+          acc[i].z = fmaf(x, v[i].z, acc[i].z), acc[i].w = fmaf(x, v[i].w, acc[i].w);
+        }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -558,14 +577,14 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
   using L = Layout<MT, NK, NV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + L::ctl);
-  const Ctx c{a, ctl};
+  const Ctx c{a, ctl, &ctl->stop, a.tries};
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int qs = a.tile_rows / a.G, rs = a.tile_rows % a.G;
   if (t == 0) {
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
       mbar_init(&ctl->k_full[i], 33);
-      mbar_init(&ctl->k_empty[i], 1);
+      mbar_init(&ctl->k_empty[i], 2);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -575,20 +594,20 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->v_full[i], kConvWarps);
-      mbar_init(&ctl->v_empty[i], 1);
+      mbar_init(&ctl->v_empty[i], 2);
       mbar_init(&ctl->s_full[i], 1);
       mbar_init(&ctl->p_half[i], 4);
       mbar_init(&ctl->p_full[i], 4);
       mbar_init(&ctl->o_done[i], 1);
+      mbar_init(&ctl->fin[i], 1);
+      mbar_init(&ctl->group[i], 4);
       mbar_init(&ctl->it_full[i], 32);
-      mbar_init(&ctl->it_empty[i], kSoftWarps + kConvWarps + 1);
+      mbar_init(&ctl->it_empty[i], kSoftWarps + kConvWarps + 3);
     }
     mbar_init(&ctl->q_full, kSoftWarps);
-    mbar_init(&ctl->group[0], 4);
-    mbar_init(&ctl->group[1], 4);
+    mbar_init(&ctl->q_free, 2);
     mbar_init(&ctl->second, 4);
     mbar_init(&ctl->taken, 4);
-    mbar_init(&ctl->fin, 1);
     ctl->stop = 0u;
     mbar_fence_init();
   }
@@ -607,59 +626,53 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (t == 0) {
       atomicCAS(a.status, 0u, (3u << 24) | (9u << 16));
-      ctl->stop = 1u;
+      ctl->stop = 9u;
     }
     __syncthreads();
   } else if (warp >= kMmaWarp) {
    reg_dec<kRestRegs>();
-   if (warp == kLoadWarp) {
-    // ---- the plan, and pages into the rings
-    if (lane == 0) tma_prefetch_desc(&a.tm_k);
+   if (warp >= kLoadWarp) {
+    // ---- codes and scales into the rings; the first of the two walks the plan
+    Loader ld;
+    ld.v = warp > kLoadWarp;
+    ld.stages = ld.v ? NV : NK;
+    ld.codes = smem + (ld.v ? L::raw : L::k), ld.sf = smem + (ld.v ? L::sv : L::sfk);
+    ld.scales = ld.v ? a.vs : a.ks;
+    ld.full = ld.v ? ctl->r_full : ctl->k_full, ld.empty = ld.v ? ctl->r_empty : ctl->k_empty;
     chunk::Walk walk;
-    walk.init(a, ranges, blockIdx.x, qs, rs, lane);
+    if (!ld.v) {
+      if (lane == 0) tma_prefetch_desc(&a.tm_k);
+      walk.init(a, ranges, blockIdx.x, qs, rs, lane);
+    }
     Ring<2> it;
-    Loader<NK, NV> ld;
-    ld.k = smem + L::k, ld.raw = smem + L::raw, ld.sfk = smem + L::sfk, ld.sv = smem + L::sv;
-    for (bool some = true, ok = true; some && ok; it.step()) {
-      Item w;
-      some = walk.next(a, lane, w);
-      if (!some) w.t0 = w.t1 = 0;
-      int pid = some ? ld.page(a, w, w.t0, lane) : -1;
-      if (!wait(c, &ctl->it_empty[it.slot], it.phase ^ 1u, 2u)) break;
-      if (lane == 0) ctl->item[it.slot] = w;
-      __syncwarp();
-      mbar_arrive(&ctl->it_full[it.slot]);
-      for (int k = w.t0; ok && k < w.t1; ++k) {
-        const int next = k + 1 < w.t1 ? ld.page(a, w, k + 1, lane) : -1;
-        ok = ld.tile(c, w, k, pid, lane);
-        pid = next;
+#pragma unroll 1
+    for (;; it.step()) {
+      Item& w = ctl->item[it.slot];
+      if (!ld.v) {
+        Item next;
+        if (!walk.next(a, lane, next)) next.t0 = next.t1 = 0;
+        if (!wait(c, &ctl->it_empty[it.slot], it.phase ^ 1u, 2u)) break;
+        if (lane == 0) w = next;
+        __syncwarp();
+        mbar_arrive(&ctl->it_full[it.slot]);
+      } else if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) {
+        break;
       }
-      ld.flush(c, lane);
+      if (w.t0 == w.t1 || !ld.item(c, w, lane)) break;
+      if (ld.v) warp_arrive(&ctl->it_empty[it.slot], lane);
     }
-    // copies in flight land before the block ends
-    if (ctl->stop != 0u) {
-      ld.flush(c, lane);
-      const uint64_t t0 = globaltimer_ns();
-      for (int i = 0; i < NK; ++i)
-        while (!mbar_try_wait(&ctl->k_full[i], ld.kr.phase ^ (i >= ld.kr.slot ? 1u : 0u)) &&
-               globaltimer_ns() - t0 < 20000000ull) {
-        }
-      for (int i = 0; i < NV; ++i)
-        while (!mbar_try_wait(&ctl->r_full[i], ld.vr.phase ^ (i >= ld.vr.slot ? 1u : 0u)) &&
-               globaltimer_ns() - t0 < 20000000ull) {
-        }
-    }
-   } else if (warp == kMmaWarp) {
-    // ---- products: the warp walks together, one lane issues
-    const uint64_t dq = smem_desc(smem_u32(smem + L::q), 16, 1024, kSwizzle128B);
+    if (*c.stop != 0u) ld.drain();
+   } else {
+    // ---- products of stream m: the warp walks together, one lane issues
+    const int m = warp - kMmaWarp;
     const uint64_t dk = smem_desc(smem_u32(smem + L::k), 16, 1024, kSwizzle128B);
     const uint64_t dv = smem_desc(smem_u32(smem + L::v), kHalf, 1024, kSwizzle128B);
-    const uint64_t dsq = smem_desc(smem_u32(smem + L::sfq), 0, 128, kSwizzleNone);
     const uint64_t dsk = smem_desc(smem_u32(smem + L::sfk), 0, 128, kSwizzleNone);
+    const uint32_t S = tmem + m * kColS, O = tmem + kColO + m * 128, sfq = tmem + kColSfq + 8 * m;
     Ring<2> it;
     Ring<NK> kr;
     Ring<kSlots> vr;
-    uint32_t q_phase = 0, p_phase[2] = {0, 0}, odd_tile = 0;
+    uint32_t q_phase = 0, p_phase = 0, odd = 0;
     bool issued = false;
     for (;; it.step()) {
       if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) break;
@@ -671,77 +684,96 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       if (!wait(c, &ctl->q_full, q_phase, 5u)) break;
       q_phase ^= 1u;
       tc_fence_after();
-      const int steps = pair ? 2 * tiles : tiles;
-      if (elect_one()) {  // the queries' scales: stream, term
-        for (int i = 0; i < (pair ? 4 : 2); ++i) tc_cp_32x128b_warpx4(tmem + kColSfq + 4 * i, dsq + i * (kScales >> 4));
+      // the stream's queries (one half of the tile, or all of it) and their scales
+      const int qt = pair ? 2 * m : 0;
+      const uint64_t dq = smem_desc(smem_u32(smem + L::q + qt * kQCodes), 16, 1024, kSwizzle128B);
+      const uint64_t dsq = smem_desc(smem_u32(smem + L::sfq + qt * kScales), 0, 128, kSwizzleNone);
+      if (elect_one()) {
+        tc_cp_32x128b_warpx4(sfq, dsq);
+        tc_cp_32x128b_warpx4(sfq + 4, dsq + (kScales >> 4));
       }
       __syncwarp();
-      // step i: stream i % 2; with a pair two steps share a key tile
-      auto scores = [&](int i) -> bool {
-        const int m = i & 1;
-        if (!pair || m == 0)
+      const int step = pair ? 1 : 2, begin = pair ? 0 : m;
+      const int last = tiles - 1 - (pair ? 0 : ((tiles - 1 - begin) & 1));  // the stream's last tile (below begin: none)
+      int kt = 0, vt = 0;  // the next tile of the ring, of the bf16 slots
+      // tiles of the other stream are let go unused
+      auto skip_k = [&](int to) -> bool {
+        for (; kt < to; ++kt) {
           if (!wait(c, &ctl->k_full[kr.slot], kr.phase, 6u)) return false;
-        tc_fence_after();
-        const uint64_t q = dq + (pair && m ? 2 * kQCodes >> 4 : 0u), k0 = dk + kr.slot * (kCodes >> 4);
-        const uint32_t d = tmem + m * kColS, sfk = tmem + kColSfk + 4 * odd_tile,
-                       sfq = tmem + kColSfq + (pair && m ? 8 : 0);
-        if (elect_one()) {
-          if (!pair || m == 0) tc_cp_32x128b_warpx4(sfk, dsk + kr.slot * (kScales >> 4));
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {  // step k / 2 of 32 dimensions, term k % 2
-            const uint32_t o = (32 * (k >> 1)) >> 4;
-            tc_mma_mxf8(d, q + (k & 1) * (kQCodes >> 4) + o, k0 + o, idesc_mxf8_e4m3(kKeys, k >> 1, k >> 1),
-                        sfq + 4 * (k & 1), sfk, k > 0);
-          }
-          tc_commit(&ctl->s_full[m]);
-          if (!pair || m == 1) tc_commit(&ctl->k_empty[kr.slot]);
-        }
-        __syncwarp();
-        if (!pair || m == 1) {
+          if (lane == 0) mbar_arrive(&ctl->k_empty[kr.slot]);
           kr.step();
-          odd_tile ^= 1u;
         }
         return true;
       };
-      bool ok = scores(0);
-      if (ok && steps > 1) ok = scores(1);
-      for (int i = 0; ok && i < steps; ++i) {
-        const int m = i & 1;
-        if (!pair || m == 0) ok = wait(c, &ctl->v_full[vr.slot], vr.phase, 7u);
-        const uint32_t ph = m ? p_phase[1] : p_phase[0];
-        ok = ok && wait(c, &ctl->p_half[m], ph, 8u);
+      auto skip_v = [&](int to) -> bool {
+        for (; vt < to; ++vt) {
+          if (!wait(c, &ctl->v_full[vr.slot], vr.phase, 7u)) return false;
+          if (lane == 0) mbar_arrive(&ctl->v_empty[vr.slot]);
+          vr.step();
+        }
+        return true;
+      };
+      auto scores = [&](int j) -> bool {
+        if (!skip_k(j) || !wait(c, &ctl->k_full[kr.slot], kr.phase, 6u)) return false;
+        fence_proxy_async_shared();  // the scales came by generic copies
+        tc_fence_after();
+        const uint64_t k0 = dk + kr.slot * (kCodes >> 4);
+        const uint32_t sfk = tmem + kColSfk + 8 * m + 4 * odd;
+        if (elect_one()) {
+          tc_cp_32x128b_warpx4(sfk, dsk + kr.slot * (kScales >> 4));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {  // step k / 2 of 32 dimensions, term k % 2
+            const uint32_t o = (32 * (k >> 1)) >> 4;
+            tc_mma_mxf8(S, dq + (k & 1) * (kQCodes >> 4) + o, k0 + o, idesc_mxf8_e4m3(kKeys, k >> 1, k >> 1),
+                        sfq + 4 * (k & 1), sfk, k > 0);
+          }
+          tc_commit(&ctl->s_full[m]);
+          tc_commit(&ctl->k_empty[kr.slot]);
+          if (j == last) tc_commit(&ctl->q_free);
+        }
+        __syncwarp();
+        kr.step();
+        ++kt;
+        odd ^= 1u;
+        return true;
+      };
+      bool ok = true;
+      if (begin <= last)
+        ok = scores(begin);
+      else if (lane == 0)
+        mbar_arrive(&ctl->q_free);
+      for (int j = begin; ok && j <= last; j += step) {
+        ok = skip_v(j) && wait(c, &ctl->v_full[vr.slot], vr.phase, 7u) && wait(c, &ctl->p_half[m], p_phase, 8u);
         if (!ok) break;
         tc_fence_after();
         const uint64_t v0 = dv + vr.slot * (kOperand >> 4);
-        const uint32_t d = tmem + kColO + m * 128, p = tmem + m * kColS;
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_ts(d, p + 8 * k, v0 + k * (2048 >> 4), kIdescPv, (i >= 2 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < 4; ++k) mma_ts(O, S + 8 * k, v0 + k * (2048 >> 4), kIdescPv, (j > begin || k > 0) ? 1u : 0u);
         }
         __syncwarp();
-        ok = wait(c, &ctl->p_full[m], ph, 8u);
+        ok = wait(c, &ctl->p_full[m], p_phase, 9u);
         if (!ok) break;
-        if (m)
-          p_phase[1] ^= 1u;
-        else
-          p_phase[0] ^= 1u;
+        p_phase ^= 1u;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int k = 4; k < kKeys / 16; ++k) mma_ts(d, p + 8 * k, v0 + k * (2048 >> 4), kIdescPv, 1u);
-          if (!pair || m == 1) tc_commit(&ctl->v_empty[vr.slot]);
-          if (i + 2 >= steps) tc_commit(&ctl->o_done[m]);
+          for (int k = 4; k < kKeys / 16; ++k) mma_ts(O, S + 8 * k, v0 + k * (2048 >> 4), kIdescPv, 1u);
+          tc_commit(&ctl->v_empty[vr.slot]);
+          if (j == last) tc_commit(&ctl->o_done[m]);
         }
         __syncwarp();
-        if (!pair || m == 1) vr.step();
-        if (i + 2 < steps) ok = scores(i + 2);
+        vr.step();
+        ++vt;
+        if (j < last) ok = scores(j + step);
       }
+      ok = ok && skip_k(tiles) && skip_v(tiles);
       if (!ok) break;
     }
-    if (issued && ctl->stop != 0u) {  // products in flight end before tensor memory is given back
-      if (lane == 0) tc_commit(&ctl->fin);
+    if (issued && *c.stop != 0u) {  // products in flight end before tensor memory is given back
+      if (lane == 0) tc_commit(&ctl->fin[m]);
       const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(&ctl->fin, 0) && globaltimer_ns() - t0 < 20000000ull) {
+      while (!mbar_try_wait(&ctl->fin[m], 0) && globaltimer_ns() - t0 < 20000000ull) {
       }
     }
     __syncwarp();
@@ -777,23 +809,30 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
   } else {
     // ---- softmax: stream m, a thread a row
     reg_inc<kSoftRegs>();
-    const int m = warp >> 2, wl = warp & 3, row = t & 127;
+    const int m = warp >> 2, wl = warp & 3, row = 32 * wl + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
     const uint32_t S = tmem + lanes + m * kColS, O = tmem + lanes + kColO + m * 128;
     Ring<2> it;
-    uint32_t s_phase = 0, o_phase = 0, g_phase = 0, x_phase = 0;
-    for (bool ok = true; ok; it.step()) {
-      if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) break;
-      const Item& w = ctl->item[it.slot];  // given back at the item's end
-      if (w.t0 == w.t1) break;
-      const bool pair = w.rows > 128;
-      const int tr = (pair ? 128 * m : 0) + row;  // row in the tile
-      if (pair)
-        load_queries(a, w, w.r0 + 128 * m, smem + L::q + m * 2 * kQCodes, smem + L::sfq + m * 2 * kScales, 0, 128, wl, lane);
+    uint32_t s_phase = 0, o_phase = 0, g_phase = 0, x_phase = 0, f_phase = 0;
+    // the queries of the item in a slot, when the products are done with the last ones
+    auto queries = [&](int slot) {
+      const Item& w = ctl->item[slot];
+      if (w.t0 == w.t1) return;
+      if (w.rows > 128)
+        load_queries(a, w, w.r0 + 128 * m, smem + L::q + m * 2 * kQCodes, smem + L::sfq + m * 2 * kScales, 0, 128,
+                     wl, lane);
       else
         load_queries(a, w, w.r0, smem + L::q, smem + L::sfq, 64 * m, 64, wl, lane);
       fence_proxy_async_shared();
       warp_arrive(&ctl->q_full, lane);
+    };
+    bool ok = wait(c, &ctl->it_full[0], 0, 4u);
+    if (ok) queries(0);
+    while (ok) {
+      const Item& w = ctl->item[it.slot];  // given back at the item's end
+      if (w.t0 == w.t1) break;
+      const bool pair = w.rows > 128;
+      const int tr = (pair ? 128 * m : 0) + row;  // row in the tile
       const int rr = w.r0 + min(tr, w.rows - 1), tok = rr / a.G;
       const int pos = w.len - w.n + tok;
       const bool busy = (pair ? 128 * m : 0) + 32 * wl < w.rows;  // the warp has a row
@@ -802,10 +841,10 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       const int see_hi = __reduce_min_sync(0xFFFFFFFFu, pos) + 1;
       const int mine = a.window > 0 ? pos - a.window + 1 : 0;
       RowState st{-INFINITY, 0.f};
-      const int step = pair ? 1 : 2;
+      const int step = pair ? 1 : 2, t1 = w.t1;
       int k = w.t0 + (pair ? 0 : m);
-      const bool any = k < w.t1;
-      for (bool first = true; k < w.t1; k += step, first = false) {
+      const bool any = k < t1;
+      for (bool first = true; k < t1; k += step, first = false) {
         ok = wait(c, &ctl->s_full[m], s_phase, 10u);
         if (!ok) break;
         s_phase ^= 1u;
@@ -819,7 +858,15 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         tc_fence_before();
         warp_arrive(&ctl->p_full[m], lane);
       }
+      // the next item's queries go in under this one's end
+      ok = ok && wait(c, &ctl->q_free, f_phase, 5u);
       if (!ok) break;
+      f_phase ^= 1u;
+      const int slot = it.slot;
+      it.step();
+      ok = wait(c, &ctl->it_full[it.slot], it.phase, 4u);
+      if (!ok) break;
+      queries(it.slot);
       if (any) {
         ok = wait(c, &ctl->o_done[m], o_phase, 11u);
         if (!ok) break;
@@ -828,54 +875,52 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       }
       float f0 = 1.f, f1 = 0.f;  // the streams' shares of the row's output
       if (!pair) {
-        // the second stream's sums through tensor memory to the first, which adds both up
+        // the second stream's maximum and sum to the first, which adds both up
         if (m == 1) {
-          tmem_st2(S, st.m, any ? st.l : 0.f);
-          tmem_st_wait();
-          tc_fence_before();
+          ctl->ml[row] = make_float2(st.m, st.l);
           warp_arrive(&ctl->second, lane);
         } else {
           ok = wait(c, &ctl->second, x_phase, 12u);
           if (!ok) break;
-          tc_fence_after();
-          float m1, l1;
-          tmem_ld2(S + kColS, m1, l1);
-          tmem_ld_wait();
-          const float M = fmaxf(st.m, m1);
+          const float2 ml = ctl->ml[row];
+          const float M = fmaxf(st.m, ml.x);
           f0 = st.m == -INFINITY ? 0.f : exp2_fast(st.m - M);
-          f1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - M);
-          st.l = f0 * st.l + f1 * l1;
+          f1 = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
+          st.l = f0 * st.l + f1 * ml.y;
           st.m = M;
+          tc_fence_after();
         }
       }
       if (pair || m == 0) {
-        const bool two = !pair && w.t1 - w.t0 > 1;
+        const bool two = !pair && t1 - w.t0 > 1, whole = w.whole;
         const bool write = tr < w.rows;
-        const int slot = w.whole ? 0 : chunk::part_slot(w, ranges, blockIdx.x);
-        if (w.whole) {
+        const int part = whole ? 0 : chunk::part_slot(w, ranges, blockIdx.x);
+        if (whole) {
           const float inv = st.l > 0.f ? 1.f / st.l : 0.f;
           f0 *= inv, f1 *= inv;
         }
         uint16_t* y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
-        const size_t rec = static_cast<size_t>(slot) * a.slot_rows + min(tr, w.rows - 1);
+        const size_t rec = static_cast<size_t>(part) * a.slot_rows + min(tr, w.rows - 1);
         if (busy) {
 #pragma unroll 1
           for (int col = 0; col < kD; col += 32) {
             float o[32];
             tmem_ld32(O + col, o);
             tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = f0 != 0.f ? f0 * o[i] : 0.f;
             if (two) {
-              float o1[32];
-              tmem_ld32(O + 128 + col, o1);
-              tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = (f0 != 0.f ? f0 * o[i] : 0.f) + (f1 != 0.f ? f1 * o1[i] : 0.f);
-            } else {
+              for (int j = 0; j < 32; j += 16) {
+                float o1[16];
+                tmem_ld16f(O + 128 + col + j, o1);
+                tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = f0 != 0.f ? f0 * o[i] : 0.f;
+                for (int i = 0; i < 16; ++i) o[j + i] += f1 != 0.f ? f1 * o1[i] : 0.f;
+              }
             }
             if (write) {
-              if (w.whole) {
+              if (whole) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 8)
                   *reinterpret_cast<uint4*>(y + col + i) =
@@ -888,10 +933,10 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
               }
             }
           }
-          if (!w.whole && write) a.rec_ml[rec] = make_float2(st.m, st.l);
+          if (!whole && write) a.rec_ml[rec] = make_float2(st.m, st.l);
         }
         tc_fence_before();
-        if (!w.whole) {
+        if (!whole) {
           // the last part to arrive adds them up, in the blocks' order
           __threadfence();
           warp_arrive(&ctl->group[m], lane);
@@ -910,14 +955,9 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
           if (!ok) break;
           g_phase ^= 1u;
           if (ctl->last[m]) {
-            // the factors lie where the group's queries were (their products are done);
-            // few rows are spread over the four warps
             const int base = pair ? 128 * m : 0, rows = min(128, w.rows - base), each = (rows + 3) / 4;
             const int mine_rows = min(each, rows - wl * each);
-            if (mine_rows > 0)
-              merge_rows(a, w, ranges, base + wl * each, mine_rows,
-                         reinterpret_cast<float*>(smem + L::q + (pair ? m * 2 * kQCodes : 0u)) + 1024 * wl, lane);
-            fence_proxy_async_shared();
+            if (mine_rows > 0) merge_rows(a, w, ranges, base + wl * each, mine_rows, lane);
           }
         }
       }
@@ -931,11 +971,13 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         }
         x_phase ^= 1u;
       }
-      warp_arrive(&ctl->it_empty[it.slot], lane);
+      warp_arrive(&ctl->it_empty[slot], lane);
     }
   }
   // ---- the end: every role is here, and nothing is in flight
   __syncthreads();
+  if (t == 0 && ctl->stop != 0u)  // FSOPS_ERR_TIMEOUT
+    atomicCAS(a.status, 0u, (5u << 24) | (ctl->stop << 16) | (blockIdx.x & 0xFFFFu));
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 

@@ -31,7 +31,7 @@ struct ChunkArgs {
   int negate;                 // sm_scale < 0: q enters with its sign turned
   int tile_rows;              // rows of a query tile: 128 or 256
   int grid;
-  uint64_t timeout_ns;
+  uint32_t tries;             // of a wait before it gives up
 };
 
 // Rows of a query tile for T rows of B sequences in groups of G heads.
