@@ -32,7 +32,10 @@
 // bf16 (exact: four significant bits) by the convert warps, once a key tile,
 // and multiplied by the probabilities from tensor memory.
 // A key tile is 112 tokens: two score tiles, two outputs of 128 columns and the
-// scale factors then share the 512 columns of tensor memory.
+// scale factors then share the 512 columns of tensor memory.  A stream's scores
+// are two sections of 64 and 48 keys, each computed, turned into probabilities
+// (in its place) and used by itself: while one is under the exponentials, the
+// other's products and the next tile's scores are.
 //
 // The probabilities are rounded to bf16 (2^-8 at most, the size of the output's
 // own rounding, independent from token to token); maxima, sums and outputs are
@@ -54,15 +57,13 @@ using chunk::kKeys;
 constexpr int kD = kChunkD;
 constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 2;  // two warps each
-constexpr int kBlock = 32 * (kMmaWarp + 4);            // warps come in groups of four
-// Registers: every thread starts with 128 (16 warps); the groups share them as
-// they need, 2 x 176 + 80 + 80 = 4 x 128.
-constexpr int kSoftRegs = 176, kConvRegs = 80, kRestRegs = 80;
+constexpr int kBlock = 32 * (kLoadWarp + 2);
 constexpr uint32_t kCodes = kKeys * kD;               // bytes of a K or V tile of codes
 constexpr uint32_t kQCodes = 128 * kD;                // bytes of one term of a query tile's half
 constexpr uint32_t kScales = 512;                     // bytes kept for a tile's scales
 constexpr uint32_t kOperand = kKeys * kD * 2;         // V as bf16: two halves of 64 dimensions,
 constexpr uint32_t kHalf = kOperand / 2;              // [tokens][128 bytes], 128-byte swizzle
+constexpr int kFirst = 64;                            // keys of a tile's first section
 constexpr int kSlots = 2;                             // bf16 V tiles
 constexpr float kGrow = 8.f;                          // in powers of two
 static_assert(kKeys % 16 == 0 && kCodes % 1024 == 0, "16-token groups, whole swizzle atoms");
@@ -70,16 +71,19 @@ static_assert(kKeys % 16 == 0 && kCodes % 1024 == 0, "16-token groups, whole swi
 // streams, outputs, scale factors of the queries (stream, term) and of K
 // (stream, tile parity).
 constexpr uint32_t kColS = 128, kColO = 256, kColSfq = 112, kColSfk = 240;
+static_assert(kColS == 128, "a stream's scores and outputs are equally far apart");
 
 struct Ctl {
   uint64_t k_full[5], k_empty[5], r_full[4], r_empty[4];  // rings of K and V codes
   uint64_t v_full[kSlots], v_empty[kSlots];
-  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], q_full, q_free, fin[2];
+  uint64_t s_full[2][2], p_full[2][2];  // stream, section
+  uint64_t o_first[2], o_done[2], q_full, q_free, fin[2];
   uint64_t group[2], second, taken;  // a stream's warps; the second stream's sums ready, and read
   uint64_t it_full[2], it_empty[2];
   Item item[2];
   float2 ml[128];                    // maxima and sums of the second stream's rows
   long long red[kBlock / 32];
+  chunk::Ranges ranges;
   uint32_t tmem, stop, last[2];
 };
 // Shared memory for MT halves of 128 rows of queries, NK tiles of K and NV of V in flight.
@@ -169,14 +173,6 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
   return e != 0;
 }
-template <int n>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n));
-}
-template <int n>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -235,10 +231,11 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t m) {
 
 // ---------------------------------------------------------------- load warps
 // One of them copies K's key tiles into its ring (boxes of 16 tokens, swizzled
-// as the products read them; a page holds whole groups of 16), the other V's
-// (a page's tokens a copy), and their scales: K's in the order that tcgen05.cp
-// wants, V's token by token.  A copy costs its warp about 50 cycles to issue,
-// which is why there are two; page ids are fetched a tile ahead.
+// as the products read them; a page holds whole groups of 16), the other V's,
+// and their scales: K's in the order that tcgen05.cp wants, V's token by token.
+// A copy costs its warp about 50 cycles to issue, which is why there are two
+// warps.  Four tiles' groups are looked up at a time, one a lane, and the next
+// four's pages fetched meanwhile.
 __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -258,64 +255,57 @@ struct Loader {
   int slot = 0;
   uint32_t phase = 0;
 
-  __device__ __forceinline__ int page(const ChunkArgs& a, const Item& w, int tok) const {
-    tok = min(max(tok, w.lo), w.hi - 1);  // (the same page where the tokens' group is seen at all)
-    return __ldg(a.table + static_cast<long long>(w.b) * a.max_pages + (tok >> a.log2P));
-  }
-  // first row of token tok's place on a page; a bad page id is reported and page 0 read instead
-  __device__ __forceinline__ int row(const ChunkArgs& a, const Item& w, int pid, int tok) const {
-    if (pid < 0 || pid >= a.num_pages) {
-      atomicCAS(a.status, 0u, (1u << 24) | (2u << 16) | (static_cast<uint32_t>(w.b) & 0xFFFFu));
-      pid = 0;
-    }
-    return ((pid * a.Hkv + w.hk) << a.log2P) + (tok & ((1 << a.log2P) - 1));  // below 2^31
-  }
   __device__ __forceinline__ bool item(const Ctx& c, const Item& w, int lane) {
+    constexpr int kGroups = kKeys / 16, kBatch = 4;  // groups of a tile, tiles of a batch
     const ChunkArgs& a = c.a;
-    const int each = v ? 1 << a.log2P : 16;  // tokens of a copy
-    const int t1 = w.t1, lo16 = w.lo & ~15, hi16 = (w.hi + 15) & ~15;
-    int copy_page = 0, scale_page = 0, tok = 0, n = 0;
-    auto look = [&](int tile) {  // the lane's copy of a tile, and the pages
-      const int from = max(tile * kKeys, lo16), at = (v ? from & -each : tile * kKeys) + lane * each;
-      tok = max(at, from);
-      n = min(at + each, min((tile + 1) * kKeys, hi16)) - tok;
-      copy_page = page(a, w, tok);
-      scale_page = page(a, w, tile * kKeys + 4 * lane);
-    };
-    if (w.t0 < t1) look(w.t0);
+    const int t0 = w.t0, t1 = w.t1, lo = w.lo, hi = w.hi, hk = w.hk, mask = (1 << a.log2P) - 1;
+    const int32_t* table = a.table + static_cast<long long>(w.b) * a.max_pages;
+    auto page = [&](int tok) { return __ldg(table + (min(max(tok, lo), hi - 1) >> a.log2P)); };
+    int tok = 16 * (t0 * kGroups + lane);  // the lane's group
+    int pid = page(tok);
+    const int part = lane >> 2, in = 4 * (lane & 3);  // the lane's four tokens among a tile's scales
+    const uint32_t sdst = v ? 16u * lane : ((4u * lane) & 31u) * 16u + ((4u * lane) >> 5) * 4u;
 #pragma unroll 1
-    for (int k = w.t0; k < t1; ++k) {
-      const int t4 = k * kKeys + 4 * lane;
-      const bool scaled = lane < kKeys / 4 && t4 < w.hi && t4 + 4 > w.lo;
-      const size_t r = n > 0 ? row(a, w, copy_page, tok) : 0;
-      const uint8_t* s = scales + (scaled ? static_cast<size_t>(row(a, w, scale_page, t4)) * (kD / 32) : 0);
-      const int bytes = n * kD;
-      uint8_t* d = codes + slot * kCodes + (tok - k * kKeys) * kD;
-      if (k + 1 < t1) look(k + 1);
-      if (!wait(c, empty + slot, phase ^ 1u, 3u)) return false;
-      uint64_t* bar = full + slot;
-      fence_proxy_async_shared();
-      if (lane == 0)
-        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(min((k + 1) * kKeys, hi16) - max(k * kKeys, lo16)) * kD);
-      __syncwarp();
-      if (bytes > 0) {
-        if (v)
-          bulk_load_plain(d, a.vc + r * kD, bytes, bar);
-        else
-          tma_load_plain(d, &a.tm_k, bar, 0, static_cast<int>(r));
+    for (int k = t0; k < t1; k += kBatch) {
+      if (pid < 0 || pid >= a.num_pages) {  // reported, and page 0 read instead
+        atomicCAS(a.status, 0u, (1u << 24) | (2u << 16) | (static_cast<uint32_t>(w.b) & 0xFFFFu));
+        pid = 0;
       }
-      if (scaled) {
-        // K: token 4 lane + i at row % 32 times 16 bytes, row / 32 times 4
-        const uint32_t f = smem_u32(sf + slot * kScales) + (v ? 16 * lane : ((4 * lane) & 31) * 16 + ((4 * lane) >> 5) * 4);
-        if (v) {
-          copy_async16(f, s);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) copy_async4(f + 16 * i, s + 4 * i);
+      // first row of the group (below 2^31), -1 when no row of the queries sees it
+      const bool seen = lane < kGroups * kBatch && tok < hi && tok + 16 > lo;
+      const int row = seen ? ((pid * a.Hkv + hk) << a.log2P) + (tok & mask) : -1;
+      const uint32_t all = __ballot_sync(0xFFFFFFFFu, seen);
+      tok += 16 * kGroups * kBatch;
+      pid = page(tok);
+#pragma unroll 1
+      for (int i = 0; i < kBatch && k + i < t1; ++i) {
+        const int group = lane - kGroups * i;  // of this tile, where it is 0 .. 6
+        const int srow = __shfl_sync(0xFFFFFFFFu, row, min(kGroups * i + part, 31));
+        uint64_t* bar = full + slot;
+        if (!wait(c, empty + slot, phase ^ 1u, 3u)) return false;
+        fence_proxy_async_shared();
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc((all >> (kGroups * i)) & ((1u << kGroups) - 1u)) * 16u * kD);
+        __syncwarp();
+        if (group >= 0 && group < kGroups && row >= 0) {
+          uint8_t* d = codes + slot * kCodes + group * 16 * kD;
+          if (v)
+            bulk_load_plain(d, a.vc + static_cast<size_t>(row) * kD, 16 * kD, bar);
+          else
+            tma_load_plain(d, &a.tm_k, bar, 0, row);
         }
+        if (part < kGroups && srow >= 0) {
+          const uint8_t* s = scales + static_cast<size_t>(srow + in) * (kD / 32);
+          const uint32_t d = smem_u32(sf + slot * kScales) + sdst;
+          if (v) {
+            copy_async16(d, s);
+          } else {  // token 4 lane + i at row % 32 times 16 bytes, row / 32 times 4
+#pragma unroll
+            for (int j = 0; j < 4; ++j) copy_async4(d + 16 * j, s + 4 * j);
+          }
+        }
+        copy_async_arrive(bar);
+        if (++slot == stages) slot = 0, phase ^= 1u;
       }
-      copy_async_arrive(bar);
-      if (++slot == stages) slot = 0, phase ^= 1u;
     }
     return true;
   }
@@ -343,7 +333,7 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, const uint8_t* 
   raw += r0 * kD + 16 * piece, sc += 4 * r0 + (piece >> 1);
   uint4 next = *reinterpret_cast<const uint4*>(raw);
   uint32_t snext = *sc;
-#pragma unroll 1
+#pragma unroll 2
   for (int i = 0; i < kPasses; ++i) {
     const uint4 x = next;
     const uint32_t s = snext;
@@ -438,14 +428,14 @@ __device__ __forceinline__ void mask_cols(float (&s)[n], int col0, int from, int
     if (col0 + i < from || col0 + i >= upto) s[i] = -INFINITY;
 }
 template <int n>
-__device__ __forceinline__ float max_cols(const float (&s)[n], float m) {
-  float m1 = max3(s[0], s[1], m), m2 = max3(s[2], s[3], s[4]);
+__device__ __forceinline__ float max_cols(const float (&s)[n]) {
+  float m1 = s[0], m2 = s[1];
 #pragma unroll
-  for (int i = 5; i + 3 < n; i += 4) {
+  for (int i = 2; i + 3 < n; i += 4) {
     m1 = max3(m1, s[i], s[i + 1]);
     m2 = max3(m2, s[i + 2], s[i + 3]);
   }
-  return max3(m1, m2, fmaxf(s[n - 3], fmaxf(s[n - 2], s[n - 1])));
+  return max3(m1, fmaxf(m2, s[n - 2]), s[n - 1]);
 }
 // p = 2^(s * scale - ms) as bf16 pairs; the sum of p joins `sum`.
 template <int n>
@@ -459,65 +449,64 @@ __device__ __forceinline__ void exp_cols(const float (&s)[n], float scale, float
     p[i] = bf16x2_rn(x.x, x.y);
   }
 }
-// One key tile of the thread's row; from / upto: the tile's columns that it
-// sees.  `half`: the barrier that hands the first 64 probabilities to the
-// products, before the others are computed.
-__device__ __forceinline__ void softmax_tile(const ChunkArgs& a, uint32_t S, uint32_t O, bool masked, int from, int upto,
-                                             bool first, RowState& st, uint64_t* half, int lane) {
-  float x0[32], x1[32], x2[32], x3[16];
+// Section u of a key tile (64 or 48 columns at S + 64 u) of the thread's row;
+// from / upto: the section's columns that it sees.  `busy`: the barrier that
+// says that the products before are done with the outputs.
+__device__ __forceinline__ bool softmax_section(const Ctx& c, uint32_t S, uint32_t O, int u, bool masked, int from, int upto,
+                                                bool first, RowState& st, uint64_t* busy, uint32_t busy_phase) {
+  const float scale = c.a.scale_log2;
+  float x0[32], x1[16], x2[16];
   tmem_ld32(S, x0);
-  tmem_ld32(S + 32, x1);
-  tmem_ld32(S + 64, x2);
-  tmem_ld16f(S + 96, x3);
-  tmem_ld_wait();
-  if (masked) {
-    mask_cols(x0, 0, from, upto), mask_cols(x1, 32, from, upto);
-    mask_cols(x2, 64, from, upto), mask_cols(x3, 96, from, upto);
+  tmem_ld16f(S + 32, x1);
+  if (u == 0) {
+    tmem_ld16f(S + 48, x2);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x2[i] = -INFINITY;
   }
-  const float mx = fmaxf(max3(max_cols(x0, -INFINITY), max_cols(x1, -INFINITY), max_cols(x2, -INFINITY)),
-                         max_cols(x3, -INFINITY)) * a.scale_log2;
+  tmem_ld_wait();
+  if (masked) mask_cols(x0, 0, from, upto), mask_cols(x1, 32, from, upto), mask_cols(x2, 48, from, upto);
+  const float mx = max3(max_cols(x0), max_cols(x1), max_cols(x2)) * scale;
   float al = 1.f;
   if (mx > st.m + kGrow || st.m == -INFINITY) {
     const float mn = fmaxf(st.m, mx);
     al = mn == -INFINITY ? 1.f : exp2_fast(st.m - mn);
     st.m = mn;
   }
-  if (!first && __any_sync(0xFFFFFFFFu, al != 1.f)) {
-    // the outputs so far in the new unit (the scores' arrival says that their products are done)
+  if (!first && __any_sync(0xFFFFFFFFu, al != 1.f)) {  // the outputs so far in the new unit
+    if (!wait(c, busy, busy_phase, 11u)) return false;
+    tc_fence_after();
     float o[16];
 #pragma unroll 1
-    for (int c = 0; c < kD; c += 16) {
-      tmem_ld16f(O + c, o);
+    for (int col = 0; col < kD; col += 16) {
+      tmem_ld16f(O + col, o);
       tmem_ld_wait();
-      uint32_t u[16];
+      uint32_t v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * al);
-      tmem_st16(O + c, u);
+      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(o[i] * al);
+      tmem_st16(O + col, v);
     }
   }
   const float ms = st.m == -INFINITY ? 0.f : st.m;
   float2 sum = make_float2(0.f, 0.f), sum1 = sum;
   // the probabilities take the scores' place (all of them are in registers)
-  uint32_t p[16];
-  exp_cols(x0, a.scale_log2, ms, sum, p);
-  tmem_st16(S, p);
-  exp_cols(x1, a.scale_log2, ms, sum1, p);
-  tmem_st16(S + 16, p);
-  tmem_st_wait();
-  tc_fence_before();
-  warp_arrive(half, lane);
-  exp_cols(x2, a.scale_log2, ms, sum, p);
-  tmem_st16(S + 32, p);
-  uint32_t p3[8];
-  exp_cols(x3, a.scale_log2, ms, sum1, p3);
-  tmem_st8(S + 48, p3);
+  uint32_t p0[16], p1[8];
+  exp_cols(x0, scale, ms, sum, p0);
+  tmem_st16(S, p0);
+  exp_cols(x1, scale, ms, sum1, p1);
+  tmem_st8(S + 16, p1);
+  if (u == 0) {
+    exp_cols(x2, scale, ms, sum1, p1);
+    tmem_st8(S + 24, p1);
+  }
   st.l = fmaf(st.l, al, (sum.x + sum.y) + (sum1.x + sum1.y));
   tmem_st_wait();
+  return true;
 }
 
 // The parts of `rows` (at most 32) rows of the tile from row0 on added up by a
 // warp, always in the blocks' order: lane = row for the maxima, sums and
-// factors, then eight rows at a time, four columns a lane.
+// factors, then four rows at a time, four columns a lane.
 __device__ __forceinline__ void merge_rows(const ChunkArgs& a, const Item& w, const chunk::Ranges& rg, int row0, int rows,
                                            int lane) {
   const int own = row0 + min(lane, rows - 1);
@@ -536,24 +525,24 @@ __device__ __forceinline__ void merge_rows(const ChunkArgs& a, const Item& w, co
     if (sl >= 0) M = fmaxf(M, __ldcg(&a.rec_ml[static_cast<size_t>(sl) * a.slot_rows + own].x));
   }
   float den = 0.f;
-  for (int g = 0; g < rows; g += 8) {
-    float4 acc[8];
+  for (int g = 0; g < rows; g += 4) {
+    float4 acc[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
     for (int p = 0; p < blocks; ++p) {
       const int sl = slot_of(p);
       if (sl < 0) continue;
       const float2 ml = __ldcg(&a.rec_ml[static_cast<size_t>(sl) * a.slot_rows + own]);
       const float4* src = reinterpret_cast<const float4*>(a.rec + (static_cast<size_t>(sl) * a.slot_rows + row0 + g) * kD) + lane;
-      float4 v[8];
+      float4 v[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 4; ++i)
         if (g + i < rows) v[i] = __ldcg(src + i * (kD / 4));
       const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
       if (g == 0) den = fmaf(f, ml.y, den);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 4; ++i)
         if (g + i < rows) {
           const float x = __shfl_sync(0xFFFFFFFFu, f, g + i);
           acc[i].x = fmaf(x, v[i].x, acc[i].x), acc[i].y = fmaf(x, v[i].y, acc[i].y);
@@ -561,7 +550,7 @@ __device__ __forceinline__ void merge_rows(const ChunkArgs& a, const Item& w, co
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       if (g + i >= rows) break;
       const float d = __shfl_sync(0xFFFFFFFFu, den, g + i), inv = d > 0.f ? 1.f / d : 0.f;
       const int rr = w.r0 + row0 + g + i, tok = rr / a.G;
@@ -595,9 +584,12 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->v_full[i], kConvWarps);
       mbar_init(&ctl->v_empty[i], 2);
-      mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->p_half[i], 4);
-      mbar_init(&ctl->p_full[i], 4);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        mbar_init(&ctl->s_full[i][u], 1);
+        mbar_init(&ctl->p_full[i][u], 4);
+      }
+      mbar_init(&ctl->o_first[i], 1);
       mbar_init(&ctl->o_done[i], 1);
       mbar_init(&ctl->fin[i], 1);
       mbar_init(&ctl->group[i], 4);
@@ -616,12 +608,11 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     tmem_relinquish();
   }
   const long long units = chunk::all_units(a, qs, rs, ctl->red);  // a block-wide barrier inside
+  if (t == 0) ctl->ranges.make(units, a.grid);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-  chunk::Ranges ranges;
-  ranges.make(units, a.grid);
   // the shared memory starts on a swizzle atom (checked, as all offsets rely on it)
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (t == 0) {
@@ -630,7 +621,6 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     }
     __syncthreads();
   } else if (warp >= kMmaWarp) {
-   reg_dec<kRestRegs>();
    if (warp >= kLoadWarp) {
     // ---- codes and scales into the rings; the first of the two walks the plan
     Loader ld;
@@ -642,7 +632,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     chunk::Walk walk;
     if (!ld.v) {
       if (lane == 0) tma_prefetch_desc(&a.tm_k);
-      walk.init(a, ranges, blockIdx.x, qs, rs, lane);
+      walk.init(a, ctl->ranges, blockIdx.x, qs, rs, lane);
     }
     Ring<2> it;
 #pragma unroll 1
@@ -713,59 +703,71 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         }
         return true;
       };
-      auto scores = [&](int j) -> bool {
-        if (!skip_k(j) || !wait(c, &ctl->k_full[kr.slot], kr.phase, 6u)) return false;
-        fence_proxy_async_shared();  // the scales came by generic copies
+      // section u of tile j's scores; the first one brings K's scales
+      auto scores = [&](int j, int u) -> bool {
+        if (u == 0) {
+          if (!skip_k(j) || !wait(c, &ctl->k_full[kr.slot], kr.phase, 6u)) return false;
+          fence_proxy_async_shared();  // the scales came by generic copies
+          odd ^= 1u;
+        }
         tc_fence_after();
-        const uint64_t k0 = dk + kr.slot * (kCodes >> 4);
-        const uint32_t sfk = tmem + kColSfk + 8 * m + 4 * odd;
+        const uint64_t k0 = dk + kr.slot * (kCodes >> 4) + u * (kFirst * kD >> 4);
+        const uint32_t sfk = tmem + kColSfk + 8 * m + 4 * odd, d = S + kFirst * u;
+        const uint32_t idesc = idesc_mxf8_e4m3(0, 0, 0) | (((u ? kKeys - kFirst : kFirst) >> 3) << 17);
         if (elect_one()) {
-          tc_cp_32x128b_warpx4(sfk, dsk + kr.slot * (kScales >> 4));
+          if (u == 0) tc_cp_32x128b_warpx4(sfk, dsk + kr.slot * (kScales >> 4));
 #pragma unroll
           for (int k = 0; k < 8; ++k) {  // step k / 2 of 32 dimensions, term k % 2
             const uint32_t o = (32 * (k >> 1)) >> 4;
-            tc_mma_mxf8(S, dq + (k & 1) * (kQCodes >> 4) + o, k0 + o, idesc_mxf8_e4m3(kKeys, k >> 1, k >> 1),
-                        sfq + 4 * (k & 1), sfk, k > 0);
+            tc_mma_mxf8(d, dq + (k & 1) * (kQCodes >> 4) + o, k0 + o, idesc | ((k >> 1) << 4) | ((k >> 1) << 29),
+                        sfq + 4 * (k & 1), sfk + 2 * u, k > 0);
           }
-          tc_commit(&ctl->s_full[m]);
-          tc_commit(&ctl->k_empty[kr.slot]);
-          if (j == last) tc_commit(&ctl->q_free);
+          tc_commit(&ctl->s_full[m][u]);
+          if (u) {
+            tc_commit(&ctl->k_empty[kr.slot]);
+            if (j == last) tc_commit(&ctl->q_free);
+          }
         }
         __syncwarp();
-        kr.step();
-        ++kt;
-        odd ^= 1u;
+        if (u) {
+          kr.step();
+          ++kt;
+        }
         return true;
       };
       bool ok = true;
       if (begin <= last)
-        ok = scores(begin);
+        ok = scores(begin, 0) && scores(begin, 1);
       else if (lane == 0)
         mbar_arrive(&ctl->q_free);
+#pragma unroll 1
       for (int j = begin; ok && j <= last; j += step) {
-        ok = skip_v(j) && wait(c, &ctl->v_full[vr.slot], vr.phase, 7u) && wait(c, &ctl->p_half[m], p_phase, 8u);
-        if (!ok) break;
-        tc_fence_after();
+        ok = skip_v(j) && wait(c, &ctl->v_full[vr.slot], vr.phase, 7u);
         const uint64_t v0 = dv + vr.slot * (kOperand >> 4);
-        if (elect_one()) {
+#pragma unroll 1
+        for (int u = 0; ok && u < 2; ++u) {
+          ok = wait(c, &ctl->p_full[m][u], p_phase, 8u);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vu = v0 + u * (kFirst * 128 >> 4);
+          const uint32_t p = S + kFirst * u;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_ts(O, S + 8 * k, v0 + k * (2048 >> 4), kIdescPv, (j > begin || k > 0) ? 1u : 0u);
+            for (int k = 0; k < 3; ++k) mma_ts(O, p + 8 * k, vu + k * (2048 >> 4), kIdescPv, (j > begin || u > 0 || k > 0) ? 1u : 0u);
+            if (u == 0) {
+              mma_ts(O, p + 24, vu + 3 * (2048 >> 4), kIdescPv, 1u);
+              tc_commit(&ctl->o_first[m]);
+            } else {
+              tc_commit(&ctl->v_empty[vr.slot]);
+              if (j == last) tc_commit(&ctl->o_done[m]);
+            }
+          }
+          __syncwarp();
+          if (j < last) ok = scores(j + step, u);
         }
-        __syncwarp();
-        ok = wait(c, &ctl->p_full[m], p_phase, 9u);
-        if (!ok) break;
         p_phase ^= 1u;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 4; k < kKeys / 16; ++k) mma_ts(O, S + 8 * k, v0 + k * (2048 >> 4), kIdescPv, 1u);
-          tc_commit(&ctl->v_empty[vr.slot]);
-          if (j == last) tc_commit(&ctl->o_done[m]);
-        }
-        __syncwarp();
         vr.step();
         ++vt;
-        if (j < last) ok = scores(j + step);
       }
       ok = ok && skip_k(tiles) && skip_v(tiles);
       if (!ok) break;
@@ -780,7 +782,6 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
    }
   } else if (warp >= kSoftWarps) {
     // ---- codes to bf16
-    reg_dec<kConvRegs>();
     const int ct = t - 32 * kSoftWarps;
     Ring<2> it;
     Ring<NV> ring;
@@ -808,55 +809,60 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     }
   } else {
     // ---- softmax: stream m, a thread a row
-    reg_inc<kSoftRegs>();
     const int m = warp >> 2, wl = warp & 3, row = 32 * wl + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
-    const uint32_t S = tmem + lanes + m * kColS, O = tmem + lanes + kColO + m * 128;
-    Ring<2> it;
-    uint32_t s_phase = 0, o_phase = 0, g_phase = 0, x_phase = 0, f_phase = 0;
+    const uint32_t S = tmem + lanes + m * kColS;  // (the outputs are kColO further)
     // the queries of the item in a slot, when the products are done with the last ones
     auto queries = [&](int slot) {
       const Item& w = ctl->item[slot];
       if (w.t0 == w.t1) return;
-      if (w.rows > 128)
-        load_queries(a, w, w.r0 + 128 * m, smem + L::q + m * 2 * kQCodes, smem + L::sfq + m * 2 * kScales, 0, 128,
-                     wl, lane);
-      else
-        load_queries(a, w, w.r0, smem + L::q, smem + L::sfq, 64 * m, 64, wl, lane);
+      const bool pair = w.rows > 128;
+      load_queries(a, w, w.r0 + (pair ? 128 * m : 0), smem + L::q + (pair ? m * 2 * kQCodes : 0),
+                   smem + L::sfq + (pair ? m * 2 * kScales : 0), pair ? 0 : 64 * m, pair ? 128 : 64, wl, lane);
       fence_proxy_async_shared();
       warp_arrive(&ctl->q_full, lane);
     };
+    Ring<2> it;
+    uint32_t s_phase = 0, o_phase = 0, g_phase = 0, x_phase = 0, f_phase = 0;
     bool ok = wait(c, &ctl->it_full[0], 0, 4u);
     if (ok) queries(0);
+    // (what an item's end needs is read again there, to keep the loop's registers few)
+#pragma unroll 1
     while (ok) {
-      const Item& w = ctl->item[it.slot];  // given back at the item's end
-      if (w.t0 == w.t1) break;
-      const bool pair = w.rows > 128;
-      const int tr = (pair ? 128 * m : 0) + row;  // row in the tile
-      const int rr = w.r0 + min(tr, w.rows - 1), tok = rr / a.G;
-      const int pos = w.len - w.n + tok;
-      const bool busy = (pair ? 128 * m : 0) + 32 * wl < w.rows;  // the warp has a row
-      // the warp's rows see all of a tile between these tokens
-      const int see_lo = a.window > 0 ? __reduce_max_sync(0xFFFFFFFFu, pos) - a.window + 1 : 0;
-      const int see_hi = __reduce_min_sync(0xFFFFFFFFu, pos) + 1;
-      const int mine = a.window > 0 ? pos - a.window + 1 : 0;
       RowState st{-INFINITY, 0.f};
-      const int step = pair ? 1 : 2, t1 = w.t1;
-      int k = w.t0 + (pair ? 0 : m);
-      const bool any = k < t1;
-      for (bool first = true; k < t1; k += step, first = false) {
-        ok = wait(c, &ctl->s_full[m], s_phase, 10u);
-        if (!ok) break;
-        s_phase ^= 1u;
-        tc_fence_after();
-        const int tok0 = k * kKeys;
-        if (busy)
-          softmax_tile(a, S, O, tok0 < see_lo || tok0 + kKeys > see_hi, mine - tok0, pos + 1 - tok0, first, st,
-                       &ctl->p_half[m], lane);
-        else
-          warp_arrive(&ctl->p_half[m], lane);
-        tc_fence_before();
-        warp_arrive(&ctl->p_full[m], lane);
+      bool any;
+      {
+        const Item& w = ctl->item[it.slot];  // given back at the item's end
+        if (w.t0 == w.t1) break;
+        const bool pair = w.rows > 128;
+        const int rr = w.r0 + min((pair ? 128 * m : 0) + row, w.rows - 1);
+        // the row sees the tokens from .. upto - 1, the warp's rows all of those lo .. hi - 1
+        const int upto = w.len - w.n + rr / a.G + 1, from = a.window > 0 ? upto - a.window : 0;
+        const int lo = __reduce_max_sync(0xFFFFFFFFu, from), hi = __reduce_min_sync(0xFFFFFFFFu, upto);
+        const bool busy = (pair ? 128 * m : 0) + 32 * wl < w.rows;  // the warp has a row
+        const int step = pair ? 1 : 2, t1 = w.t1;
+        int k = w.t0 + (pair ? 0 : m);
+        any = k < t1;
+#pragma unroll 1
+        for (bool first = true; k < t1; k += step, first = false) {
+#pragma unroll 1
+          for (int u = 0; u < 2; ++u) {
+            ok = wait(c, &ctl->s_full[m][u], s_phase, 10u);
+            if (!ok) break;
+            tc_fence_after();
+            const int tok0 = k * kKeys + kFirst * u, n = u ? kKeys - kFirst : kFirst;
+            // before the first section, the tile before is done when this tile's
+            // second scores are there; before the second, the first's products
+            if (busy)
+              ok = softmax_section(c, S + kFirst * u, S + kColO, u, tok0 < lo || tok0 + n > hi, from - tok0, upto - tok0,
+                                   first && u == 0, st, u ? &ctl->o_first[m] : &ctl->s_full[m][1], s_phase);
+            if (!ok) break;
+            tc_fence_before();
+            warp_arrive(&ctl->p_full[m][u], lane);
+          }
+          if (!ok) break;
+          s_phase ^= 1u;
+        }
       }
       // the next item's queries go in under this one's end
       ok = ok && wait(c, &ctl->q_free, f_phase, 5u);
@@ -873,6 +879,10 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         o_phase ^= 1u;
         tc_fence_after();
       }
+      const Item& w = ctl->item[slot];
+      const bool pair = w.rows > 128;
+      const int tr = (pair ? 128 * m : 0) + row;                  // row in the tile
+      const bool busy = tr - lane < w.rows, write = tr < w.rows;  // of the warp, of the thread
       float f0 = 1.f, f1 = 0.f;  // the streams' shares of the row's output
       if (!pair) {
         // the second stream's maximum and sum to the first, which adds both up
@@ -882,58 +892,57 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         } else {
           ok = wait(c, &ctl->second, x_phase, 12u);
           if (!ok) break;
-          const float2 ml = ctl->ml[row];
-          const float M = fmaxf(st.m, ml.x);
+          const float m1 = ctl->ml[row].x, l1 = ctl->ml[row].y, M = fmaxf(st.m, m1);
           f0 = st.m == -INFINITY ? 0.f : exp2_fast(st.m - M);
-          f1 = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
-          st.l = f0 * st.l + f1 * ml.y;
+          f1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - M);
+          st.l = f0 * st.l + f1 * l1;
           st.m = M;
           tc_fence_after();
         }
       }
       if (pair || m == 0) {
-        const bool two = !pair && t1 - w.t0 > 1, whole = w.whole;
-        const bool write = tr < w.rows;
-        const int part = whole ? 0 : chunk::part_slot(w, ranges, blockIdx.x);
+        const bool two = !pair && w.t1 - w.t0 > 1, whole = w.whole;
+        float* rec = nullptr;
+        uint16_t* y = nullptr;
         if (whole) {
           const float inv = st.l > 0.f ? 1.f / st.l : 0.f;
           f0 *= inv, f1 *= inv;
+          const int rr = w.r0 + min(tr, w.rows - 1), tok = rr / a.G;
+          y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
+        } else {
+          const size_t r = static_cast<size_t>(chunk::part_slot(w, ctl->ranges, blockIdx.x)) * a.slot_rows + min(tr, w.rows - 1);
+          rec = a.rec + r * kD;
+          if (write) a.rec_ml[r] = make_float2(st.m, st.l);
         }
-        uint16_t* y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
-        const size_t rec = static_cast<size_t>(part) * a.slot_rows + min(tr, w.rows - 1);
         if (busy) {
 #pragma unroll 1
-          for (int col = 0; col < kD; col += 32) {
-            float o[32];
-            tmem_ld32(O + col, o);
+          for (int col = 0; col < kD; col += 16) {
+            float o[16];
+            tmem_ld16f(S + kColO + col, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = f0 != 0.f ? f0 * o[i] : 0.f;
+            for (int i = 0; i < 16; ++i) o[i] = f0 != 0.f ? f0 * o[i] : 0.f;
             if (two) {
+              float o1[16];
+              tmem_ld16f(S + kColO + 128 + col, o1);
+              tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 32; j += 16) {
-                float o1[16];
-                tmem_ld16f(O + 128 + col + j, o1);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[j + i] += f1 != 0.f ? f1 * o1[i] : 0.f;
-              }
+              for (int i = 0; i < 16; ++i) o[i] += f1 != 0.f ? f1 * o1[i] : 0.f;
             }
             if (write) {
               if (whole) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 8)
+                for (int i = 0; i < 16; i += 8)
                   *reinterpret_cast<uint4*>(y + col + i) =
                       make_uint4(bf16x2_rn(o[i], o[i + 2]), bf16x2_rn(o[i + 1], o[i + 3]),
                                  bf16x2_rn(o[i + 4], o[i + 6]), bf16x2_rn(o[i + 5], o[i + 7]));
               } else {
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                  *reinterpret_cast<float4*>(a.rec + rec * kD + col + i) = make_float4(o[i], o[i + 2], o[i + 1], o[i + 3]);
+                for (int i = 0; i < 16; i += 4)
+                  *reinterpret_cast<float4*>(rec + col + i) = make_float4(o[i], o[i + 2], o[i + 1], o[i + 3]);
               }
             }
           }
-          if (!whole && write) a.rec_ml[rec] = make_float2(st.m, st.l);
         }
         tc_fence_before();
         if (!whole) {
@@ -956,8 +965,8 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
           g_phase ^= 1u;
           if (ctl->last[m]) {
             const int base = pair ? 128 * m : 0, rows = min(128, w.rows - base), each = (rows + 3) / 4;
-            const int mine_rows = min(each, rows - wl * each);
-            if (mine_rows > 0) merge_rows(a, w, ranges, base + wl * each, mine_rows, lane);
+            const int mine = min(each, rows - wl * each);
+            if (mine > 0) merge_rows(a, w, ctl->ranges, base + wl * each, mine, lane);
           }
         }
       }
