@@ -703,71 +703,76 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         }
         return true;
       };
-      // section u of tile j's scores; the first one brings K's scales
-      auto scores = [&](int j, int u) -> bool {
-        if (u == 0) {
-          if (!skip_k(j) || !wait(c, &ctl->k_full[kr.slot], kr.phase, 6u)) return false;
-          fence_proxy_async_shared();  // the scales came by generic copies
-          odd ^= 1u;
-        }
-        tc_fence_after();
+      // a tile's K and its scales are there
+      auto keys = [&](int j) -> bool {
+        if (!skip_k(j) || !wait(c, &ctl->k_full[kr.slot], kr.phase, 6u)) return false;
+        fence_proxy_async_shared();  // the scales came by generic copies
+        odd ^= 1u;
+        return true;
+      };
+      // (by one lane) section u of a tile's scores; the first one brings K's scales
+      auto scores = [&](int u, bool end) {
         const uint64_t k0 = dk + kr.slot * (kCodes >> 4) + u * (kFirst * kD >> 4);
         const uint32_t sfk = tmem + kColSfk + 8 * m + 4 * odd, d = S + kFirst * u;
         const uint32_t idesc = idesc_mxf8_e4m3(0, 0, 0) | (((u ? kKeys - kFirst : kFirst) >> 3) << 17);
-        if (elect_one()) {
-          if (u == 0) tc_cp_32x128b_warpx4(sfk, dsk + kr.slot * (kScales >> 4));
+        if (u == 0) tc_cp_32x128b_warpx4(sfk, dsk + kr.slot * (kScales >> 4));
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {  // step k / 2 of 32 dimensions, term k % 2
-            const uint32_t o = (32 * (k >> 1)) >> 4;
-            tc_mma_mxf8(d, dq + (k & 1) * (kQCodes >> 4) + o, k0 + o, idesc | ((k >> 1) << 4) | ((k >> 1) << 29),
-                        sfq + 4 * (k & 1), sfk + 2 * u, k > 0);
-          }
-          tc_commit(&ctl->s_full[m][u]);
-          if (u) {
-            tc_commit(&ctl->k_empty[kr.slot]);
-            if (j == last) tc_commit(&ctl->q_free);
-          }
+        for (int k = 0; k < 8; ++k) {  // step k / 2 of 32 dimensions, term k % 2
+          const uint32_t o = (32 * (k >> 1)) >> 4;
+          tc_mma_mxf8(d, dq + (k & 1) * (kQCodes >> 4) + o, k0 + o, idesc | ((k >> 1) << 4) | ((k >> 1) << 29),
+                      sfq + 4 * (k & 1), sfk + 2 * u, k > 0);
         }
-        __syncwarp();
+        tc_commit(&ctl->s_full[m][u]);
         if (u) {
-          kr.step();
-          ++kt;
+          tc_commit(&ctl->k_empty[kr.slot]);
+          if (end) tc_commit(&ctl->q_free);
         }
-        return true;
       };
+      auto keys_done = [&]() {
+        kr.step();
+        ++kt;
+      };
+      // Tile j: what does not depend on the probabilities is waited for first;
+      // once they are there, their products and the next tile's scores go out
+      // in one piece.  (Tile begin - step has no probabilities.)
       bool ok = true;
-      if (begin <= last)
-        ok = scores(begin, 0) && scores(begin, 1);
-      else if (lane == 0)
-        mbar_arrive(&ctl->q_free);
+      if (begin > last && lane == 0) mbar_arrive(&ctl->q_free);
 #pragma unroll 1
-      for (int j = begin; ok && j <= last; j += step) {
-        ok = skip_v(j) && wait(c, &ctl->v_full[vr.slot], vr.phase, 7u);
+      for (int j = begin - step; ok && j <= last && begin <= last; j += step) {
+        const bool head = j < begin, more = j < last;
+        if (!head) ok = skip_v(j) && wait(c, &ctl->v_full[vr.slot], vr.phase, 7u);
+        if (ok && more) ok = keys(j + step);
         const uint64_t v0 = dv + vr.slot * (kOperand >> 4);
 #pragma unroll 1
         for (int u = 0; ok && u < 2; ++u) {
-          ok = wait(c, &ctl->p_full[m][u], p_phase, 8u);
+          if (!head) ok = wait(c, &ctl->p_full[m][u], p_phase, 8u);
           if (!ok) break;
           tc_fence_after();
           const uint64_t vu = v0 + u * (kFirst * 128 >> 4);
           const uint32_t p = S + kFirst * u;
           if (elect_one()) {
+            if (!head) {
 #pragma unroll
-            for (int k = 0; k < 3; ++k) mma_ts(O, p + 8 * k, vu + k * (2048 >> 4), kIdescPv, (j > begin || u > 0 || k > 0) ? 1u : 0u);
-            if (u == 0) {
-              mma_ts(O, p + 24, vu + 3 * (2048 >> 4), kIdescPv, 1u);
-              tc_commit(&ctl->o_first[m]);
-            } else {
-              tc_commit(&ctl->v_empty[vr.slot]);
-              if (j == last) tc_commit(&ctl->o_done[m]);
+              for (int k = 0; k < 3; ++k)
+                mma_ts(O, p + 8 * k, vu + k * (2048 >> 4), kIdescPv, (j > begin || u > 0 || k > 0) ? 1u : 0u);
+              if (u == 0) {
+                mma_ts(O, p + 24, vu + 3 * (2048 >> 4), kIdescPv, 1u);
+                if (!more) tc_commit(&ctl->o_first[m]);
+              } else {
+                tc_commit(&ctl->v_empty[vr.slot]);
+                if (!more) tc_commit(&ctl->o_done[m]);
+              }
             }
+            if (more) scores(u, j + step == last);
           }
           __syncwarp();
-          if (j < last) ok = scores(j + step, u);
         }
-        p_phase ^= 1u;
-        vr.step();
-        ++vt;
+        if (!head) {
+          p_phase ^= 1u;
+          vr.step();
+          ++vt;
+        }
+        if (more) keys_done();
       }
       ok = ok && skip_k(tiles) && skip_v(tiles);
       if (!ok) break;
@@ -851,11 +856,13 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
             if (!ok) break;
             tc_fence_after();
             const int tok0 = k * kKeys + kFirst * u, n = u ? kKeys - kFirst : kFirst;
-            // before the first section, the tile before is done when this tile's
-            // second scores are there; before the second, the first's products
+            // the products before a section are done when the scores issued after
+            // them are there: this tile's second ones, the next tile's first
+            const bool more = k + step < t1;
             if (busy)
               ok = softmax_section(c, S + kFirst * u, S + kColO, u, tok0 < lo || tok0 + n > hi, from - tok0, upto - tok0,
-                                   first && u == 0, st, u ? &ctl->o_first[m] : &ctl->s_full[m][1], s_phase);
+                                   first && u == 0, st, u == 0 ? &ctl->s_full[m][1] : more ? &ctl->s_full[m][0] : &ctl->o_first[m],
+                                   u == 0 ? s_phase : more ? s_phase ^ 1u : o_phase);
             if (!ok) break;
             tc_fence_before();
             warp_arrive(&ctl->p_full[m][u], lane);
