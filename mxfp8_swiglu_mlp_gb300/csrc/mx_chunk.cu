@@ -429,13 +429,14 @@ __device__ __forceinline__ void mask_cols(float (&s)[n], int col0, int from, int
 }
 template <int n>
 __device__ __forceinline__ float max_cols(const float (&s)[n]) {
-  float m1 = s[0], m2 = s[1];
+  float m[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-  for (int i = 2; i + 3 < n; i += 4) {
-    m1 = max3(m1, s[i], s[i + 1]);
-    m2 = max3(m2, s[i + 2], s[i + 3]);
-  }
-  return max3(m1, fmaxf(m2, s[n - 2]), s[n - 1]);
+  for (int i = 4; i + 7 < n; i += 8)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = max3(m[j], s[i + 2 * j], s[i + 2 * j + 1]);
+#pragma unroll
+  for (int i = n - 4; i < n; ++i) m[i & 3] = fmaxf(m[i & 3], s[i]);
+  return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 // p = 2^(s * scale - ms) as bf16 pairs; the sum of p joins `sum`.
 template <int n>
@@ -449,32 +450,30 @@ __device__ __forceinline__ void exp_cols(const float (&s)[n], float scale, float
     p[i] = bf16x2_rn(x.x, x.y);
   }
 }
-// Section u of a key tile (64 or 48 columns at S + 64 u) of the thread's row;
-// from / upto: the section's columns that it sees.  `busy`: the barrier that
-// says that the products before are done with the outputs.
-__device__ __forceinline__ bool softmax_section(const Ctx& c, uint32_t S, uint32_t O, int u, bool masked, int from, int upto,
-                                                bool first, RowState& st, uint64_t* busy, uint32_t busy_phase) {
+// Section u of a key tile (64 or 48 columns at S) of the thread's row; from /
+// upto: the section's columns that it sees.  `before`: the barrier that says
+// that the products before are done with the outputs.  (Few branches: each one
+// that the compiler takes for divergent costs as much as ten columns.)
+template <int u>
+__device__ __forceinline__ bool softmax_section(const Ctx& c, uint32_t S, uint32_t O, bool masked, int from, int upto,
+                                                bool first, RowState& st, uint64_t* before, uint32_t phase) {
+  constexpr int n1 = u == 0 ? 32 : 16;
   const float scale = c.a.scale_log2;
-  float x0[32], x1[16], x2[16];
+  float x0[32], x1[n1];
   tmem_ld32(S, x0);
-  tmem_ld16f(S + 32, x1);
-  if (u == 0) {
-    tmem_ld16f(S + 48, x2);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x2[i] = -INFINITY;
-  }
+  if constexpr (u == 0)
+    tmem_ld32(S + 32, x1);
+  else
+    tmem_ld16f(S + 32, x1);
   tmem_ld_wait();
-  if (masked) mask_cols(x0, 0, from, upto), mask_cols(x1, 32, from, upto), mask_cols(x2, 48, from, upto);
-  const float mx = max3(max_cols(x0), max_cols(x1), max_cols(x2)) * scale;
-  float al = 1.f;
-  if (mx > st.m + kGrow || st.m == -INFINITY) {
-    const float mn = fmaxf(st.m, mx);
-    al = mn == -INFINITY ? 1.f : exp2_fast(st.m - mn);
-    st.m = mn;
-  }
-  if (!first && __any_sync(0xFFFFFFFFu, al != 1.f)) {  // the outputs so far in the new unit
-    if (!wait(c, busy, busy_phase, 11u)) return false;
+  if (__any_sync(0xFFFFFFFFu, masked)) mask_cols(x0, 0, from, upto), mask_cols(x1, 32, from, upto);
+  const float mx = fmaxf(max_cols(x0), max_cols(x1)) * scale;
+  const float mo = st.m, mn = mx > mo + kGrow || mo == -INFINITY ? fmaxf(mo, mx) : mo;
+  const float ms = mn == -INFINITY ? 0.f : mn;
+  const float al = mn == mo ? 1.f : exp2_fast(mo - ms);
+  st.m = mn;
+  if (__any_sync(0xFFFFFFFFu, al != 1.f) && !first) {  // the outputs so far in the new unit
+    if (!wait(c, before, phase, 11u)) return false;
     tc_fence_after();
     float o[16];
 #pragma unroll 1
@@ -487,28 +486,34 @@ __device__ __forceinline__ bool softmax_section(const Ctx& c, uint32_t S, uint32
       tmem_st16(O + col, v);
     }
   }
-  const float ms = st.m == -INFINITY ? 0.f : st.m;
   float2 sum = make_float2(0.f, 0.f), sum1 = sum;
   // the probabilities take the scores' place (all of them are in registers)
-  uint32_t p0[16], p1[8];
+  uint32_t p0[16], p1[n1 / 2];
   exp_cols(x0, scale, ms, sum, p0);
   tmem_st16(S, p0);
   exp_cols(x1, scale, ms, sum1, p1);
-  tmem_st8(S + 16, p1);
-  if (u == 0) {
-    exp_cols(x2, scale, ms, sum1, p1);
-    tmem_st8(S + 24, p1);
-  }
+  if constexpr (u == 0)
+    tmem_st16(S + 16, p1);
+  else
+    tmem_st8(S + 16, p1);
   st.l = fmaf(st.l, al, (sum.x + sum.y) + (sum1.x + sum1.y));
   tmem_st_wait();
   return true;
 }
 
-// The parts of `rows` (at most 32) rows of the tile from row0 on added up by a
-// warp, always in the blocks' order: lane = row for the maxima, sums and
-// factors, then four rows at a time, four columns a lane.
+// 32 outputs (in the order of V's stored columns) times f to a row.
+__device__ __forceinline__ void put32(uint16_t* y, const float (&o)[32], float f) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    *reinterpret_cast<uint4*>(y + i) =
+        make_uint4(bf16x2_rn(o[i] * f, o[i + 2] * f), bf16x2_rn(o[i + 1] * f, o[i + 3] * f),
+                   bf16x2_rn(o[i + 4] * f, o[i + 6] * f), bf16x2_rn(o[i + 5] * f, o[i + 7] * f));
+}
+// Columns chunk * 32 .., chunk + step, .. of up to 32 rows of the tile (from row0
+// on, a lane a row) added up over the tile's parts, always in the blocks'
+// order.  The parts lie column by column, so that a warp reads whole lines.
 __device__ __forceinline__ void merge_rows(const ChunkArgs& a, const Item& w, const chunk::Ranges& rg, int row0, int rows,
-                                           int lane) {
+                                           int chunk, int step, int lane) {
   const int own = row0 + min(lane, rows - 1);
   const int blocks = w.last - w.first + 1;
   int slots = -1, from = -32;  // slots of the parts from .. from + 31, one a lane
@@ -524,40 +529,29 @@ __device__ __forceinline__ void merge_rows(const ChunkArgs& a, const Item& w, co
     const int sl = slot_of(p);
     if (sl >= 0) M = fmaxf(M, __ldcg(&a.rec_ml[static_cast<size_t>(sl) * a.slot_rows + own].x));
   }
-  float den = 0.f;
-  for (int g = 0; g < rows; g += 4) {
-    float4 acc[4];
+  const int rr = w.r0 + own, tok = rr / a.G;
+  uint16_t* y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
+#pragma unroll 1
+  for (; chunk < kD / 32; chunk += step) {
+    float o[32], den = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+#pragma unroll 1
     for (int p = 0; p < blocks; ++p) {
       const int sl = slot_of(p);
       if (sl < 0) continue;
+      const float* src = a.rec + (static_cast<size_t>(sl) * kD + 32 * chunk) * a.slot_rows + own;
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = __ldcg(src + static_cast<size_t>(i) * a.slot_rows);
       const float2 ml = __ldcg(&a.rec_ml[static_cast<size_t>(sl) * a.slot_rows + own]);
-      const float4* src = reinterpret_cast<const float4*>(a.rec + (static_cast<size_t>(sl) * a.slot_rows + row0 + g) * kD) + lane;
-      float4 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (g + i < rows) v[i] = __ldcg(src + i * (kD / 4));
       const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
-      if (g == 0) den = fmaf(f, ml.y, den);
+      den = fmaf(f, ml.y, den);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (g + i < rows) {
-          const float x = __shfl_sync(0xFFFFFFFFu, f, g + i);
-          acc[i].x = fmaf(x, v[i].x, acc[i].x), acc[i].y = fmaf(x, v[i].y, acc[i].y);
-          acc[i].z = fmaf(x, v[i].z, acc[i].z), acc[i].w = fmaf(x, v[i].w, acc[i].w);
-        }
+      for (int i = 0; i < 32; ++i) o[i] = fmaf(f, v[i], o[i]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (g + i >= rows) break;
-      const float d = __shfl_sync(0xFFFFFFFFu, den, g + i), inv = d > 0.f ? 1.f / d : 0.f;
-      const int rr = w.r0 + row0 + g + i, tok = rr / a.G;
-      uint16_t* y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
-      reinterpret_cast<uint2*>(y)[lane] =
-          make_uint2(bf16x2_rn(acc[i].x * inv, acc[i].y * inv), bf16x2_rn(acc[i].z * inv, acc[i].w * inv));
-    }
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    if (lane < rows) put32(y + 32 * chunk, o, inv);
   }
 }
 
@@ -587,7 +581,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         mbar_init(&ctl->s_full[i][u], 1);
-        mbar_init(&ctl->p_full[i][u], 4);
+        mbar_init(&ctl->p_full[i][u], 128);
       }
       mbar_init(&ctl->o_first[i], 1);
       mbar_init(&ctl->o_done[i], 1);
@@ -850,23 +844,26 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         any = k < t1;
 #pragma unroll 1
         for (bool first = true; k < t1; k += step, first = false) {
-#pragma unroll 1
-          for (int u = 0; u < 2; ++u) {
-            ok = wait(c, &ctl->s_full[m][u], s_phase, 10u);
-            if (!ok) break;
-            tc_fence_after();
-            const int tok0 = k * kKeys + kFirst * u, n = u ? kKeys - kFirst : kFirst;
-            // the products before a section are done when the scores issued after
-            // them are there: this tile's second ones, the next tile's first
-            const bool more = k + step < t1;
-            if (busy)
-              ok = softmax_section(c, S + kFirst * u, S + kColO, u, tok0 < lo || tok0 + n > hi, from - tok0, upto - tok0,
-                                   first && u == 0, st, u == 0 ? &ctl->s_full[m][1] : more ? &ctl->s_full[m][0] : &ctl->o_first[m],
-                                   u == 0 ? s_phase : more ? s_phase ^ 1u : o_phase);
-            if (!ok) break;
-            tc_fence_before();
-            warp_arrive(&ctl->p_full[m][u], lane);
-          }
+          const int tok0 = k * kKeys, tok1 = tok0 + kFirst;
+          // the products before a section are done when the scores issued after
+          // them are there: this tile's second ones, the next tile's first
+          ok = wait(c, &ctl->s_full[m][0], s_phase, 10u);
+          if (!ok) break;
+          tc_fence_after();
+          if (busy)
+            ok = softmax_section<0>(c, S, S + kColO, tok0 < lo || tok1 > hi, from - tok0, upto - tok0, first, st,
+                                    &ctl->s_full[m][1], s_phase);
+          tc_fence_before();
+          mbar_arrive(&ctl->p_full[m][0]);
+          ok = ok && wait(c, &ctl->s_full[m][1], s_phase, 10u);
+          if (!ok) break;
+          tc_fence_after();
+          const bool more = k + step < t1;
+          if (busy)
+            ok = softmax_section<1>(c, S + kFirst, S + kColO, tok1 < lo || tok0 + kKeys > hi, from - tok1, upto - tok1, false,
+                                    st, more ? &ctl->s_full[m][0] : &ctl->o_first[m], more ? s_phase ^ 1u : o_phase);
+          tc_fence_before();
+          mbar_arrive(&ctl->p_full[m][1]);
           if (!ok) break;
           s_phase ^= 1u;
         }
@@ -917,36 +914,31 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
           const int rr = w.r0 + min(tr, w.rows - 1), tok = rr / a.G;
           y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
         } else {
-          const size_t r = static_cast<size_t>(chunk::part_slot(w, ctl->ranges, blockIdx.x)) * a.slot_rows + min(tr, w.rows - 1);
-          rec = a.rec + r * kD;
-          if (write) a.rec_ml[r] = make_float2(st.m, st.l);
+          const size_t slot = chunk::part_slot(w, ctl->ranges, blockIdx.x);
+          rec = a.rec + slot * kD * a.slot_rows + min(tr, w.rows - 1);
+          if (write) a.rec_ml[slot * a.slot_rows + tr] = make_float2(st.m, st.l);
         }
         if (busy) {
 #pragma unroll 1
-          for (int col = 0; col < kD; col += 16) {
-            float o[16];
-            tmem_ld16f(S + kColO + col, o);
+          for (int col = 0; col < kD; col += 32) {
+            float o[32];
+            tmem_ld32(S + kColO + col, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = f0 != 0.f ? f0 * o[i] : 0.f;
+            for (int i = 0; i < 32; ++i) o[i] = f0 != 0.f ? f0 * o[i] : 0.f;
             if (two) {
-              float o1[16];
-              tmem_ld16f(S + kColO + 128 + col, o1);
+              float o1[32];
+              tmem_ld32(S + kColO + 128 + col, o1);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] += f1 != 0.f ? f1 * o1[i] : 0.f;
+              for (int i = 0; i < 32; ++i) o[i] += f1 != 0.f ? f1 * o1[i] : 0.f;
             }
             if (write) {
               if (whole) {
-#pragma unroll
-                for (int i = 0; i < 16; i += 8)
-                  *reinterpret_cast<uint4*>(y + col + i) =
-                      make_uint4(bf16x2_rn(o[i], o[i + 2]), bf16x2_rn(o[i + 1], o[i + 3]),
-                                 bf16x2_rn(o[i + 4], o[i + 6]), bf16x2_rn(o[i + 5], o[i + 7]));
+                put32(y + col, o, 1.f);
               } else {
 #pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                  *reinterpret_cast<float4*>(rec + col + i) = make_float4(o[i], o[i + 2], o[i + 1], o[i + 3]);
+                for (int i = 0; i < 32; ++i) rec[static_cast<size_t>(col + i) * a.slot_rows] = o[i];
               }
             }
           }
@@ -971,9 +963,11 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
           if (!ok) break;
           g_phase ^= 1u;
           if (ctl->last[m]) {
-            const int base = pair ? 128 * m : 0, rows = min(128, w.rows - base), each = (rows + 3) / 4;
-            const int mine = min(each, rows - wl * each);
-            if (mine > 0) merge_rows(a, w, ctl->ranges, base + wl * each, mine, lane);
+            // 32 rows a warp; with fewer groups of rows, the warps share their columns
+            const int base = pair ? 128 * m : 0, rows = min(128, w.rows - base), groups = (rows + 31) / 32;
+            const int g = wl % groups, step = 4 / groups;
+            if (wl / groups < step)
+              merge_rows(a, w, ctl->ranges, base + 32 * g, min(32, rows - 32 * g), wl / groups, step, lane);
           }
         }
       }

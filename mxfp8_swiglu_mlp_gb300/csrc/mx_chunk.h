@@ -23,7 +23,7 @@ struct ChunkArgs {
   const int32_t* lens;        // [B]
   uint32_t* status;           // first error (status << 24 | site << 16 | sequence)
   uint32_t* count;            // [2 * grid] parts of a query tile that have arrived (zero between calls)
-  float* rec;                 // [2 * grid][slot_rows][128] unnormalised outputs of parts
+  float* rec;                 // [2 * grid][128][slot_rows] unnormalised outputs of parts
   float2* rec_ml;             // [2 * grid][slot_rows] running maximum (base 2) and sum
   int slot_rows;
   int T, B, Hq, Hkv, G, log2P, num_pages, max_pages, window;
