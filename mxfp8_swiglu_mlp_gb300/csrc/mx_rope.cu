@@ -16,13 +16,17 @@
 // the fp32 product p * inv_freq is off by p * 2^-24 radians.
 //
 // Both kernels move each byte once and are bound by HBM (long inputs) or by
-// launch latency (a decode step).  A lane holds 16 consecutive elements of a
-// head (two 16-byte loads), so a group of D / 16 lanes holds the head: its
-// sum of squares takes log2(lanes) shuffles, the pair partner of a lane in
-// the half-split order is the lane R / 32 further, and a 32-element MXFP8
-// block is two lanes.  A warp keeps one token's sines and cosines in registers
-// over the heads it does.
+// launch latency (a decode step).  A lane holds two chunks of 8 consecutive
+// elements (16-byte loads) of a head, in the half-split order one from each
+// half: so a rotation's pairs are in one lane, D / 16 lanes hold a head, and
+// its sum of squares takes log2(lanes) shuffles.  A warp computes a token's
+// R / 2 sines and cosines once, one frequency a lane, hands them round through
+// shared memory and keeps its lanes' eight in registers over the token's
+// heads.  The turn fractions (fp64, whose rate is a small part of fp32's here)
+// are computed once a block, whose warps go on to further tokens.
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "mx_device.cuh"
 #include "mx_rope.h"
@@ -31,7 +35,8 @@ namespace fsops {
 
 namespace {
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeThreads = 128, kRopeBlocks = 6;  // blocks an SM: 80 registers a thread
+constexpr int kMaxRotary = 256;
 
 // Fraction of a turn per position, in units of 2^-64 turns.
 __device__ __forceinline__ long long turn_fraction(float inv_freq) {
@@ -47,136 +52,161 @@ __device__ __forceinline__ void turn_sincos(long long f, int p, float* sn, float
   sincospif(half, sn, cs);
 }
 
-// A lane's place and tables: lane `l` of the head's D / 16.  nf frequencies
-// (16 in the half-split order, 8 for adjacent pairs) as sn / cs; `rot` when
-// the lane's elements are rotated.
-struct LaneRope {
-  float sn[16], cs[16];  // adjacent pairs use the first 8
-  bool rot;
-  int partner;           // lane offset of the pair partner (half-split)
+// The block's turn fractions, a thread each.
+__device__ __forceinline__ void load_turns(long long* turns, const RopeArgs& a) {
+  for (int i = threadIdx.x; i < a.R / 2; i += kRopeThreads)
+    turns[i] = turn_fraction(__ldg(a.inv_freq + i));
+  __syncthreads();
+}
+
+// A lane's place in a head of D / 16 lanes: its chunks of 8 elements, and
+// whether they are rotated, by the frequencies 8 l .. 8 l + 7 either way.
+struct Place {
+  int c0, c1;  // first elements of the chunks
+  bool on, rot, split;
 };
-__device__ __forceinline__ void load_rope(LaneRope& r, const RopeArgs& a, int l, int pos) {
-  r.rot = 16 * l < a.R;
-  r.partner = 0;
-  if (!r.rot) return;
-  if (a.interleaved) {
+__device__ __forceinline__ Place lane_place(int l, int D, const RopeArgs& a) {
+  Place p;
+  p.split = !a.interleaved;
+  const int half = p.split ? a.R / 16 : 0;  // lanes with a chunk of each half
+  p.c0 = 8 * (l < half ? l : 2 * l);
+  p.c1 = 8 * (l < half ? l + half : 2 * l + 1);
+  p.on = 16 * l < D;
+  p.rot = 16 * l < a.R;
+  return p;
+}
+
+struct Angles {
+  float cs[8], sn[8];
+};
+// The token's angles, by the whole warp through its `tab`.
+__device__ __forceinline__ void token_angles(Angles& g, const long long* turns, const RopeArgs& a, const Place& p, int l,
+                                             int lane, int pos, float2* tab) {
+  if (a.R == 0) return;
+  __syncwarp();  // the last token's have been read
+#pragma unroll 1
+  for (int i = lane; i < a.R / 2; i += 32) {
+    float sn, cs;
+    turn_sincos(turns[i], pos, &sn, &cs);
+    tab[i] = make_float2(cs, sn);
+  }
+  __syncwarp();
+  if (p.rot) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) turn_sincos(turn_fraction(__ldg(a.inv_freq + 8 * l + i)), pos, &r.sn[i], &r.cs[i]);
-  } else {
-    const int h = a.R / 32;  // lanes of a half
-    const bool second = l >= h;
-    r.partner = second ? -h : h;
-    const int f0 = 16 * (second ? l - h : l);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      turn_sincos(turn_fraction(__ldg(a.inv_freq + f0 + i)), pos, &r.sn[i], &r.cs[i]);
-      if (!second) r.sn[i] = -r.sn[i];  // u' = u cos - w sin, w' = w cos + u sin
+    for (int i = 0; i < 4; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(tab + 8 * l)[i];
+      g.cs[2 * i] = x.x, g.sn[2 * i] = x.y, g.cs[2 * i + 1] = x.z, g.sn[2 * i + 1] = x.w;
     }
   }
 }
 
-// The lane's 16 elements (raw bf16) normed and rotated, in fp32.  gw / gp are
-// the gains of the lane's and of its partner's elements (bf16 pairs).  Every
+struct Raw {
+  uint4 a, b;
+};
+__device__ __forceinline__ Raw load_chunks(const uint16_t* head, const Place& p, bool on) {
+  Raw w;
+  w.a = w.b = make_uint4(0u, 0u, 0u, 0u);
+  if (on) {
+    w.a = *reinterpret_cast<const uint4*>(head + p.c0);
+    w.b = *reinterpret_cast<const uint4*>(head + p.c1);
+  }
+  return w;
+}
+__device__ __forceinline__ uint32_t word(const Raw& w, int i) {
+  const uint4& v = i < 4 ? w.a : w.b;
+  return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+}
+
+// The lane's 16 elements in fp32, normed with the gains gw and rotated.  Every
 // lane of the warp calls it; LPH lanes hold a head.
 template <int LPH>
-__device__ __forceinline__ void norm_rotate(const uint32_t (&w)[8], bool norm, const uint32_t (&gw)[8],
-                                            const uint32_t (&gp)[8], float inv_d, float eps, const LaneRope& r,
-                                            bool split, float (&v)[16]) {
-  float rn = 1.f;
+__device__ __forceinline__ void norm_rotate(const Raw& w, bool norm, const Raw& gw, float inv_d, float eps,
+                                            const Place& p, bool rot, const Angles& g, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[2 * i] = bf16_lo(word(w, i)), v[2 * i + 1] = bf16_hi(word(w, i));
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) ss = fmaf(v[i], v[i], ss);
+#pragma unroll
+  for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
   if (norm) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(bf16_lo(w[i]), bf16_lo(w[i]), fmaf(bf16_hi(w[i]), bf16_hi(w[i]), ss));
-#pragma unroll
-    for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-    rn = rsqrtf(fmaf(ss, inv_d, eps));
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
-    if (norm) {
-      v[2 * i] *= rn * bf16_lo(gw[i]);
-      v[2 * i + 1] *= rn * bf16_hi(gw[i]);
-    }
-  }
-  if (split) {
-    const int src = (threadIdx.x & 31) + r.partner;
+    const float rn = rsqrtf(fmaf(ss, inv_d, eps));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t pw = __shfl_sync(0xFFFFFFFFu, w[i], src);
-      if (r.rot) {
-        float p0 = bf16_lo(pw), p1 = bf16_hi(pw);
-        if (norm) {
-          p0 *= rn * bf16_lo(gp[i]);
-          p1 *= rn * bf16_hi(gp[i]);
-        }
-        v[2 * i] = fmaf(v[2 * i], r.cs[2 * i], p0 * r.sn[2 * i]);
-        v[2 * i + 1] = fmaf(v[2 * i + 1], r.cs[2 * i + 1], p1 * r.sn[2 * i + 1]);
-      }
+      v[2 * i] *= rn * bf16_lo(word(gw, i));
+      v[2 * i + 1] *= rn * bf16_hi(word(gw, i));
     }
-  } else if (r.rot) {
+  }
+  if (!rot) return;
+  if (p.split) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float u = v[i], x = v[8 + i];
+      v[i] = fmaf(u, g.cs[i], -x * g.sn[i]);
+      v[8 + i] = fmaf(x, g.cs[i], u * g.sn[i]);
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float u = v[2 * i], x = v[2 * i + 1];
-      v[2 * i] = fmaf(u, r.cs[i], -x * r.sn[i]);
-      v[2 * i + 1] = fmaf(x, r.cs[i], u * r.sn[i]);
+      v[2 * i] = fmaf(u, g.cs[i], -x * g.sn[i]);
+      v[2 * i + 1] = fmaf(x, g.cs[i], u * g.sn[i]);
     }
   }
 }
 
-__device__ __forceinline__ void load16(const uint16_t* p, bool on, uint32_t (&w)[8]) {
-  uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-  if (on) {
-    a = *reinterpret_cast<const uint4*>(p);
-    b = *reinterpret_cast<const uint4*>(p + 8);
-  }
-  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-  w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-}
 __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
-// Warp (token, part): heads of q (which = 0), then of k (which = 1), 32 / LPH
-// at a time; `parts` warps share a token's heads.
+// Unit (token, part): heads 0 .. of q then k, 32 / LPH a step; `parts` units
+// share a token's steps.  Each step's loads are issued a step ahead.
 template <int LPH>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int parts) {
-  constexpr int HW = 32 / LPH;  // heads of a warp step
-  const int lane = threadIdx.x & 31, l = lane % LPH, sub = lane / LPH;
-  const long long wid = static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  const int t = static_cast<int>(wid / parts), part = static_cast<int>(wid % parts);
-  if (t >= a.T) return;
-  const bool on = 16 * l < a.D;
-  LaneRope r;
-  load_rope(r, a.rope, on ? l : LPH * 1024, __ldg(a.positions + t));
-  const bool split = a.rope.R > 0 && !a.rope.interleaved;
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
+    norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int parts, int units) {
+  constexpr int HW = 32 / LPH;  // heads of a step
+  __shared__ __align__(16) float2 tab[kRopeThreads / 32][kMaxRotary / 2];
+  __shared__ long long turns[kMaxRotary / 2];
+  const int lane = threadIdx.x & 31, l = lane % LPH, sub = lane / LPH, warp = threadIdx.x >> 5;
+  const int warps = gridDim.x * (kRopeThreads / 32);
+  load_turns(turns, a.rope);
+  int u = blockIdx.x * (kRopeThreads / 32) + warp;
+  if (u >= units) return;
+  int pos = a.rope.R > 0 ? __ldg(a.positions + u / parts) : 0;
+  const Place p = lane_place(l, a.D, a.rope);
+  const int heads = a.H[0] + a.H[1], steps = (heads + HW - 1) / HW;
   const float inv_d = 1.f / static_cast<float>(a.D);
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const int steps = (a.H[which] + HW - 1) / HW;
-    if (steps == 0) continue;
-    const bool norm = a.gamma[which] != nullptr;
-    uint32_t gw[8], gp[8];
-    load16(a.gamma[which] + 16 * l, norm && on, gw);
-    load16(a.gamma[which] + 16 * (l + r.partner), norm && on, gp);
-    const uint16_t* x = a.x[which] + static_cast<long long>(t) * a.ldx[which] + 16 * l;
-    uint16_t* y = a.y[which] + static_cast<long long>(t) * a.ldy[which] + 16 * l;
+  const Raw gq = load_chunks(a.gamma[0], p, p.on && a.gamma[0] != nullptr);
+  const Raw gk = load_chunks(a.gamma[1], p, p.on && a.gamma[1] != nullptr);
+  for (; u < units; u += warps) {
+    const int t = u / parts, part = u % parts;
+    const uint16_t* q = a.x[0] + t * a.ldx[0];
+    const uint16_t* k = a.x[1] + t * a.ldx[1] - static_cast<long long>(a.H[0]) * a.D;
+    uint16_t* yq = a.y[0] + t * a.ldy[0];
+    uint16_t* yk = a.y[1] + t * a.ldy[1] - static_cast<long long>(a.H[0]) * a.D;
+    int h = part * HW + sub;
+    Raw w = load_chunks((h < a.H[0] ? q : k) + h * a.D, p, p.on && h < heads);
+    const int at = pos;
+    if (a.rope.R > 0 && u + warps < units) pos = __ldg(a.positions + (u + warps) / parts);
+    Angles g;
+    token_angles(g, turns, a.rope, p, l, lane, at, tab[warp]);
     for (int s = part; s < steps; s += parts) {
-      const int h = s * HW + sub;
-      const bool mine = on && h < a.H[which];
-      uint32_t w[8];
-      load16(x + h * a.D, mine, w);
+      const int hn = h + parts * HW;
+      const Raw next = load_chunks((hn < a.H[0] ? q : k) + hn * a.D, p, p.on && hn < heads);
+      const bool is_k = h >= a.H[0];
       float v[16];
-      norm_rotate<LPH>(w, norm, gw, gp, inv_d, a.eps, r, split, v);
-      if (mine) {
-        uint4* d = reinterpret_cast<uint4*>(y + h * a.D);
-        d[0] = make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
-        d[1] = make_uint4(bf16x2_rn(v[8], v[9]), bf16x2_rn(v[10], v[11]), bf16x2_rn(v[12], v[13]),
-                          bf16x2_rn(v[14], v[15]));
+      norm_rotate<LPH>(w, (is_k ? a.gamma[1] : a.gamma[0]) != nullptr, is_k ? gk : gq, inv_d, a.eps, p, p.rot, g, v);
+      if (p.on && h < heads) {
+        uint16_t* y = (is_k ? yk : yq) + h * a.D;
+        *reinterpret_cast<uint4*>(y + p.c0) =
+            make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+        *reinterpret_cast<uint4*>(y + p.c1) = make_uint4(bf16x2_rn(v[8], v[9]), bf16x2_rn(v[10], v[11]),
+                                                         bf16x2_rn(v[12], v[13]), bf16x2_rn(v[14], v[15]));
       }
+      w = next;
+      h = hn;
     }
   }
 }
@@ -202,89 +232,114 @@ __device__ __forceinline__ void report(uint32_t* status, uint32_t code, uint32_t
   atomicCAS(status, 0u, (code << 24) | (site << 16) | (static_cast<uint32_t>(b) & 0xFFFFu));
 }
 
-// Warp (token, part): the KV heads of k (which = 0), then of v.
-__global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(const __grid_constant__ KvAppendArgs a, int parts) {
-  constexpr int D = 128, LPH = 8, HW = 4;
-  const int lane = threadIdx.x & 31, l = lane % LPH, sub = lane / LPH;
-  const long long wid = static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  const int t = static_cast<int>(wid / parts), part = static_cast<int>(wid % parts);
-  if (t >= a.T) return;
+// Where a token goes: its row of head 0 in the cache (-1: nowhere).
+struct Slot {
+  long long row;
+  int pos;
+};
+__device__ __forceinline__ Slot find_slot(const KvAppendArgs& a, int t, int lane) {
+  Slot r;
+  r.row = -1;
+  r.pos = 0;
   const int b = find_sequence(a.cu, a.B, t, lane);
-  if (b < 0) return;  // a padding row
+  if (b < 0) return r;  // a padding row
   const int place = __ldg(a.lens + b) - (__ldg(a.cu + b + 1) - t);  // lens[b] - n + (t - cu[b])
   if (place < 0 || (place >> a.log2P) >= a.max_pages) {
     if (lane == 0) report(a.status, 1u, 1u, b);
-    return;
+    return r;
   }
   const int page = __ldg(a.table + static_cast<long long>(b) * a.max_pages + (place >> a.log2P));
   if (page < 0 || page >= a.num_pages) {
     if (lane == 0) report(a.status, 1u, 2u, b);
-    return;
+    return r;
   }
-  const int P = 1 << a.log2P, slot = place & (P - 1);
-  LaneRope r;
-  const int steps = (a.Hkv + HW - 1) / HW;
-  const bool split = a.rope.R > 0 && !a.rope.interleaved;
-  if (part < steps)
-    load_rope(r, a.rope, l, a.positions != nullptr ? __ldg(a.positions + t) : place);
-  else
-    r.rot = false, r.partner = 0;
-  const bool norm = a.gamma != nullptr;
-  uint32_t gw[8], gp[8];
-  load16(a.gamma + 16 * l, norm, gw);
-  load16(a.gamma + 16 * (l + r.partner), norm, gp);
-  for (int s = part; s < 2 * steps; s += parts) {
-    const int which = s >= steps, h = (which ? s - steps : s) * HW + sub;
-    const bool mine = h < a.Hkv;
-    uint32_t w[8];
-    load16(a.x[which] + static_cast<long long>(t) * a.ldx[which] + h * D + 16 * l, mine, w);
-    float v[16];
-    if (which == 0) {
-      norm_rotate<LPH>(w, norm, gw, gp, 1.f / D, a.eps, r, split, v);
-    } else {
+  r.row = ((static_cast<long long>(page) * a.Hkv) << a.log2P) + (place & ((1 << a.log2P) - 1));
+  r.pos = a.positions != nullptr ? __ldg(a.positions + t) : place;
+  return r;
+}
+
+// Unit (token, part): the KV heads of k, then of v, four a step.
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
+    kv_append_kernel(const __grid_constant__ KvAppendArgs a, int parts, int units) {
+  constexpr int D = 128, LPH = 8, HW = 4;
+  __shared__ __align__(16) float2 tab[kRopeThreads / 32][D / 2];
+  __shared__ long long turns[D / 2];
+  __shared__ __align__(16) float peak[kRopeThreads / 32][HW][D / 8];  // largest magnitude of each chunk
+  const int lane = threadIdx.x & 31, l = lane % LPH, sub = lane / LPH, warp = threadIdx.x >> 5;
+  const int warps = gridDim.x * (kRopeThreads / 32);
+  load_turns(turns, a.rope);
+  int u = blockIdx.x * (kRopeThreads / 32) + warp;
+  if (u >= units) return;
+  const Place p = lane_place(l, D, a.rope);
+  const int heads = 2 * a.Hkv, steps = (heads + HW - 1) / HW;
+  const Raw gk = load_chunks(a.gamma, p, a.gamma != nullptr);
+  for (; u < units; u += warps) {
+    const int t = u / parts, part = u % parts;
+    const uint16_t* k = a.x[0] + t * a.ldx[0];
+    const uint16_t* v0 = a.x[1] + t * a.ldx[1] - static_cast<long long>(a.Hkv) * D;
+    int h = part * HW + sub;
+    Raw w = load_chunks((h < a.Hkv ? k : v0) + h * D, p, h < heads);
+    const Slot to = find_slot(a, t, lane);
+    if (to.row < 0) continue;
+    Angles g;
+    if (part * HW < a.Hkv) token_angles(g, turns, a.rope, p, l, lane, to.pos, tab[warp]);
+    for (int s = part; s < steps; s += parts) {
+      const int hn = h + parts * HW;
+      const Raw next = load_chunks((hn < a.Hkv ? k : v0) + hn * D, p, hn < heads);
+      const bool is_k = h < a.Hkv;
+      float v[16];
+      norm_rotate<LPH>(w, is_k && a.gamma != nullptr, gk, 1.f / D, a.eps, p, is_k && p.rot, g, v);
+      // a block of 32 is four chunks, of two or four lanes: their peaks by way
+      // of shared memory; fp32 straight to E4M3, one rounding
+      float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
-    }
-    // the MXFP8 block of lanes l and l ^ 1; fp32 straight to E4M3, one rounding
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
-    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-    const uint32_t sc = ue8m0_from_amax(amax);
-    const float inv = inv_scale_from_ue8m0(sc);
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c[i] = e4m3x4_code(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
-    // the head's four scale bytes in one word
-    uint32_t sw = sc << (8 * (l >> 1));
-    sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 2);
-    sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 4);
-    if (mine) {
-      const long long row = (static_cast<long long>(page) * a.Hkv + h) * P + slot;
-      *reinterpret_cast<uint4*>(a.codes[which] + row * D + 16 * l) = make_uint4(c[0], c[1], c[2], c[3]);
-      if (l == 0) *reinterpret_cast<uint32_t*>(a.scales[which] + row * (D / 32)) = sw;
+      for (int i = 0; i < 8; ++i) m0 = fmaxf(m0, fabsf(v[i])), m1 = fmaxf(m1, fabsf(v[8 + i]));
+      float* pk = peak[warp][sub];
+      __syncwarp();  // the last step's have been read
+      pk[p.c0 / 8] = m0;
+      pk[p.c1 / 8] = m1;
+      __syncwarp();
+      const float4 q0 = *reinterpret_cast<const float4*>(pk + p.c0 / 32 * 4);
+      const float4 q1 = *reinterpret_cast<const float4*>(pk + p.c1 / 32 * 4);
+      const uint32_t s0 = ue8m0_from_amax(fmaxf(fmaxf(q0.x, q0.y), fmaxf(q0.z, q0.w)));
+      const uint32_t s1 = ue8m0_from_amax(fmaxf(fmaxf(q1.x, q1.y), fmaxf(q1.z, q1.w)));
+      const float i0 = inv_scale_from_ue8m0(s0), i1 = inv_scale_from_ue8m0(s1);
+      if (h < heads) {
+        const long long row = to.row + (static_cast<long long>(is_k ? h : h - a.Hkv) << a.log2P);
+        uint8_t* c = (is_k ? a.codes[0] : a.codes[1]) + row * D;
+        uint8_t* sc = (is_k ? a.scales[0] : a.scales[1]) + row * (D / 32);
+        *reinterpret_cast<uint2*>(c + p.c0) = make_uint2(e4m3x4_code(v[0] * i0, v[1] * i0, v[2] * i0, v[3] * i0),
+                                                         e4m3x4_code(v[4] * i0, v[5] * i0, v[6] * i0, v[7] * i0));
+        *reinterpret_cast<uint2*>(c + p.c1) =
+            make_uint2(e4m3x4_code(v[8] * i1, v[9] * i1, v[10] * i1, v[11] * i1),
+                       e4m3x4_code(v[12] * i1, v[13] * i1, v[14] * i1, v[15] * i1));
+        if (p.c0 % 32 == 0) sc[p.c0 / 32] = static_cast<uint8_t>(s0);
+        if (p.c1 % 32 == 0) sc[p.c1 / 32] = static_cast<uint8_t>(s1);
+      }
+      w = next;
+      h = hn;
     }
   }
 }
 
-// Warps that share a token's `steps` warp steps: one step a warp while all of
-// them fit the GPU at once (latency), the whole token in one warp when there
-// are tokens enough (its sines and cosines are computed once).
+// Units that share a token's steps: one step each while all of them fit the
+// GPU at once (latency), else fewer (a token's sines and cosines are computed
+// once a unit).
 int token_parts(long long tokens, int steps, int sms) {
-  const long long resident = static_cast<long long>(sms) * 16;
+  const long long resident = static_cast<long long>(sms) * kRopeBlocks * (kRopeThreads / 32);
   int parts = steps;
   while (parts > 1 && tokens * parts > resident) parts = (parts + 1) / 2;
   return parts;
 }
+unsigned unit_blocks(int units, int sms) {
+  return static_cast<unsigned>(std::min((units + kRopeThreads / 32 - 1) / (kRopeThreads / 32), sms * kRopeBlocks));
+}
 
 template <int LPH>
 cudaError_t norm_rope_lph(const NormRopeArgs& a, int sms, cudaStream_t stream) {
-  const int hw = 32 / LPH;
-  const int steps = (a.H[0] + hw - 1) / hw > (a.H[1] + hw - 1) / hw ? (a.H[0] + hw - 1) / hw : (a.H[1] + hw - 1) / hw;
-  const int parts = token_parts(a.T, steps, sms);
-  const long long warps = static_cast<long long>(a.T) * parts;
-  norm_rope_kernel<LPH><<<static_cast<unsigned>((warps + 3) / 4), kRopeThreads, 0, stream>>>(a, parts);
+  const int hw = 32 / LPH, steps = (a.H[0] + a.H[1] + hw - 1) / hw;
+  const int parts = token_parts(a.T, steps, sms), units = a.T * parts;
+  norm_rope_kernel<LPH><<<unit_blocks(units, sms), kRopeThreads, 0, stream>>>(a, parts, units);
   return cudaGetLastError();
 }
 
@@ -299,10 +354,9 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, int sms, cudaStream_t stream
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, int sms, cudaStream_t stream) {
-  const int steps = 2 * ((a.Hkv + 3) / 4);
-  const int parts = token_parts(a.T, steps, sms);
-  const long long warps = static_cast<long long>(a.T) * parts;
-  kv_append_kernel<<<static_cast<unsigned>((warps + 3) / 4), kRopeThreads, 0, stream>>>(a, parts);
+  const int steps = (2 * a.Hkv + 3) / 4;
+  const int parts = token_parts(a.T, steps, sms), units = a.T * parts;
+  kv_append_kernel<<<unit_blocks(units, sms), kRopeThreads, 0, stream>>>(a, parts, units);
   return cudaGetLastError();
 }
 
