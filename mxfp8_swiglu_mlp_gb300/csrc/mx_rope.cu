@@ -35,7 +35,11 @@ namespace fsops {
 
 namespace {
 
-constexpr int kRopeThreads = 128, kRopeBlocks = 6;  // blocks an SM: 80 registers a thread
+constexpr int kRopeThreads = 128;
+// Blocks an SM, at 80 and 96 registers a thread.  Measured: norm_rope with 16384
+// tokens of 32 + 8 heads of 128 takes 60 us with 6, 65 with 5, 81 with 8 (spills);
+// the append of 11k tokens of 8 heads 22 us with 5, 25 with 6 (spills).
+constexpr int kRopeBlocks = 6, kAppendBlocks = 5;
 constexpr int kMaxRotary = 256;
 
 // Fraction of a turn per position, in units of 2^-64 turns.
@@ -165,14 +169,14 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
 // share a token's steps.  Each step's loads are issued a step ahead.
 template <int LPH>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
-    norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int parts, int units) {
+    norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int parts, unsigned units) {
   constexpr int HW = 32 / LPH;  // heads of a step
   __shared__ __align__(16) float2 tab[kRopeThreads / 32][kMaxRotary / 2];
   __shared__ long long turns[kMaxRotary / 2];
   const int lane = threadIdx.x & 31, l = lane % LPH, sub = lane / LPH, warp = threadIdx.x >> 5;
-  const int warps = gridDim.x * (kRopeThreads / 32);
+  const unsigned warps = gridDim.x * (kRopeThreads / 32);
   load_turns(turns, a.rope);
-  int u = blockIdx.x * (kRopeThreads / 32) + warp;
+  unsigned u = blockIdx.x * (kRopeThreads / 32) + warp;
   if (u >= units) return;
   int pos = a.rope.R > 0 ? __ldg(a.positions + u / parts) : 0;
   const Place p = lane_place(l, a.D, a.rope);
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
   const Raw gq = load_chunks(a.gamma[0], p, p.on && a.gamma[0] != nullptr);
   const Raw gk = load_chunks(a.gamma[1], p, p.on && a.gamma[1] != nullptr);
   for (; u < units; u += warps) {
-    const int t = u / parts, part = u % parts;
+    const int t = static_cast<int>(u / parts), part = static_cast<int>(u % parts);
     const uint16_t* q = a.x[0] + t * a.ldx[0];
     const uint16_t* k = a.x[1] + t * a.ldx[1] - static_cast<long long>(a.H[0]) * a.D;
     uint16_t* yq = a.y[0] + t * a.ldy[0];
@@ -259,22 +263,22 @@ __device__ __forceinline__ Slot find_slot(const KvAppendArgs& a, int t, int lane
 }
 
 // Unit (token, part): the KV heads of k, then of v, four a step.
-__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
-    kv_append_kernel(const __grid_constant__ KvAppendArgs a, int parts, int units) {
+__global__ void __launch_bounds__(kRopeThreads, kAppendBlocks)
+    kv_append_kernel(const __grid_constant__ KvAppendArgs a, int parts, unsigned units) {
   constexpr int D = 128, LPH = 8, HW = 4;
   __shared__ __align__(16) float2 tab[kRopeThreads / 32][D / 2];
   __shared__ long long turns[D / 2];
   __shared__ __align__(16) float peak[kRopeThreads / 32][HW][D / 8];  // largest magnitude of each chunk
   const int lane = threadIdx.x & 31, l = lane % LPH, sub = lane / LPH, warp = threadIdx.x >> 5;
-  const int warps = gridDim.x * (kRopeThreads / 32);
+  const unsigned warps = gridDim.x * (kRopeThreads / 32);
   load_turns(turns, a.rope);
-  int u = blockIdx.x * (kRopeThreads / 32) + warp;
+  unsigned u = blockIdx.x * (kRopeThreads / 32) + warp;
   if (u >= units) return;
   const Place p = lane_place(l, D, a.rope);
   const int heads = 2 * a.Hkv, steps = (heads + HW - 1) / HW;
   const Raw gk = load_chunks(a.gamma, p, a.gamma != nullptr);
   for (; u < units; u += warps) {
-    const int t = u / parts, part = u % parts;
+    const int t = static_cast<int>(u / parts), part = static_cast<int>(u % parts);
     const uint16_t* k = a.x[0] + t * a.ldx[0];
     const uint16_t* v0 = a.x[1] + t * a.ldx[1] - static_cast<long long>(a.Hkv) * D;
     int h = part * HW + sub;
@@ -325,21 +329,21 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 // Units that share a token's steps: one step each while all of them fit the
 // GPU at once (latency), else fewer (a token's sines and cosines are computed
 // once a unit).
-int token_parts(long long tokens, int steps, int sms) {
-  const long long resident = static_cast<long long>(sms) * kRopeBlocks * (kRopeThreads / 32);
+int token_parts(long long tokens, int steps, int blocks) {
+  const long long resident = static_cast<long long>(blocks) * (kRopeThreads / 32);
   int parts = steps;
   while (parts > 1 && tokens * parts > resident) parts = (parts + 1) / 2;
   return parts;
 }
-unsigned unit_blocks(int units, int sms) {
-  return static_cast<unsigned>(std::min((units + kRopeThreads / 32 - 1) / (kRopeThreads / 32), sms * kRopeBlocks));
+unsigned unit_blocks(int units, int blocks) {
+  return static_cast<unsigned>(std::min((units - 1) / (kRopeThreads / 32) + 1, blocks));
 }
 
 template <int LPH>
 cudaError_t norm_rope_lph(const NormRopeArgs& a, int sms, cudaStream_t stream) {
   const int hw = 32 / LPH, steps = (a.H[0] + a.H[1] + hw - 1) / hw;
-  const int parts = token_parts(a.T, steps, sms), units = a.T * parts;
-  norm_rope_kernel<LPH><<<unit_blocks(units, sms), kRopeThreads, 0, stream>>>(a, parts, units);
+  const int parts = token_parts(a.T, steps, sms * kRopeBlocks), units = a.T * parts;
+  norm_rope_kernel<LPH><<<unit_blocks(units, sms * kRopeBlocks), kRopeThreads, 0, stream>>>(a, parts, units);
   return cudaGetLastError();
 }
 
@@ -355,8 +359,8 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, int sms, cudaStream_t stream
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, int sms, cudaStream_t stream) {
   const int steps = (2 * a.Hkv + 3) / 4;
-  const int parts = token_parts(a.T, steps, sms), units = a.T * parts;
-  kv_append_kernel<<<unit_blocks(units, sms), kRopeThreads, 0, stream>>>(a, parts, units);
+  const int parts = token_parts(a.T, steps, sms * kAppendBlocks), units = a.T * parts;
+  kv_append_kernel<<<unit_blocks(units, sms * kAppendBlocks), kRopeThreads, 0, stream>>>(a, parts, units);
   return cudaGetLastError();
 }
 
