@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libfsops.so")
 SOURCES = ["mx_kernels.cu", "mx_slice.cu", "mx_small.cu", "mx_blockscale.cu", "mx_gemm_tiled.cu", "mx_attention.cu",
-           "mx_rope.cu", "mx_chunk.cu", "fsops_api.cu"]
+           "mx_rope.cu", "mx_chunk.cu", "mx_chunk_few.cu", "fsops_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -9,6 +9,7 @@ namespace fsops {
 
 constexpr int kChunkD = 128;            // head dimension
 constexpr int kChunkMaxGroup = 64;      // query heads per KV head
+constexpr int kChunkFewRows = 64;       // rows of a query tile of the kernel for few rows
 constexpr size_t kChunkHeaderBytes = 256;
 constexpr size_t kChunkCounterBytes = 4096;  // two counters a block, blocks <= 256
 
@@ -23,13 +24,13 @@ struct ChunkArgs {
   const int32_t* lens;        // [B]
   uint32_t* status;           // first error (status << 24 | site << 16 | sequence)
   uint32_t* count;            // [2 * grid] parts of a query tile that have arrived (zero between calls)
-  float* rec;                 // [2 * grid][128][slot_rows] unnormalised outputs of parts
+  float* rec;                 // [2 * grid] unnormalised outputs of parts: [128][slot_rows], for few rows [slot_rows][128]
   float2* rec_ml;             // [2 * grid][slot_rows] running maximum (base 2) and sum
   int slot_rows;
   int T, B, Hq, Hkv, G, log2P, num_pages, max_pages, window;
   float scale_log2;           // |sm_scale| * log2(e)
   int negate;                 // sm_scale < 0: q enters with its sign turned
-  int tile_rows;              // rows of a query tile: 128 or 256
+  int tile_rows;              // rows of a query tile: 256, or kChunkFewRows for the kernel for few rows
   int grid;
   uint32_t tries;             // of a wait before it gives up
 };
@@ -43,5 +44,6 @@ inline int chunk_slot_rows(int T, int G, int tile_rows) {
   return r < tile_rows ? static_cast<int>(r) : tile_rows;
 }
 cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream);
+cudaError_t launch_chunk_few(const ChunkArgs& a, cudaStream_t stream);
 
 }  // namespace fsops

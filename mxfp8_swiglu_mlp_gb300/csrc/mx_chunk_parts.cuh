@@ -1,0 +1,405 @@
+// mx_chunk_parts.cuh -- what the two kernels of the chunk attention (mx_chunk.cu
+// for many rows, mx_chunk_few.cu for few) share: bounded waits, the warps that
+// load the cache and widen V, and the queries' operand.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "mx_chunk.h"
+#include "mx_chunk_plan.cuh"
+
+namespace fsops {
+
+namespace {
+
+using chunk::Item;
+using chunk::kKeys;
+
+constexpr int kD = kChunkD;
+constexpr int kConvWarps = 4;
+constexpr uint32_t kCodes = kKeys * kD;        // bytes of a K or V tile of codes
+constexpr uint32_t kScales = 512;              // bytes kept for a tile's scales
+constexpr uint32_t kOperand = kKeys * kD * 2;  // V as bf16: two halves of 64 dimensions,
+constexpr uint32_t kHalf = kOperand / 2;       // [tokens][128 bytes], 128-byte swizzle
+constexpr int kSlots = 2;                      // bf16 V tiles
+constexpr float kGrow = 8.f;                   // in powers of two
+static_assert(kKeys % 16 == 0 && kCodes % 1024 == 0, "16-token groups, whole swizzle atoms");
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_plain(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load_plain(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// One lane of the warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+struct Ctx {
+  const ChunkArgs& a;
+  volatile uint32_t* stop;  // the site of a wait that ran out
+  uint32_t tries;
+};
+// Bounded wait by a whole warp, whose lanes go on or give up together.  Every
+// wait is for another warp of the block, so thousandths of a second at most;
+// a failed try sleeps for microseconds, so the limit is a number of tries.
+// Where one runs out the block stops, and says so at its end.  (The code is
+// kept this short on purpose: the roles' loops together have to stay in the
+// instruction cache, and there are some thirty waits.)
+__device__ __forceinline__ bool wait(const Ctx& c, uint64_t* bar, uint32_t parity, uint32_t site) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xFFFFFFFFu, ok)) {
+#pragma unroll 1
+    for (uint32_t n = c.tries; !(ok = mbar_try_wait(bar, parity)); --n) {
+      if (n == 0) *c.stop = site;
+      if (*c.stop != 0u) break;
+    }
+    ok = __all_sync(0xFFFFFFFFu, ok);
+  }
+  return ok;
+}
+// A warp's arrival, after all its lanes' writes.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+// A position in a ring of n stages.
+template <int n>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == n) slot = 0, phase ^= 1u;
+  }
+};
+
+// Sixteen codes times m (a bf16 power of two, twice): four bf16 words for each
+// of the two 16-byte pieces.  A code s eeee mmm moved to s 0000eeee mmm0000 is
+// the bf16 2^-120 times its value (subnormal codes included), which m takes
+// back.  Within four codes the order is 0, 2, 1, 3: the queries are stored in
+// the same order, and the outputs' columns are put back at the end.
+__device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t m) {
+  const uint32_t even = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u);
+  const uint32_t odd = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
+  return make_uint2(mul_bf16x2(even, m), mul_bf16x2(odd, m));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// ---------------------------------------------------------------- load warps
+// One of them copies K's key tiles into its ring (boxes of 16 tokens, swizzled
+// as the products read them; a page holds whole groups of 16), the other V's,
+// and their scales: K's in the order that tcgen05.cp wants, V's token by token.
+// A copy costs its warp about 50 cycles to issue, which is why there are two
+// warps.  Four tiles' groups are looked up at a time, one a lane, and the next
+// four's pages fetched meanwhile.
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The thread's arrival on `bar` when its copies so far have landed.
+__device__ __forceinline__ void copy_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+struct Loader {
+  bool v;
+  int stages;
+  uint8_t *codes, *sf;
+  const uint8_t* scales;
+  uint64_t *full, *empty;
+  int slot = 0;
+  uint32_t phase = 0;
+
+  __device__ __forceinline__ bool item(const Ctx& c, const Item& w, int lane) {
+    constexpr int kGroups = kKeys / 16, kBatch = 4;  // groups of a tile, tiles of a batch
+    const ChunkArgs& a = c.a;
+    const int t0 = w.t0, t1 = w.t1, lo = w.lo, hi = w.hi, hk = w.hk, mask = (1 << a.log2P) - 1;
+    const int32_t* table = a.table + static_cast<long long>(w.b) * a.max_pages;
+    auto page = [&](int tok) { return __ldg(table + (min(max(tok, lo), hi - 1) >> a.log2P)); };
+    int tok = 16 * (t0 * kGroups + lane);  // the lane's group
+    int pid = page(tok);
+    const int part = lane >> 2, in = 4 * (lane & 3);  // the lane's four tokens among a tile's scales
+    const uint32_t sdst = v ? 16u * lane : ((4u * lane) & 31u) * 16u + ((4u * lane) >> 5) * 4u;
+#pragma unroll 1
+    for (int k = t0; k < t1; k += kBatch) {
+      if (pid < 0 || pid >= a.num_pages) {  // reported, and page 0 read instead
+        atomicCAS(a.status, 0u, (1u << 24) | (2u << 16) | (static_cast<uint32_t>(w.b) & 0xFFFFu));
+        pid = 0;
+      }
+      // first row of the group (below 2^31), -1 when no row of the queries sees it
+      const bool seen = lane < kGroups * kBatch && tok < hi && tok + 16 > lo;
+      const int row = seen ? ((pid * a.Hkv + hk) << a.log2P) + (tok & mask) : -1;
+      const uint32_t all = __ballot_sync(0xFFFFFFFFu, seen);
+      tok += 16 * kGroups * kBatch;
+      pid = page(tok);
+#pragma unroll 1
+      for (int i = 0; i < kBatch && k + i < t1; ++i) {
+        const int group = lane - kGroups * i;  // of this tile, where it is 0 .. 6
+        const int srow = __shfl_sync(0xFFFFFFFFu, row, min(kGroups * i + part, 31));
+        uint64_t* bar = full + slot;
+        if (!wait(c, empty + slot, phase ^ 1u, 3u)) return false;
+        fence_proxy_async_shared();
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc((all >> (kGroups * i)) & ((1u << kGroups) - 1u)) * 16u * kD);
+        __syncwarp();
+        if (group >= 0 && group < kGroups && row >= 0) {
+          uint8_t* d = codes + slot * kCodes + group * 16 * kD;
+          if (v)
+            bulk_load_plain(d, a.vc + static_cast<size_t>(row) * kD, 16 * kD, bar);
+          else
+            tma_load_plain(d, &a.tm_k, bar, 0, row);
+        }
+        if (part < kGroups && srow >= 0) {
+          const uint8_t* s = scales + static_cast<size_t>(srow + in) * (kD / 32);
+          const uint32_t d = smem_u32(sf + slot * kScales) + sdst;
+          if (v) {
+            copy_async16(d, s);
+          } else {  // token 4 lane + i at row % 32 times 16 bytes, row / 32 times 4
+#pragma unroll
+            for (int j = 0; j < 4; ++j) copy_async4(d + 16 * j, s + 4 * j);
+          }
+        }
+        copy_async_arrive(bar);
+        if (++slot == stages) slot = 0, phase ^= 1u;
+      }
+    }
+    return true;
+  }
+  // copies in flight land before the block ends (only after a wait ran out)
+  __device__ __forceinline__ void drain() {
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = 0; i < stages; ++i)
+      while (!mbar_try_wait(full + i, phase ^ (i >= slot ? 1u : 0u)) && globaltimer_ns() - t0 < 20000000ull) {
+      }
+  }
+};
+
+// The role of a load warp (v: the one for V); the other one walks the plan.
+template <int NK, int NV, class Ctl>
+__device__ __forceinline__ void load_items(const Ctx& c, Ctl* ctl, uint8_t* k, uint8_t* raw, uint8_t* sfk, uint8_t* sv,
+                                           int qs, int rs, bool v, int lane) {
+  const ChunkArgs& a = c.a;
+  Loader ld;
+  ld.v = v;
+  ld.stages = ld.v ? NV : NK;
+  ld.codes = v ? raw : k, ld.sf = v ? sv : sfk;
+  ld.scales = ld.v ? a.vs : a.ks;
+  ld.full = ld.v ? ctl->r_full : ctl->k_full, ld.empty = ld.v ? ctl->r_empty : ctl->k_empty;
+  chunk::Walk walk;
+  if (!ld.v) {
+    if (lane == 0) tma_prefetch_desc(&a.tm_k);
+    walk.init(a, ctl->ranges, blockIdx.x, qs, rs, lane);
+  }
+  Ring<2> it;
+#pragma unroll 1
+  for (;; it.step()) {
+    Item& w = ctl->item[it.slot];
+    if (!ld.v) {
+      Item next;
+      if (!walk.next(a, lane, next)) next.t0 = next.t1 = 0;
+      if (!wait(c, &ctl->it_empty[it.slot], it.phase ^ 1u, 2u)) break;
+      if (lane == 0) w = next;
+      __syncwarp();
+      mbar_arrive(&ctl->it_full[it.slot]);
+    } else if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) {
+      break;
+    }
+    if (w.t0 == w.t1 || !ld.item(c, w, lane)) break;
+    if (ld.v) warp_arrive(&ctl->it_empty[it.slot], lane);
+  }
+  if (*c.stop != 0u) ld.drain();
+}
+
+// ---------------------------------------------------------------- convert warps
+// V's codes of tokens from tok0 to a bf16 tile; tokens outside [lo, hi) become
+// zeros whatever the ring holds there.
+__device__ __forceinline__ void convert_tile(const uint8_t* raw, const uint8_t* sc, uint8_t* out, int tok0, int lo, int hi,
+                                             int t) {
+  const int piece = t & 7, r0 = t >> 3;
+  const bool inside = tok0 >= lo && tok0 + kKeys <= hi;
+  constexpr int kStep = 32 * kConvWarps / 8, kPasses = kKeys / kStep;  // rows of a pass
+  // the lanes of the second half write their two pieces in the other order, so
+  // that eight lanes meet all banks
+  const int odd = piece >> 2, first = ((2 * (piece & 3) + odd) ^ (r0 & 7)) << 4, second = first ^ 16;
+  uint8_t* row = out + odd * kHalf + r0 * 128;
+  raw += r0 * kD + 16 * piece, sc += 4 * r0 + (piece >> 1);
+  uint4 next = *reinterpret_cast<const uint4*>(raw);
+  uint32_t snext = *sc;
+#pragma unroll 2
+  for (int i = 0; i < kPasses; ++i) {
+    const uint4 x = next;
+    const uint32_t s = snext;
+    if (i + 1 < kPasses) {
+      raw += kStep * kD, sc += kStep * 4;
+      next = *reinterpret_cast<const uint4*>(raw);
+      snext = *sc;
+    }
+    const int tok = tok0 + r0 + i * kStep;
+    const bool on = inside || (tok >= lo && tok < hi);
+    uint32_t m = on ? ((min(s, 134u) + 120u) << 7) * 0x10001u : 0u;  // 2^(s - 127 + 120)
+    uint2 p0 = widen4(x.x, m), p1 = widen4(x.y, m), p2 = widen4(x.z, m), p3 = widen4(x.w, m);
+    if (on && s > 134u) {  // 2^(s - 7) is beyond bf16: the rest of it
+      m = ((s - 134u + 127u) << 7) * 0x10001u;
+      p0 = make_uint2(mul_bf16x2(p0.x, m), mul_bf16x2(p0.y, m)), p1 = make_uint2(mul_bf16x2(p1.x, m), mul_bf16x2(p1.y, m));
+      p2 = make_uint2(mul_bf16x2(p2.x, m), mul_bf16x2(p2.y, m)), p3 = make_uint2(mul_bf16x2(p3.x, m), mul_bf16x2(p3.y, m));
+    }
+    const uint4 lo8 = make_uint4(p0.x, p0.y, p1.x, p1.y), hi8 = make_uint4(p2.x, p2.y, p3.x, p3.y);
+    *reinterpret_cast<uint4*>(row + first) = odd ? hi8 : lo8;
+    *reinterpret_cast<uint4*>(row + second) = odd ? lo8 : hi8;
+    row += kStep * 128;
+  }
+}
+
+// The role of the convert warps, thread ct of them.
+template <int NV, class Ctl>
+__device__ __forceinline__ void convert_items(const Ctx& c, Ctl* ctl, const uint8_t* raw, const uint8_t* sv, uint8_t* v,
+                                              int ct, int lane) {
+  Ring<2> it;
+  Ring<NV> ring;
+  Ring<kSlots> vr;
+  for (bool ok = true; ok; it.step()) {
+    if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) break;
+    const int t0 = ctl->item[it.slot].t0, t1 = ctl->item[it.slot].t1, lo = ctl->item[it.slot].lo,
+              hi = ctl->item[it.slot].hi;
+    warp_arrive(&ctl->it_empty[it.slot], lane);
+    if (t0 == t1) break;
+    for (int k = t0; k < t1; ++k) {
+      ok = wait(c, &ctl->r_full[ring.slot], ring.phase, 3u) && wait(c, &ctl->v_empty[vr.slot], vr.phase ^ 1u, 6u);
+      if (!ok) break;
+      convert_tile(raw + ring.slot * kCodes, sv + ring.slot * kScales,
+                   v + vr.slot * kOperand, k * kKeys, lo, hi, ct);
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl->v_full[vr.slot]);
+        mbar_arrive(&ctl->r_empty[ring.slot]);
+      }
+      ring.step();
+      vr.step();
+    }
+  }
+}
+
+// ---------------------------------------------------------------- queries
+// Rows first .. first + rows - 1 of a query operand (row i is row r0 + i of the
+// sequence; the last one stands in for rows past the end) as two E4M3 terms
+// with their scales, the second `lo` rows further on, by `warps` warps (rows a
+// multiple of 16; not ragged: of 8 * warps).  Four lanes hold a block of 32
+// dimensions.
+// Where an operand keeps row r's scales: tiles of 128 rows, as tcgen05.cp wants them.
+__device__ __forceinline__ int scale_at(int r) { return (r >> 7) * static_cast<int>(kScales) + (r & 31) * 16 + ((r >> 5) & 3) * 4; }
+template <int warps, bool ragged>
+__device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item& w, int r0, uint8_t* codes, uint8_t* sf,
+                                             int first, int rows, int lo, int warp, int lane) {
+  const int R = w.n * a.G;
+  const uint32_t flip = a.negate ? 0x80008000u : 0u;
+  const int c = lane & 15;  // the lane's 8 dimensions
+#pragma unroll 1
+  for (int i0 = warp * 2 + (lane >> 4); i0 < rows; i0 += 8 * warps) {
+   uint4 xs[4];
+#pragma unroll
+   for (int k = 0; k < 4; ++k) {
+    const int rr = min(r0 + first + i0 + 2 * warps * k, R - 1), tok = rr / a.G;
+    xs[k] = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<long long>(w.c0 + tok) * a.ldq +
+                                                 (w.hk * a.G + rr - tok * a.G) * kD) + c);
+   }
+#pragma unroll
+   for (int k0 = 0; k0 < 4; ++k0) {
+    if (ragged && i0 + 2 * warps * k0 >= rows) break;
+    const int r = first + i0 + 2 * warps * k0;
+    const uint4 x = xs[k0];
+    const uint32_t u[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
+    uint32_t am = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) am = __vmaxu2(am, u[k] & 0x7FFF7FFFu);
+    am = max(am & 0xFFFFu, am >> 16);
+    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+    // the largest below 2^8 in units of the first scale: nothing saturates, and
+    // the rest is at most 2^3 of them, four bits again
+    const int e = static_cast<int>(am >> 7);
+    const uint32_t s0 = static_cast<uint32_t>(max(e - 7, 0)), s1 = static_cast<uint32_t>(max(e - 11, 0));
+    const float i0 = inv_scale_from_ue8m0(s0), i1 = inv_scale_from_ue8m0(s1);
+    const float back = s0 != 0 ? __uint_as_float(s0 << 23) : __uint_as_float(0x00400000u);
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float v0 = bf16_lo(u[2 * k]), v1 = bf16_hi(u[2 * k]), v2 = bf16_lo(u[2 * k + 1]), v3 = bf16_hi(u[2 * k + 1]);
+      h[k] = e4m3x4_code(v0 * i0, v1 * i0, v2 * i0, v3 * i0);
+      const __nv_fp8x4_e4m3* hc = reinterpret_cast<const __nv_fp8x4_e4m3*>(&h[k]);
+      const float4 hv = static_cast<float4>(*hc);
+      l[k] = e4m3x4_code(fmaf(-hv.x, back, v0) * i1, fmaf(-hv.y, back, v1) * i1, fmaf(-hv.z, back, v2) * i1,
+                         fmaf(-hv.w, back, v3) * i1);
+    }
+    uint8_t* d = codes + r * 128 + ((((c >> 1) ^ (r & 7)) << 4) | ((c & 1) << 3));
+    *reinterpret_cast<uint2*>(d) = make_uint2(h[0], h[1]);
+    *reinterpret_cast<uint2*>(d + lo * 128) = make_uint2(l[0], l[1]);
+    if ((c & 3) == 0) {
+      sf[scale_at(r) + (c >> 2)] = static_cast<uint8_t>(s0);
+      sf[scale_at(r + lo) + (c >> 2)] = static_cast<uint8_t>(s1);
+    }
+   }
+  }
+}
+
+}  // namespace
+
+}  // namespace fsops
