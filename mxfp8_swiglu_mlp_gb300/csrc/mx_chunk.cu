@@ -246,12 +246,12 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
   if (t == 0) {
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
-      mbar_init(&ctl->k_full[i], 33);
+      mbar_init(&ctl->k_full[i], 32);
       mbar_init(&ctl->k_empty[i], 2);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      mbar_init(&ctl->r_full[i], 33);
+      mbar_init(&ctl->r_full[i], 32);
       mbar_init(&ctl->r_empty[i], kConvWarps);
     }
 #pragma unroll

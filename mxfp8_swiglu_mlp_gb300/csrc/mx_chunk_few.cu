@@ -142,12 +142,12 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
   if (t == 0) {
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
-      mbar_init(&ctl->k_full[i], 33);
+      mbar_init(&ctl->k_full[i], 32);
       mbar_init(&ctl->k_empty[i], 1);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      mbar_init(&ctl->r_full[i], 33);
+      mbar_init(&ctl->r_full[i], 32);
       mbar_init(&ctl->r_empty[i], kConvWarps);
     }
 #pragma unroll
@@ -297,9 +297,9 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
     if (ok) queries(0);
 #pragma unroll 1
     while (ok) {
-      float l[16], l1[16];  // the thread's sums, of a second group of rows too
+      float2 l[8], l1[8];  // the thread's sums, of a second group of rows too
 #pragma unroll
-      for (int i = 0; i < 16; ++i) l[i] = l1[i] = 0.f;
+      for (int i = 0; i < 8; ++i) l[i] = l1[i] = make_float2(0.f, 0.f);
       int turn = 0, turn1 = 0;  // which of the scales is in use
       const int groups = (ctl->item[it.slot].rows + 15) >> 4;
       {
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                   const float al = exp2_fast(ms[i] - mn[i]);
-                  l[i] *= al;
+                  (i & 1 ? l[i >> 1].y : l[i >> 1].x) *= al;
                   v[i] = __float_as_uint(o[i] * al);
                 }
                 tmem_st16(tmem + lanes + kColO + 16 * g, v);
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
               probs();
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) l[i] += i & 1 ? e[i >> 1].y : e[i >> 1].x;
+            for (int i = 0; i < 8; ++i) l[i] = __fadd2_rn(l[i], e[i]);
             ok = wait(c, &ctl->p_free[buf], phase ^ 1u, 12u);
             if (!ok) break;
             if (live) {
@@ -418,8 +418,8 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
             }
             if (h + 2 < groups) {  // the other group of the warp comes next
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float x = l[i];
+              for (int i = 0; i < 8; ++i) {
+                const float2 x = l[i];
                 l[i] = l1[i], l1[i] = x;
               }
               const int x = turn;
@@ -443,7 +443,10 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
       for (int g = h; g < groups; g += 2) {
         float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = live ? (g == h ? l[i] : l1[i]) : 0.f;
+        for (int i = 0; i < 16; ++i) {
+          const float2 s = g == h ? l[i >> 1] : l1[i >> 1];
+          x[i] = live ? (i & 1 ? s.y : s.x) : 0.f;
+        }
         const float sum = across<true>(x, lane);
         if ((lane & 1) == 0) ctl->sums[wl][16 * g + (lane >> 1)] = sum;
       }

@@ -45,19 +45,6 @@ __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_plain(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void bulk_load_plain(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -144,12 +131,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 
 // ---------------------------------------------------------------- load warps
-// One of them copies K's key tiles into its ring (boxes of 16 tokens, swizzled
-// as the products read them; a page holds whole groups of 16), the other V's,
-// and their scales: K's in the order that tcgen05.cp wants, V's token by token.
-// A copy costs its warp about 50 cycles to issue, which is why there are two
-// warps.  Four tiles' groups are looked up at a time, one a lane, and the next
-// four's pages fetched meanwhile.
+// One of them copies K's key tiles into its ring, with the 128-byte swizzle that
+// the products read, the other V's as they are, and their scales: K's in the
+// order that tcgen05.cp wants, V's token by token.  A page holds whole groups
+// of 16 tokens, 2 KB of codes: with 16-byte asynchronous copies (four
+// instructions of a warp a group) a tile takes its warp a third of the cycles
+// that a bulk or tensor copy a group takes, whose issue is about 100 cycles each.
+// Four tiles' groups are looked up at a time, one a lane, and the next four's
+// pages fetched meanwhile.
 __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -178,6 +167,11 @@ struct Loader {
     int tok = 16 * (t0 * kGroups + lane);  // the lane's group
     int pid = page(tok);
     const int part = lane >> 2, in = 4 * (lane & 3);  // the lane's four tokens among a tile's scales
+    // a lane's 16 bytes of four rows: where they go in the first four, in the second
+    // (V: the halves of odd rows exchanged)
+    const int r4 = lane >> 3;
+    const uint32_t at0 = r4 * kD + (((lane & 7) ^ (v ? 4 * (r4 & 1) : r4)) << 4), at1 = v ? at0 : at0 ^ 64u;
+    const uint8_t* src = v ? a.vc : a.kc;
     const uint32_t sdst = v ? 16u * lane : ((4u * lane) & 31u) * 16u + ((4u * lane) >> 5) * 4u;
 #pragma unroll 1
     for (int k = t0; k < t1; k += kBatch) {
@@ -188,24 +182,24 @@ struct Loader {
       // first row of the group (below 2^31), -1 when no row of the queries sees it
       const bool seen = lane < kGroups * kBatch && tok < hi && tok + 16 > lo;
       const int row = seen ? ((pid * a.Hkv + hk) << a.log2P) + (tok & mask) : -1;
-      const uint32_t all = __ballot_sync(0xFFFFFFFFu, seen);
       tok += 16 * kGroups * kBatch;
       pid = page(tok);
 #pragma unroll 1
       for (int i = 0; i < kBatch && k + i < t1; ++i) {
-        const int group = lane - kGroups * i;  // of this tile, where it is 0 .. 6
         const int srow = __shfl_sync(0xFFFFFFFFu, row, min(kGroups * i + part, 31));
         uint64_t* bar = full + slot;
         if (!wait(c, empty + slot, phase ^ 1u, 3u)) return false;
         fence_proxy_async_shared();
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc((all >> (kGroups * i)) & ((1u << kGroups) - 1u)) * 16u * kD);
-        __syncwarp();
-        if (group >= 0 && group < kGroups && row >= 0) {
-          uint8_t* d = codes + slot * kCodes + group * 16 * kD;
-          if (v)
-            bulk_load_plain(d, a.vc + static_cast<size_t>(row) * kD, 16 * kD, bar);
-          else
-            tma_load_plain(d, &a.tm_k, bar, 0, row);
+        const uint32_t to = smem_u32(codes) + slot * kCodes;
+#pragma unroll 1
+        for (int g = 0; g < kGroups; ++g) {
+          const int grow = __shfl_sync(0xFFFFFFFFu, row, kGroups * i + g);
+          if (grow >= 0) {
+            const uint8_t* s = src + static_cast<size_t>(grow) * kD + 16 * lane;
+            const uint32_t d = to + g * 16 * kD;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) copy_async16(d + 4 * kD * j + (j & 1 ? at1 : at0), s + 4 * kD * j);
+          }
         }
         if (part < kGroups && srow >= 0) {
           const uint8_t* s = scales + static_cast<size_t>(srow + in) * (kD / 32);
@@ -244,10 +238,7 @@ __device__ __forceinline__ void load_items(const Ctx& c, Ctl* ctl, uint8_t* k, u
   ld.scales = ld.v ? a.vs : a.ks;
   ld.full = ld.v ? ctl->r_full : ctl->k_full, ld.empty = ld.v ? ctl->r_empty : ctl->k_empty;
   chunk::Walk walk;
-  if (!ld.v) {
-    if (lane == 0) tma_prefetch_desc(&a.tm_k);
-    walk.init(a, ctl->ranges, blockIdx.x, qs, rs, lane);
-  }
+  if (!ld.v) walk.init(a, ctl->ranges, blockIdx.x, qs, rs, lane);
   Ring<2> it;
 #pragma unroll 1
   for (;; it.step()) {
@@ -270,41 +261,39 @@ __device__ __forceinline__ void load_items(const Ctx& c, Ctl* ctl, uint8_t* k, u
 
 // ---------------------------------------------------------------- convert warps
 // V's codes of tokens from tok0 to a bf16 tile; tokens outside [lo, hi) become
-// zeros whatever the ring holds there.
+// zeros whatever the ring holds there.  A thread has 16 codes of every 16th
+// token: eight lanes four pieces of two tokens each, which keeps their 16-byte
+// stores (and, with the ring's halves exchanged in every other row, their
+// loads) apart in the banks.
+__device__ __forceinline__ void convert16(const uint8_t* raw, uint32_t s, uint8_t* row, int first, bool on) {
+  const uint4 x = *reinterpret_cast<const uint4*>(raw);
+  uint32_t m = on ? min(s, 134u) * 0x00800080u + 120u * 0x00800080u : 0u;  // 2^(s - 127 + 120), twice
+  uint2 p0 = widen4(x.x, m), p1 = widen4(x.y, m), p2 = widen4(x.z, m), p3 = widen4(x.w, m);
+  if (on && s > 134u) {  // 2^(s - 7) is beyond bf16: the rest of it
+    m = ((s - 134u + 127u) << 7) * 0x10001u;
+    p0 = make_uint2(mul_bf16x2(p0.x, m), mul_bf16x2(p0.y, m)), p1 = make_uint2(mul_bf16x2(p1.x, m), mul_bf16x2(p1.y, m));
+    p2 = make_uint2(mul_bf16x2(p2.x, m), mul_bf16x2(p2.y, m)), p3 = make_uint2(mul_bf16x2(p3.x, m), mul_bf16x2(p3.y, m));
+  }
+  *reinterpret_cast<uint4*>(row + first) = make_uint4(p0.x, p0.y, p1.x, p1.y);
+  *reinterpret_cast<uint4*>(row + (first ^ 16)) = make_uint4(p2.x, p2.y, p3.x, p3.y);
+}
 __device__ __forceinline__ void convert_tile(const uint8_t* raw, const uint8_t* sc, uint8_t* out, int tok0, int lo, int hi,
                                              int t) {
-  const int piece = t & 7, r0 = t >> 3;
-  const bool inside = tok0 >= lo && tok0 + kKeys <= hi;
-  constexpr int kStep = 32 * kConvWarps / 8, kPasses = kKeys / kStep;  // rows of a pass
-  // the lanes of the second half write their two pieces in the other order, so
-  // that eight lanes meet all banks
-  const int odd = piece >> 2, first = ((2 * (piece & 3) + odd) ^ (r0 & 7)) << 4, second = first ^ 16;
-  uint8_t* row = out + odd * kHalf + r0 * 128;
-  raw += r0 * kD + 16 * piece, sc += 4 * r0 + (piece >> 1);
-  uint4 next = *reinterpret_cast<const uint4*>(raw);
-  uint32_t snext = *sc;
-#pragma unroll 2
-  for (int i = 0; i < kPasses; ++i) {
-    const uint4 x = next;
-    const uint32_t s = snext;
-    if (i + 1 < kPasses) {
-      raw += kStep * kD, sc += kStep * 4;
-      next = *reinterpret_cast<const uint4*>(raw);
-      snext = *sc;
+  static_assert(kConvWarps == 4, "16 tokens a pass");
+  constexpr int kPasses = kKeys / 16;
+  const int half = (t >> 3) & 1, piece = 4 * half + (t & 3), r0 = 2 * (t >> 4) + ((t >> 2) & 1);
+  const int first = ((2 * (t & 3)) ^ (r0 & 7)) << 4;
+  out += half * kHalf + r0 * 128;
+  raw += r0 * kD + 16 * (piece ^ (4 * (r0 & 1))), sc += 4 * r0 + (piece >> 1);
+  if (tok0 >= lo && tok0 + kKeys <= hi) {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) convert16(raw + i * 16 * kD, sc[i * 64], out + i * 16 * 128, first, true);
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < kPasses; ++i) {
+      const int tok = tok0 + r0 + i * 16;
+      convert16(raw + i * 16 * kD, sc[i * 64], out + i * 16 * 128, first, tok >= lo && tok < hi);
     }
-    const int tok = tok0 + r0 + i * kStep;
-    const bool on = inside || (tok >= lo && tok < hi);
-    uint32_t m = on ? ((min(s, 134u) + 120u) << 7) * 0x10001u : 0u;  // 2^(s - 127 + 120)
-    uint2 p0 = widen4(x.x, m), p1 = widen4(x.y, m), p2 = widen4(x.z, m), p3 = widen4(x.w, m);
-    if (on && s > 134u) {  // 2^(s - 7) is beyond bf16: the rest of it
-      m = ((s - 134u + 127u) << 7) * 0x10001u;
-      p0 = make_uint2(mul_bf16x2(p0.x, m), mul_bf16x2(p0.y, m)), p1 = make_uint2(mul_bf16x2(p1.x, m), mul_bf16x2(p1.y, m));
-      p2 = make_uint2(mul_bf16x2(p2.x, m), mul_bf16x2(p2.y, m)), p3 = make_uint2(mul_bf16x2(p3.x, m), mul_bf16x2(p3.y, m));
-    }
-    const uint4 lo8 = make_uint4(p0.x, p0.y, p1.x, p1.y), hi8 = make_uint4(p2.x, p2.y, p3.x, p3.y);
-    *reinterpret_cast<uint4*>(row + first) = odd ? hi8 : lo8;
-    *reinterpret_cast<uint4*>(row + second) = odd ? lo8 : hi8;
-    row += kStep * 128;
   }
 }
 
