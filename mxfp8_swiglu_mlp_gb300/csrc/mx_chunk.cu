@@ -54,6 +54,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 2;  // two warps each
 constexpr int kBlock = 32 * (kLoadWarp + 2);
 constexpr int NK = 4, NV = 3;                         // tiles of K and of V's codes in flight
+constexpr int kSlots = 2;                             // bf16 V tiles
 constexpr uint32_t kQCodes = 128 * kD;                // bytes of one term of a query tile's half
 constexpr int kFirst = 64;                            // keys of a tile's first section
 // Columns of tensor memory: scores and (in their place) probabilities of the
@@ -98,6 +99,28 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 // ---------------------------------------------------------------- softmax warps
+// Rows first .. first + rows - 1 of a query tile's half (row i is row r0 + i of
+// the sequence; the last one stands in for rows past the end), by four warps
+// (rows a multiple of 64).
+__device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item& w, int r0, uint8_t* codes, uint8_t* sf, int first,
+                                             int rows, int warp, int lane) {
+  const int R = w.n * a.G;
+  const uint32_t flip = a.negate ? 0x80008000u : 0u;
+  const int c = lane & 15;
+#pragma unroll 1
+  for (int i0 = first + warp * 2 + (lane >> 4); i0 < first + rows; i0 += 32) {
+    uint4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int rr = min(r0 + i0 + 8 * k, R - 1), tok = rr / a.G;
+      x[k] = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<long long>(w.c0 + tok) * a.ldq +
+                                                  (w.hk * a.G + rr - tok * a.G) * kD) + c);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) store_query(x[k], flip, codes, sf, i0 + 8 * k, 128, c);
+  }
+}
+
 struct RowState {
   float m, l;  // running maximum (base 2, scaled) and sum
 };
@@ -255,9 +278,12 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       mbar_init(&ctl->r_empty[i], kConvWarps);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(&ctl->v_full[i], kConvWarps);
       mbar_init(&ctl->v_empty[i], 2);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         mbar_init(&ctl->s_full[i][u], 1);
@@ -431,7 +457,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     __syncwarp();
    }
   } else if (warp >= kSoftWarps) {
-    convert_items<NV>(c, ctl, smem + L::raw, smem + L::sv, smem + L::v, t - 32 * kSoftWarps, lane);
+    convert_items<NV, kSlots>(c, ctl, smem + L::raw, smem + L::sv, smem + L::v, t - 32 * kSoftWarps, lane);
   } else {
     // ---- softmax: stream m, a thread a row
     const int m = warp >> 2, wl = warp & 3, row = 32 * wl + lane;
@@ -442,9 +468,8 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       const Item& w = ctl->item[slot];
       if (w.t0 == w.t1) return;
       const bool pair = w.rows > 128;
-      load_queries<4, false>(a, w, w.r0 + (pair ? 128 * m : 0), smem + L::q + (pair ? m * 2 * kQCodes : 0),
-                             smem + L::sfq + (pair ? m * 2 * kScales : 0), pair ? 0 : 64 * m, pair ? 128 : 64, 128, wl,
-                             lane);
+      load_queries(a, w, w.r0 + (pair ? 128 * m : 0), smem + L::q + (pair ? m * 2 * kQCodes : 0),
+                   smem + L::sfq + (pair ? m * 2 * kScales : 0), pair ? 0 : 64 * m, pair ? 128 : 64, wl, lane);
       fence_proxy_async_shared();
       warp_arrive(&ctl->q_full, lane);
     };
@@ -541,7 +566,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
           const int rr = w.r0 + min(tr, w.rows - 1), tok = rr / a.G;
           y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
         } else {
-          const size_t slot = chunk::part_slot(w, ctl->ranges, blockIdx.x);
+          const size_t slot = w.slot;
           rec = a.rec + slot * kD * a.slot_rows + min(tr, w.rows - 1);
           if (write) a.rec_ml[slot * a.slot_rows + tr] = make_float2(st.m, st.l);
         }
@@ -621,7 +646,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
 }  // namespace
 
 int chunk_tile_rows(int T, int B, int G) {
-  return static_cast<long long>(T) * G > static_cast<long long>(kChunkFewRows) * B ? 256 : kChunkFewRows;
+  return static_cast<long long>(T) * G > 2LL * kChunkFewRows * B ? 256 : kChunkFewRows;
 }
 
 cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream) {

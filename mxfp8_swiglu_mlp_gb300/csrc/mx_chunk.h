@@ -9,7 +9,7 @@ namespace fsops {
 
 constexpr int kChunkD = 128;            // head dimension
 constexpr int kChunkMaxGroup = 64;      // query heads per KV head
-constexpr int kChunkFewRows = 64;       // rows of a query tile of the kernel for few rows
+constexpr int kChunkFewRows = 32;       // rows of a query tile of the kernel for few rows
 constexpr size_t kChunkHeaderBytes = 256;
 constexpr size_t kChunkCounterBytes = 4096;  // two counters a block, blocks <= 256
 

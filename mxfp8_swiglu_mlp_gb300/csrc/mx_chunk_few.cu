@@ -1,5 +1,5 @@
 // mx_chunk_few.cu -- the chunk attention of mx_chunk.cu for few rows: query
-// tiles of up to 64 rows (single tokens, drafted tokens), whose time is the
+// tiles of up to 32 rows (single tokens, drafted tokens), whose time is the
 // cache's bytes.
 //
 // With queries as the 128 rows of a product, a few of them would leave most of
@@ -8,22 +8,25 @@
 // of the outputs, O^T = V^T P^T, and the query rows their columns.
 //   S^T  [112 keys][2 x rows]  block-scaled E4M3 MMA on K's own codes; the two
 //        E4M3 terms of the queries are two groups of columns, added afterwards;
-//   P^T  [112 keys][64 rows] bf16 in shared memory, N-major;
-//   O^T  [128 dimensions][64 rows] with V widened to bf16 as the M-major operand.
-// A key tile costs 4 + 7 MMAs this way (with 32 rows about 200 + 330 cycles of
-// the tensor pipe), less than its 30 KB take to arrive (1250 cycles at the
-// card's copy rate), and a thread has one key and 16 rows of a tile: 8 warps,
-// four a group of 16 rows (two groups for more than 32 rows).
+//   P^T  [112 keys][32 rows] bf16 in shared memory, N-major;
+//   O^T  [128 dimensions][32 rows] with V widened to bf16 as the M-major operand.
+// A key tile costs 4 + 7 MMAs this way (about 500 cycles of the tensor pipe),
+// less than its 30 KB take to arrive (1250 cycles at the card's copy rate), and
+// a thread has one key and 16 rows of a tile: four warps for each 16 rows.
 //
-// A row's scale (its running maximum) is the same for all keys of a tile, so
-// the four warps of a row vote: while no score passes the scale by more than
-// 2^8, and nearly always none does, nothing is exchanged but the vote, and the
-// exponentials are computed under it.  Else they find the maximum together and
-// rescale.  A row's sum stays apart in the 112 threads until the item's end.
+// A row's scale (its running maximum) is the same for all keys, so the four
+// warps of a row vote, once for two tiles: while no score passes the scale by
+// more than 2^8, and nearly always none does, nothing but the vote is exchanged.
+// Else they find the maximum together, rescale, and compute the probabilities
+// again.  A row's sum stays apart in its 112 threads until the item's end.
 //
-// Products of one key tile run under the exponentials of another (scores and
-// probabilities are double buffered); loads run ahead over the items' ends, and
-// the next item's first scores are computed under this one's end.
+// Products of two key tiles run under the exponentials of the next two (scores
+// and probabilities are double buffered); loads run ahead over the items' ends,
+// and the next item's first scores are computed under this one's end.
+//
+// The code that runs once an item (queries, first maximum, end) is rolled up on
+// purpose: it is fetched anew each time, and straight-line code there cost
+// 10000 cycles an item, mostly of instruction fetches.
 #include "mx_chunk_parts.cuh"
 
 namespace fsops {
@@ -33,22 +36,24 @@ namespace {
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 2;  // two warps each
 constexpr int kBlock = 32 * (kLoadWarp + 2);
-constexpr int NK = 5, NV = 3;                 // tiles of K and of V's codes in flight
+constexpr int NK = 4, NV = 3, kSlots = 3;       // tiles of K and of V's codes in flight, of V as bf16
 constexpr int kRows = kChunkFewRows;
 constexpr uint32_t kProbs = kKeys * kRows * 2;  // a tile's probabilities
-static_assert(kRows == 64, "128 bytes of probabilities a key, one swizzle atom wide");
-// Columns of tensor memory: two tiles of scores, the outputs, scale factors of
-// the queries and of K (two tiles).
-constexpr uint32_t kColS = 128, kColO = 256, kColSfq = 320, kColSfk = 324;
+static_assert(kRows == 32, "64 bytes of probabilities a key, one swizzle atom wide");
+constexpr uint32_t kSwizzle64B = 4;
+// Columns of tensor memory: the scores of two times two tiles, the outputs, scale
+// factors of the queries and of K (four tiles).
+constexpr uint32_t kColS = 64, kColO = 256, kColSfq = 288, kColSfk = 292;
 constexpr float kNone = -3e38f;  // the scale of a row that has seen nothing
 
 struct Ctl {
   uint64_t k_full[NK], k_empty[NK], r_full[NV], r_empty[NV];  // rings of K and V codes
   uint64_t v_full[kSlots], v_empty[kSlots];
-  uint64_t s_full[2], s_free[2], p_full[2], p_free[2];  // by tile parity
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2];  // two tiles each, by turns
   uint64_t q_full, vote[2], group, fin[2], it_full[2], it_empty[2];
   Item item[2];
   float scale[2][kRows];     // the rows' scales (base 2), the one in use by turns
+  float fall[kRows];         // what the last change of scale makes of a row
   float peak[2][4][16];      // a group's maxima, of each warp
   float sums[4][kRows];
   uint32_t grown[2];         // the last vote that found a larger score
@@ -57,16 +62,22 @@ struct Ctl {
   uint32_t tmem, stop, last;
 };
 struct L {
-  static constexpr uint32_t q = 0, v = 128 * kD, p = v + kSlots * kOperand, k = p + 2 * kProbs, raw = k + NK * kCodes,
+  static constexpr uint32_t q = 0, v = 2 * kRows * kD, p = v + kSlots * kOperand, k = p + 4 * kProbs, raw = k + NK * kCodes,
                             sfk = raw + NV * kCodes, sv = sfk + NK * kScales, sfq = sv + NV * kScales,
                             ctl = sfq + kScales, bytes = ctl + sizeof(Ctl);
 };
 static_assert(L::bytes <= 232448 && NK <= 5 && NV <= 4, "shared memory");
 static_assert(NV * kCodes >= 16 * kD, "the 128-row product reads 16 rows behind the last K tile");
 
-// kind::f16, fp32 sums, bf16 operands, M = 128 (M-major, bit 15), N = 64 (N-major, bit 16).
+// kind::f16, fp32 sums, bf16 operands, M = 128 (M-major, bit 15), N = 32 (N-major, bit 16).
 constexpr uint32_t kIdescPv = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
                               ((static_cast<uint32_t>(kRows) >> 3) << 17) | ((128u >> 4) << 24);
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+               : "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -115,7 +126,7 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& a, const Item& w, con
     const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
     den = fmaf(f, ml.y, den);
     const int n = min(32, blocks - base);
-#pragma unroll 4
+#pragma unroll 2
     for (int p = 0; p < n; ++p) {
       const int slp = __shfl_sync(0xFFFFFFFFu, sl, p);
       const float fp = __shfl_sync(0xFFFFFFFFu, f, p);
@@ -151,9 +162,12 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
       mbar_init(&ctl->r_empty[i], kConvWarps);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(&ctl->v_full[i], kConvWarps);
       mbar_init(&ctl->v_empty[i], 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->s_full[i], 1);
       mbar_init(&ctl->s_free[i], kSoftWarps);
       mbar_init(&ctl->p_full[i], kSoftWarps);
@@ -196,7 +210,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
     const uint64_t dsk = smem_desc(smem_u32(smem + L::sfk), 0, 128, kSwizzleNone);
     const uint64_t dsq = smem_desc(smem_u32(smem + L::sfq), 0, 128, kSwizzleNone);
     const uint64_t dv = smem_desc(smem_u32(smem + L::v), kHalf, 1024, kSwizzle128B);
-    const uint64_t dp = smem_desc(smem_u32(smem + L::p), kProbs, 1024, kSwizzle128B);
+    const uint64_t dp = smem_desc(smem_u32(smem + L::p), kProbs, 512, kSwizzle64B);
     Ring<2> it, buf;
     Ring<NK> kr;
     Ring<kSlots> vr;
@@ -218,41 +232,45 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
         const uint32_t idesc = idesc_mxf8_e4m3(32 * groups, 0, 0);
 #pragma unroll 1
         for (int j = 0; j < tiles; ++j) {
-          ok = wait(c, &ctl->k_full[kr.slot], kr.phase, 6u) && wait(c, &ctl->s_free[buf.slot], buf.phase ^ 1u, 7u);
+          const uint32_t u = j & 1;
+          ok = (u || wait(c, &ctl->s_free[buf.slot], buf.phase ^ 1u, 7u)) && wait(c, &ctl->k_full[kr.slot], kr.phase, 6u);
           if (!ok) break;
-          fence_proxy_async_shared();  // the scales came by generic copies
+          const bool last = u || j + 1 == tiles;  // of the two
+          fence_proxy_async_shared();             // the codes came by generic copies
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t sfk = tmem + kColSfk + 4 * buf.slot;
+            const uint32_t at = 2 * buf.slot + u, sfk = tmem + kColSfk + 4 * at;
             tc_cp_32x128b_warpx4(sfk, dsk + kr.slot * (kScales >> 4));
 #pragma unroll
             for (int k = 0; k < 4; ++k)  // 32 dimensions
-              tc_mma_mxf8(tmem + kColS * buf.slot, dk + kr.slot * (kCodes >> 4) + ((32 * k) >> 4), dq + ((32 * k) >> 4),
+              tc_mma_mxf8(tmem + kColS * at, dk + kr.slot * (kCodes >> 4) + ((32 * k) >> 4), dq + ((32 * k) >> 4),
                           idesc | (k << 4) | (k << 29), sfk, tmem + kColSfq, k > 0);
-            tc_commit(&ctl->s_full[buf.slot]);
             tc_commit(&ctl->k_empty[kr.slot]);
+            if (last) tc_commit(&ctl->s_full[buf.slot]);
           }
           __syncwarp();
           kr.step();
-          buf.step();
+          if (last) buf.step();
         }
       } else {
 #pragma unroll 1
         for (int j = 0; j < tiles; ++j) {
-          ok = wait(c, &ctl->v_full[vr.slot], vr.phase, 8u) && wait(c, &ctl->p_full[buf.slot], buf.phase, 8u);
+          const uint32_t u = j & 1;
+          ok = (u || wait(c, &ctl->p_full[buf.slot], buf.phase, 8u)) && wait(c, &ctl->v_full[vr.slot], vr.phase, 8u);
           if (!ok) break;
+          const bool last = u || j + 1 == tiles;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)  // 16 tokens
               mma_ss(tmem + kColO, dv + vr.slot * (kOperand >> 4) + k * (2048 >> 4),
-                     dp + buf.slot * (kProbs >> 4) + k * (2048 >> 4), kIdescPv, (j > 0 || k > 0) ? 1u : 0u);
-            tc_commit(&ctl->p_free[buf.slot]);
+                     dp + (2 * buf.slot + u) * (kProbs >> 4) + k * (1024 >> 4), kIdescPv, (j > 0 || k > 0) ? 1u : 0u);
             tc_commit(&ctl->v_empty[vr.slot]);
+            if (last) tc_commit(&ctl->p_free[buf.slot]);
           }
           __syncwarp();
           vr.step();
-          buf.step();
+          if (last) buf.step();
         }
       }
     }
@@ -264,20 +282,32 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
     }
     __syncwarp();
   } else if (warp >= kSoftWarps) {
-    convert_items<NV>(c, ctl, smem + L::raw, smem + L::sv, smem + L::v, t - 32 * kSoftWarps, lane);
+    convert_items<NV, kSlots>(c, ctl, smem + L::raw, smem + L::sv, smem + L::v, t - 32 * kSoftWarps, lane);
   } else {
-    // ---- softmax: group of rows h (and h + 2), a thread a key
+    // ---- softmax: rows 16 h .. 16 h + 15, a thread a key
     const int h = warp >> 2, wl = warp & 3, key = 32 * wl + lane;
     const bool live = key < kKeys;
     const uint32_t lanes = static_cast<uint32_t>(32 * wl) << 16;
     const float scale = a.scale_log2;
-    uint8_t* const prow = smem + L::p + key * 128;  // the key's probabilities (of the first buffer)
-    uint32_t n = 0, votes = 0;                      // key tiles, votes so far
+    // the key's probabilities in a tile's buffer: 16-byte pieces 2 h and 2 h + 1
+    const uint32_t prow = L::p + key * 64 + ((2 * h ^ ((key >> 1) & 3)) << 4);
+    uint32_t n = 0, votes = 0, g_phase = 0;  // pairs of key tiles, votes so far
     auto queries = [&](int slot) {
       const Item& w = ctl->item[slot];
       if (w.t0 == w.t1) return;
-      const int rows = (w.rows + 15) & ~15;
-      load_queries<kSoftWarps, true>(a, w, w.r0, smem + L::q, smem + L::sfq, 0, rows, rows, warp, lane);
+      const int rows = (w.rows + 15) & ~15, R = w.n * a.G;
+      const uint32_t flip = a.negate ? 0x80008000u : 0u;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u), x1 = x;
+#pragma unroll 1
+      for (int i = rows / 16 - 1; i >= 0; --i) {
+        x1 = x;
+        const int rr = min(w.r0 + 16 * i + 2 * warp + (lane >> 4), R - 1), tok = rr / a.G;
+        x = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<long long>(w.c0 + tok) * a.ldq +
+                                                 (w.hk * a.G + rr - tok * a.G) * kD) + (lane & 15));
+      }
+#pragma unroll 1
+      for (int i = 0; 16 * i < rows; ++i, x = x1)
+        store_query(x, flip, smem + L::q, smem + L::sfq, 16 * i + 2 * warp + (lane >> 4), rows, lane & 15);
       fence_proxy_async_shared();
       warp_arrive(&ctl->q_full, lane);
     };
@@ -285,7 +315,6 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
       warp_arrive(&ctl->vote[h], lane);
       return wait(c, &ctl->vote[h], votes++ & 1u, 11u);
     };
-    uint32_t g_phase = 0;
     auto meet_all = [&]() -> bool {
       warp_arrive(&ctl->group, lane);
       const bool r = wait(c, &ctl->group, g_phase, 13u);
@@ -293,142 +322,148 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
       return r;
     };
     Ring<2> it;
+    int turn = 0;  // which of the scales is in use
     bool ok = wait(c, &ctl->it_full[0], 0, 4u);
     if (ok) queries(0);
 #pragma unroll 1
     while (ok) {
-      float2 l[8], l1[8];  // the thread's sums, of a second group of rows too
+      float2 l[8];  // the thread's sums
 #pragma unroll
-      for (int i = 0; i < 8; ++i) l[i] = l1[i] = make_float2(0.f, 0.f);
-      int turn = 0, turn1 = 0;  // which of the scales is in use
+      for (int i = 0; i < 8; ++i) l[i] = make_float2(0.f, 0.f);
       const int groups = (ctl->item[it.slot].rows + 15) >> 4;
       {
         const Item& w = ctl->item[it.slot];  // given back at the item's end
         if (w.t0 == w.t1) break;
-        const int t0 = w.t0, t1 = w.t1;
-        // all rows see the tokens lo .. hi - 1
-        const int base = w.len - w.n + 1, hi = base + w.r0 / a.G,
-                  lo = a.window > 0 ? base + (w.r0 + w.rows - 1) / a.G - a.window : 0;
+        const int t1 = w.t1, hi = w.len - w.n + 1 + w.r0 / a.G,  // all rows see the tokens lo .. hi - 1
+                  lo = a.window > 0 ? w.len - w.n + 1 + (w.r0 + w.rows - 1) / a.G - a.window : 0;
+        turn ^= 1;
+        if (lane < 16) ctl->scale[turn][16 * h + lane] = kNone;  // (every warp of the row writes the same)
+        __syncwarp();
 #pragma unroll 1
-        for (int k = t0; k < t1; ++k, ++n) {
+        for (int k0 = w.t0; k0 < t1; k0 += 2, ++n) {
           const uint32_t buf = n & 1u, phase = (n >> 1) & 1u;
-          const bool fresh = k == t0, masked = k * kKeys < lo || (k + 1) * kKeys > hi;
-          ok = wait(c, &ctl->s_full[buf], phase, 10u);
+          const int k1 = min(k0 + 2, t1);
+          ok = wait(c, &ctl->s_full[buf], phase, 10u) && wait(c, &ctl->p_free[buf], phase ^ 1u, 12u);
           if (!ok) break;
           tc_fence_after();
-          if (h >= groups) warp_arrive(&ctl->s_free[buf], lane);
-#pragma unroll 1
-          for (int g = h; g < groups; g += 2) {
-            float2 s[8];
-            {
+          if (h < groups) {
+            // the scores of tile k (not yet scaled)
+            auto scores = [&](int k, float2(&s)[8]) {
+              const uint32_t S = tmem + lanes + kColS * (2 * buf + (k - k0)) + 16 * h;
               float x[16], y[16];
-              const uint32_t S = tmem + lanes + kColS * buf + 16 * g;
               tmem_ld16f(S, x);
               tmem_ld16f(S + 16 * groups, y);
               tmem_ld_wait();
-              if (g + 2 >= groups) {
-                tc_fence_before();
-                warp_arrive(&ctl->s_free[buf], lane);
-              }
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 s[i] = __fadd2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(y[2 * i], y[2 * i + 1]));
-            }
-            if (masked) {
-              const int r = w.r0 + 16 * g, tok = k * kKeys + key;
-              int upto = base + r / a.G, in = r % a.G;
+              if (k * kKeys < lo || (k + 1) * kKeys > hi) {
+                const int r = w.r0 + 16 * h, tok = k * kKeys + key;
+                int upto = w.len - w.n + 1 + r / a.G, in = r % a.G;
+                uint32_t hide = 0;
+#pragma unroll 1
+                for (int i = 0; i < 16; ++i) {
+                  const int u = min(upto, w.len);
+                  if (tok >= u || (a.window > 0 && tok < u - a.window)) hide |= 1u << i;
+                  if (++in == a.G) in = 0, ++upto;
+                }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int u = min(upto, w.len);
-                if (tok >= u || (a.window > 0 && tok < u - a.window)) (i & 1 ? s[i >> 1].y : s[i >> 1].x) = -INFINITY;
-                if (++in == a.G) in = 0, ++upto;
-              }
-            }
-            float* ms = ctl->scale[turn] + 16 * g;
-            uint32_t p[8];
-            float2 e[8];
-            float top = -INFINITY;
-            auto probs = [&]() {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float4 m4 = *reinterpret_cast<const float4*>(ms + 4 * i);
-                e[2 * i] = __ffma2_rn(s[2 * i], make_float2(scale, scale), make_float2(-m4.x, -m4.y));
-                e[2 * i + 1] = __ffma2_rn(s[2 * i + 1], make_float2(scale, scale), make_float2(-m4.z, -m4.w));
-              }
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                top = max3(top, e[i].x, e[i].y);
-                e[i].x = exp2_fast(e[i].x), e[i].y = exp2_fast(e[i].y);
-                p[i] = bf16x2_rn(e[i].x, e[i].y);
+                for (int i = 0; i < 8; ++i) {
+                  if (hide & (1u << (2 * i))) s[i].x = -INFINITY;
+                  if (hide & (2u << (2 * i))) s[i].y = -INFINITY;
+                }
               }
             };
-            if (!fresh) {
-              probs();
-              if (__any_sync(0xFFFFFFFFu, live && top > kGrow) && lane == 0)
-                *reinterpret_cast<volatile uint32_t*>(&ctl->grown[h]) = votes + 1u;
-            }
-            ok = meet();
-            if (!ok) break;
-            if (fresh || *reinterpret_cast<volatile uint32_t*>(&ctl->grown[h]) == votes) {
+            float2 add[8];
+#pragma unroll 1
+            for (bool again = false;; again = true) {
+              const float4* ms = reinterpret_cast<const float4*>(ctl->scale[turn] + 16 * h);
+              float top = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) add[i] = make_float2(0.f, 0.f);
+#pragma unroll 1
+              for (int k = k0; k < k1; ++k) {
+                float2 s[8];
+                uint32_t p[8];
+                scores(k, s);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float4 m = ms[i];
+                  s[2 * i] = __ffma2_rn(s[2 * i], make_float2(scale, scale), make_float2(-m.x, -m.y));
+                  s[2 * i + 1] = __ffma2_rn(s[2 * i + 1], make_float2(scale, scale), make_float2(-m.z, -m.w));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  top = max3(top, s[i].x, s[i].y);
+                  s[i].x = exp2_fast(s[i].x), s[i].y = exp2_fast(s[i].y);
+                  add[i] = __fadd2_rn(add[i], s[i]);
+                  p[i] = bf16x2_rn(s[i].x, s[i].y);
+                }
+                if (live) {
+                  uint8_t* d = smem + (prow + (2 * buf + (k - k0)) * kProbs);
+                  *reinterpret_cast<uint4*>(d) = make_uint4(p[0], p[1], p[2], p[3]);
+                  *reinterpret_cast<uint4*>(smem + ((prow ^ 16u) + (2 * buf + (k - k0)) * kProbs)) =
+                      make_uint4(p[4], p[5], p[6], p[7]);
+                }
+              }
+              if (again) break;
+              volatile uint32_t* grown = &ctl->grown[h];
+              if (__any_sync(0xFFFFFFFFu, live && top > kGrow) && lane == 0) *grown = votes + 1u;
+              ok = meet();
+              if (!ok || *grown != votes) break;
               // the rows' maxima, and what has been added up so far in the new unit
               float x[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = live ? (i & 1 ? s[i >> 1].y : s[i >> 1].x) * scale : -INFINITY;
-              const float mx = across<false>(x, lane);
+              for (int i = 0; i < 16; ++i) x[i] = -INFINITY;
+#pragma unroll 1
+              for (int k = k0; k < k1; ++k) {
+                float2 s[8];
+                scores(k, s);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = fmaxf(x[i], live ? (i & 1 ? s[i >> 1].y : s[i >> 1].x) : -INFINITY);
+              }
+              const float mx = across<false>(x, lane) * scale;
               if ((lane & 1) == 0) ctl->peak[h][wl][lane >> 1] = mx;
               ok = meet();
               if (!ok) break;
-              float* mn = ctl->scale[turn ^ 1] + 16 * g;
               if (lane < 16) {  // (every warp of the row writes the same)
                 const float(*pk)[16] = ctl->peak[h];
-                const float m = fmaxf(max3(pk[0][lane], pk[1][lane], pk[2][lane]), pk[3][lane]), mo = fresh ? kNone : ms[lane];
-                mn[lane] = m > mo + kGrow ? m : mo;
+                const float m = fmaxf(max3(pk[0][lane], pk[1][lane], pk[2][lane]), pk[3][lane]),
+                            mo = ctl->scale[turn][16 * h + lane], mn = m > mo + kGrow ? m : mo;
+                ctl->scale[turn ^ 1][16 * h + lane] = mn;
+                ctl->fall[16 * h + lane] = exp2_fast(mo - mn);
               }
+              turn ^= 1;
               __syncwarp();
-              if (!fresh) {
+              if (k0 > w.t0) {
                 ok = wait(c, &ctl->p_free[buf ^ 1u], ((n - 1u) >> 1) & 1u, 11u);
                 if (!ok) break;
                 tc_fence_after();
-                float o[16];
-                uint32_t v[16];
-                tmem_ld16f(tmem + lanes + kColO + 16 * g, o);
-                tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float al = exp2_fast(ms[i] - mn[i]);
-                  (i & 1 ? l[i >> 1].y : l[i >> 1].x) *= al;
-                  v[i] = __float_as_uint(o[i] * al);
+                for (int i = 0; i < 4; ++i) {
+                  const float4 f = *reinterpret_cast<const float4*>(ctl->fall + 16 * h + 4 * i);
+                  const uint32_t O = tmem + lanes + kColO + 16 * h + 4 * i;
+                  float o[4];
+                  tmem_ld4(O, o);
+                  tmem_ld_wait();
+                  tmem_st4(O, __float_as_uint(o[0] * f.x), __float_as_uint(o[1] * f.y), __float_as_uint(o[2] * f.z),
+                           __float_as_uint(o[3] * f.w));
+                  l[2 * i].x *= f.x, l[2 * i].y *= f.y, l[2 * i + 1].x *= f.z, l[2 * i + 1].y *= f.w;
                 }
-                tmem_st16(tmem + lanes + kColO + 16 * g, v);
                 tmem_st_wait();
-                tc_fence_before();
               }
-              turn ^= 1;
-              ms = mn;
-              probs();
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) l[i] = __fadd2_rn(l[i], e[i]);
-            ok = wait(c, &ctl->p_free[buf], phase ^ 1u, 12u);
             if (!ok) break;
-            if (live) {
-              uint4* d = reinterpret_cast<uint4*>(prow + buf * kProbs);
-              d[(2 * g) ^ (key & 7)] = make_uint4(p[0], p[1], p[2], p[3]);
-              d[(2 * g + 1) ^ (key & 7)] = make_uint4(p[4], p[5], p[6], p[7]);
-            }
-            if (h + 2 < groups) {  // the other group of the warp comes next
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 x = l[i];
-                l[i] = l1[i], l1[i] = x;
-              }
-              const int x = turn;
-              turn = turn1, turn1 = x;
-            }
+            for (int i = 0; i < 8; ++i) l[i] = __fadd2_rn(l[i], add[i]);
           }
-          if (!ok) break;
+          tc_fence_before();
           fence_proxy_async_shared();
-          warp_arrive(&ctl->p_full[buf], lane);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ctl->s_free[buf]);
+            mbar_arrive(&ctl->p_full[buf]);
+          }
         }
       }
       if (!ok) break;
@@ -438,54 +473,50 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
       ok = wait(c, &ctl->it_full[it.slot], it.phase, 4u);
       if (!ok) break;
       queries(it.slot);
-      // the rows' sums
-#pragma unroll 1
-      for (int g = h; g < groups; g += 2) {
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 s = g == h ? l[i >> 1] : l1[i >> 1];
-          x[i] = live ? (i & 1 ? s.y : s.x) : 0.f;
-        }
-        const float sum = across<true>(x, lane);
-        if ((lane & 1) == 0) ctl->sums[wl][16 * g + (lane >> 1)] = sum;
-      }
-      ok = meet() && wait(c, &ctl->p_free[(n - 1u) & 1u], ((n - 1u) >> 1) & 1u, 11u);
-      if (!ok) break;
-      tc_fence_after();
       const Item& w = ctl->item[slot];
       const bool whole = w.whole;
-      const size_t rec = whole ? 0 : static_cast<size_t>(chunk::part_slot(w, ctl->ranges, blockIdx.x)) * a.slot_rows;
-#pragma unroll 1
-      for (int g = h; g < groups; g += 2) {
-        const int r = 16 * g + (lane & 15);
+      if (h < groups) {
+        // the rows' sums
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = live ? (i & 1 ? l[i >> 1].y : l[i >> 1].x) : 0.f;
+        const float part = across<true>(x, lane);
+        if ((lane & 1) == 0) ctl->sums[wl][16 * h + (lane >> 1)] = part;
+        ok = meet() && wait(c, &ctl->p_free[(n - 1u) & 1u], ((n - 1u) >> 1) & 1u, 11u);
+        if (!ok) break;
+        tc_fence_after();
+        const int r = 16 * h + (lane & 15);
         const float sum = (ctl->sums[0][r] + ctl->sums[1][r]) + (ctl->sums[2][r] + ctl->sums[3][r]);
-        const float m = ctl->scale[g == h ? turn : turn1][r];
+        const float m = ctl->scale[turn][r];
         const float f = whole ? (sum > 0.f ? 1.f / sum : 0.f) : m == kNone ? 0.f : 1.f;
+        const size_t rec = whole ? 0 : static_cast<size_t>(w.slot) * a.slot_rows;
         if (!whole && wl == 0 && lane < 16 && r < w.rows)
           a.rec_ml[rec + r] = make_float2(m == kNone ? -INFINITY : m, sum);
-        float o[16];
-        tmem_ld16f(tmem + lanes + kColO + 16 * g, o);
-        tmem_ld_wait();
-        const int rr = w.r0 + 16 * g, left = w.rows - 16 * g;
-        int tok = rr / a.G, in = rr - tok * a.G;
         const int dim = (key & ~3) | ((key & 1) << 1) | ((key >> 1) & 1);  // stored order 0, 2, 1, 3
+        const int rr = w.r0 + 16 * h, left = w.rows - 16 * h;
+        int tok = rr / a.G, in = rr - tok * a.G;
         uint16_t* y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + in) * kD + dim;
-        float* z = a.rec + (rec + 16 * g) * kD + key;
+        float* z = a.rec + (rec + 16 * h) * kD + key;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 16; i0 += 4) {
+          float o[4];
+          tmem_ld4(tmem + lanes + kColO + 16 * h + i0, o);
+          tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float fi = __shfl_sync(0xFFFFFFFFu, f, i), v = fi != 0.f ? fi * o[i] : 0.f;
-          if (i < left) {
-            if (whole)
-              *y = static_cast<uint16_t>(bf16x2_rn(v, 0.f));
-            else
-              z[i * kD] = v;
+          for (int i = 0; i < 4; ++i) {
+            const float fi = __shfl_sync(0xFFFFFFFFu, f, i0 + i), v = fi != 0.f ? fi * o[i] : 0.f;
+            if (i0 + i < left) {
+              if (whole)
+                *y = static_cast<uint16_t>(bf16x2_rn(v, 0.f));
+              else
+                *z = v;
+            }
+            z += kD, y += kD;
+            if (++in == a.G) in = 0, y += a.ldo - static_cast<long long>(a.G) * kD;
           }
-          y += kD;
-          if (++in == a.G) in = 0, y += a.ldo - static_cast<long long>(a.G) * kD;
         }
+        tc_fence_before();
       }
-      tc_fence_before();
       if (!whole) {
         // the last part to arrive adds them up, in the blocks' order
         __threadfence();

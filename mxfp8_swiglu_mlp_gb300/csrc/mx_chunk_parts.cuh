@@ -20,7 +20,6 @@ constexpr uint32_t kCodes = kKeys * kD;        // bytes of a K or V tile of code
 constexpr uint32_t kScales = 512;              // bytes kept for a tile's scales
 constexpr uint32_t kOperand = kKeys * kD * 2;  // V as bf16: two halves of 64 dimensions,
 constexpr uint32_t kHalf = kOperand / 2;       // [tokens][128 bytes], 128-byte swizzle
-constexpr int kSlots = 2;                      // bf16 V tiles
 constexpr float kGrow = 8.f;                   // in powers of two
 static_assert(kKeys % 16 == 0 && kCodes % 1024 == 0, "16-token groups, whole swizzle atoms");
 
@@ -298,7 +297,7 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, const uint8_t* 
 }
 
 // The role of the convert warps, thread ct of them.
-template <int NV, class Ctl>
+template <int NV, int kSlots, class Ctl>
 __device__ __forceinline__ void convert_items(const Ctx& c, Ctl* ctl, const uint8_t* raw, const uint8_t* sv, uint8_t* v,
                                               int ct, int lane) {
   Ring<2> it;
@@ -328,64 +327,41 @@ __device__ __forceinline__ void convert_items(const Ctx& c, Ctl* ctl, const uint
 }
 
 // ---------------------------------------------------------------- queries
-// Rows first .. first + rows - 1 of a query operand (row i is row r0 + i of the
-// sequence; the last one stands in for rows past the end) as two E4M3 terms
-// with their scales, the second `lo` rows further on, by `warps` warps (rows a
-// multiple of 16; not ragged: of 8 * warps).  Four lanes hold a block of 32
-// dimensions.
 // Where an operand keeps row r's scales: tiles of 128 rows, as tcgen05.cp wants them.
 __device__ __forceinline__ int scale_at(int r) { return (r >> 7) * static_cast<int>(kScales) + (r & 31) * 16 + ((r >> 5) & 3) * 4; }
-template <int warps, bool ragged>
-__device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item& w, int r0, uint8_t* codes, uint8_t* sf,
-                                             int first, int rows, int lo, int warp, int lane) {
-  const int R = w.n * a.G;
-  const uint32_t flip = a.negate ? 0x80008000u : 0u;
-  const int c = lane & 15;  // the lane's 8 dimensions
-#pragma unroll 1
-  for (int i0 = warp * 2 + (lane >> 4); i0 < rows; i0 += 8 * warps) {
-   uint4 xs[4];
+// 8 dimensions (piece c of 16) of row r of a query operand as two E4M3 terms
+// with their scales, the second `lo` rows further on.  Four lanes hold a block
+// of 32 dimensions.
+__device__ __forceinline__ void store_query(uint4 x, uint32_t flip, uint8_t* codes, uint8_t* sf, int r, int lo, int c) {
+  const uint32_t u[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
+  uint32_t am = 0;
 #pragma unroll
-   for (int k = 0; k < 4; ++k) {
-    const int rr = min(r0 + first + i0 + 2 * warps * k, R - 1), tok = rr / a.G;
-    xs[k] = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<long long>(w.c0 + tok) * a.ldq +
-                                                 (w.hk * a.G + rr - tok * a.G) * kD) + c);
-   }
+  for (int k = 0; k < 4; ++k) am = __vmaxu2(am, u[k] & 0x7FFF7FFFu);
+  am = max(am & 0xFFFFu, am >> 16);
+  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+  // the largest below 2^8 in units of the first scale: nothing saturates, and
+  // the rest is at most 2^3 of them, four bits again
+  const int e = static_cast<int>(am >> 7);
+  const uint32_t s0 = static_cast<uint32_t>(max(e - 7, 0)), s1 = static_cast<uint32_t>(max(e - 11, 0));
+  const float i0 = inv_scale_from_ue8m0(s0), i1 = inv_scale_from_ue8m0(s1);
+  const float back = s0 != 0 ? __uint_as_float(s0 << 23) : __uint_as_float(0x00400000u);
+  uint32_t h[2], l[2];
 #pragma unroll
-   for (int k0 = 0; k0 < 4; ++k0) {
-    if (ragged && i0 + 2 * warps * k0 >= rows) break;
-    const int r = first + i0 + 2 * warps * k0;
-    const uint4 x = xs[k0];
-    const uint32_t u[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
-    uint32_t am = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) am = __vmaxu2(am, u[k] & 0x7FFF7FFFu);
-    am = max(am & 0xFFFFu, am >> 16);
-    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-    // the largest below 2^8 in units of the first scale: nothing saturates, and
-    // the rest is at most 2^3 of them, four bits again
-    const int e = static_cast<int>(am >> 7);
-    const uint32_t s0 = static_cast<uint32_t>(max(e - 7, 0)), s1 = static_cast<uint32_t>(max(e - 11, 0));
-    const float i0 = inv_scale_from_ue8m0(s0), i1 = inv_scale_from_ue8m0(s1);
-    const float back = s0 != 0 ? __uint_as_float(s0 << 23) : __uint_as_float(0x00400000u);
-    uint32_t h[2], l[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float v0 = bf16_lo(u[2 * k]), v1 = bf16_hi(u[2 * k]), v2 = bf16_lo(u[2 * k + 1]), v3 = bf16_hi(u[2 * k + 1]);
-      h[k] = e4m3x4_code(v0 * i0, v1 * i0, v2 * i0, v3 * i0);
-      const __nv_fp8x4_e4m3* hc = reinterpret_cast<const __nv_fp8x4_e4m3*>(&h[k]);
-      const float4 hv = static_cast<float4>(*hc);
-      l[k] = e4m3x4_code(fmaf(-hv.x, back, v0) * i1, fmaf(-hv.y, back, v1) * i1, fmaf(-hv.z, back, v2) * i1,
-                         fmaf(-hv.w, back, v3) * i1);
-    }
-    uint8_t* d = codes + r * 128 + ((((c >> 1) ^ (r & 7)) << 4) | ((c & 1) << 3));
-    *reinterpret_cast<uint2*>(d) = make_uint2(h[0], h[1]);
-    *reinterpret_cast<uint2*>(d + lo * 128) = make_uint2(l[0], l[1]);
-    if ((c & 3) == 0) {
-      sf[scale_at(r) + (c >> 2)] = static_cast<uint8_t>(s0);
-      sf[scale_at(r + lo) + (c >> 2)] = static_cast<uint8_t>(s1);
-    }
-   }
+  for (int k = 0; k < 2; ++k) {
+    const float v0 = bf16_lo(u[2 * k]), v1 = bf16_hi(u[2 * k]), v2 = bf16_lo(u[2 * k + 1]), v3 = bf16_hi(u[2 * k + 1]);
+    h[k] = e4m3x4_code(v0 * i0, v1 * i0, v2 * i0, v3 * i0);
+    const __nv_fp8x4_e4m3* hc = reinterpret_cast<const __nv_fp8x4_e4m3*>(&h[k]);
+    const float4 hv = static_cast<float4>(*hc);
+    l[k] = e4m3x4_code(fmaf(-hv.x, back, v0) * i1, fmaf(-hv.y, back, v1) * i1, fmaf(-hv.z, back, v2) * i1,
+                       fmaf(-hv.w, back, v3) * i1);
+  }
+  uint8_t* d = codes + r * 128 + ((((c >> 1) ^ (r & 7)) << 4) | ((c & 1) << 3));
+  *reinterpret_cast<uint2*>(d) = make_uint2(h[0], h[1]);
+  *reinterpret_cast<uint2*>(d + lo * 128) = make_uint2(l[0], l[1]);
+  if ((c & 3) == 0) {
+    sf[scale_at(r) + (c >> 2)] = static_cast<uint8_t>(s0);
+    sf[scale_at(r + lo) + (c >> 2)] = static_cast<uint8_t>(s1);
   }
 }
 

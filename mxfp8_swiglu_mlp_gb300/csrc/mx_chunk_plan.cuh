@@ -86,7 +86,8 @@ __device__ __forceinline__ long long seq_units(const ChunkArgs& a, const Seq& s,
 // Key tiles of a query tile (nt of them, cost w each) that lie before unit y of it.
 __device__ __forceinline__ int tiles_before(long long y, int nt, int w) {
   if (y <= kTileCost) return 0;
-  const long long t = (y - kTileCost + w - 1) / w;
+  y += w - 1 - kTileCost;
+  const long long t = w == kPairCost ? y / kPairCost : y / kHalfCost;
   return t < nt ? static_cast<int>(t) : nt;
 }
 
@@ -117,6 +118,7 @@ struct Item {
   int tb, nt;             // key tiles of the tile
   int first, last;        // blocks that have a share of the tile
   int parts;              // how many of them have a key tile
+  int slot;               // where the part's results go (unless it is the whole tile)
   long long x;            // unit at which the tile begins
 };
 // Block c's part of the tile: its slot, or -1 when it has no key tile.
@@ -148,7 +150,7 @@ __device__ inline long long all_units(const ChunkArgs& a, int qs, int rs, long l
 // A warp's way through its block's range.
 struct Walk {
   Ranges r;
-  int qs, rs;
+  int qs, rs, block;
   long long x, end;      // where it is, where the range ends
   long long head;        // unit at which the current KV head began (the tile's units follow)
   long long at;          // unit at which the current query tile begins
@@ -156,8 +158,8 @@ struct Walk {
   Seq s;
   Tiles t;
 
-  __device__ inline void init(const ChunkArgs& a, const Ranges& rr, int block, int qs_, int rs_, int lane) {
-    r = rr, qs = qs_, rs = rs_;
+  __device__ inline void init(const ChunkArgs& a, const Ranges& rr, int block_, int qs_, int rs_, int lane) {
+    r = rr, qs = qs_, rs = rs_, block = block_;
     b = a.B;
     x = end = 0;
     if (block >= r.blocks) return;
@@ -223,8 +225,10 @@ struct Walk {
       w.t0 = w.tb + p0, w.t1 = w.tb + p1;
       w.whole = p0 == 0 && p1 == w.nt;
       w.parts = 1;
+      w.slot = -1;
       if (!w.whole) {
         w.first = r.block_of(w.x), w.last = r.block_of(stop - 1);
+        w.slot = part_slot(w, r, block);
         w.parts = 0;
         for (int c = w.first; c <= w.last; c += 32)
           w.parts += __popc(__ballot_sync(0xFFFFFFFFu, c + lane <= w.last && part_slot(w, r, c + lane) >= 0));
