@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
           if (!ok) break;
           g_phase ^= 1u;
           if (row == 0) {
-            uint32_t* count = a.count + 2 * w.first + m;
+            uint32_t* count = a.count + kChunkCounters * w.first + m;
             const bool last = atomicAdd(count, 1u) == static_cast<uint32_t>(w.parts) - 1u;
             if (last) *count = 0u;
             ctl->last[m] = last;

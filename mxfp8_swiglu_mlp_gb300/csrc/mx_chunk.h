@@ -11,7 +11,8 @@ constexpr int kChunkD = 128;            // head dimension
 constexpr int kChunkMaxGroup = 64;      // query heads per KV head
 constexpr int kChunkFewRows = 32;       // rows of a query tile of the kernel for few rows
 constexpr size_t kChunkHeaderBytes = 256;
-constexpr size_t kChunkCounterBytes = 4096;  // two counters a block, blocks <= 256
+constexpr int kChunkCounters = 8;       // of a block: parts of a query tile that have arrived, by warp or stream
+constexpr size_t kChunkCounterBytes = 256 * kChunkCounters * sizeof(uint32_t);  // blocks <= 256
 
 struct ChunkArgs {
   CUtensorMap tm_k;           // K codes as [num_pages * Hkv * P, 128] bytes, boxes of 16 rows, 128-byte swizzle
@@ -23,7 +24,7 @@ struct ChunkArgs {
   const int32_t* cu;          // [B + 1]
   const int32_t* lens;        // [B]
   uint32_t* status;           // first error (status << 24 | site << 16 | sequence)
-  uint32_t* count;            // [2 * grid] parts of a query tile that have arrived (zero between calls)
+  uint32_t* count;            // [grid][kChunkCounters] (zero between calls)
   float* rec;                 // [2 * grid] unnormalised outputs of parts: [128][slot_rows], for few rows [slot_rows][128]
   float2* rec_ml;             // [2 * grid][slot_rows] running maximum (base 2) and sum
   int slot_rows;

@@ -50,16 +50,16 @@ struct Ctl {
   uint64_t k_full[NK], k_empty[NK], r_full[NV], r_empty[NV];  // rings of K and V codes
   uint64_t v_full[kSlots], v_empty[kSlots];
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2];  // two tiles each, by turns
-  uint64_t q_full, vote[2], group, fin[2], it_full[2], it_empty[2];
+  uint64_t q_full, vote[2], fin[2], it_full[2], it_empty[2];
   Item item[2];
-  float scale[2][kRows];     // the rows' scales (base 2), the one in use by turns
-  float fall[kRows];         // what the last change of scale makes of a row
+  alignas(16) float scale[2][kRows];     // the rows' scales (base 2), the one in use by turns
+  alignas(16) float fall[kRows];         // what the last change of scale makes of a row
   float peak[2][4][16];      // a group's maxima, of each warp
   float sums[4][kRows];
   uint32_t grown[2];         // the last vote that found a larger score
   long long red[kBlock / 32];
   chunk::Ranges ranges;
-  uint32_t tmem, stop, last;
+  uint32_t tmem, stop;
 };
 struct L {
   static constexpr uint32_t q = 0, v = 2 * kRows * kD, p = v + kSlots * kOperand, k = p + 4 * kProbs, raw = k + NK * kCodes,
@@ -67,6 +67,7 @@ struct L {
                             ctl = sfq + kScales, bytes = ctl + sizeof(Ctl);
 };
 static_assert(L::bytes <= 232448 && NK <= 5 && NV <= 4, "shared memory");
+static_assert(L::ctl % 16 == 0 && alignof(Ctl) == 16 && L::p % 1024 == 0 && L::v % 1024 == 0 && L::k % 1024 == 0, "alignment");
 static_assert(NV * kCodes >= 16 * kD, "the 128-row product reads 16 rows behind the last K tile");
 
 // kind::f16, fp32 sums, bf16 operands, M = 128 (M-major, bit 15), N = 32 (N-major, bit 16).
@@ -102,46 +103,59 @@ __device__ __forceinline__ float across(float (&v)[16], int lane) {
   return both(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
 }
 
-// One row of a query tile added up over the tile's parts, in the blocks' order,
-// by a warp: four (stored) dimensions a lane.
-__device__ __forceinline__ void merge_row(const ChunkArgs& a, const Item& w, const chunk::Ranges& rg, int row, int lane) {
-  const int blocks = w.last - w.first + 1;
-  auto part = [&](int p, float2& ml) {  // the lane's part: its slot, maximum and sum
-    const int sl = p < blocks ? chunk::part_slot(w, rg, w.first + p) : -1;
-    ml = sl >= 0 ? __ldcg(&a.rec_ml[static_cast<size_t>(sl) * a.slot_rows + row]) : make_float2(-INFINITY, 0.f);
-    return sl;
+// A warp's share (16 rows from row0 on, the 32 stored dimensions from dim0 on) of
+// a query tile added up over the tile's parts, in the blocks' order.  A lane has
+// four dimensions of every fourth row.
+__device__ __forceinline__ void merge_share(const ChunkArgs& a, const Item& w, const chunk::Ranges& rg, int row0, int dim0,
+                                            int lane) {
+  const int blocks = w.last - w.first + 1, dim = dim0 + 4 * (lane & 7);
+  int slots = -1, from = -32;  // slots of the parts from .. from + 31, one a lane
+  auto slot_of = [&](int p) -> size_t {
+    if (p >= from + 32 || p < from) {
+      from = p & ~31;
+      slots = from + lane < blocks ? chunk::part_slot(w, rg, w.first + from + lane) : -1;
+    }
+    return static_cast<size_t>(static_cast<long long>(__shfl_sync(0xFFFFFFFFu, slots, p & 31)) * a.slot_rows);
   };
-  float2 ml;
-  float M = -INFINITY;
-  for (int base = 0; base < blocks; base += 32) {
-    part(base + lane, ml);
-    M = fmaxf(M, ml.x);
+  const size_t none = static_cast<size_t>(-static_cast<long long>(a.slot_rows));
+  float M = -INFINITY;  // of row lane % 16
+#pragma unroll 1
+  for (int p = 0; p < blocks; ++p) {
+    const size_t at = slot_of(p);
+    if (at != none) M = fmaxf(M, __ldcg(&a.rec_ml[at + min(row0 + (lane & 15), w.rows - 1)].x));
   }
+  float den[4];
+  float4 o[4];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  float den = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int base = 0; base < blocks; base += 32) {
-    const int sl = part(base + lane, ml);
-    const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
-    den = fmaf(f, ml.y, den);
-    const int n = min(32, blocks - base);
-#pragma unroll 2
-    for (int p = 0; p < n; ++p) {
-      const int slp = __shfl_sync(0xFFFFFFFFu, sl, p);
-      const float fp = __shfl_sync(0xFFFFFFFFu, f, p);
-      if (fp == 0.f) continue;
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.rec + (static_cast<size_t>(slp) * a.slot_rows + row) * kD) + lane);
-      o.x = fmaf(fp, x.x, o.x), o.y = fmaf(fp, x.y, o.y), o.z = fmaf(fp, x.z, o.z), o.w = fmaf(fp, x.w, o.w);
+  for (int i = 0; i < 4; ++i) den[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int p = 0; p < blocks; ++p) {
+    const size_t at = slot_of(p);
+    if (at == none) continue;
+    float2 ml[4];
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = min(row0 + 4 * i + (lane >> 3), w.rows - 1);
+      ml[i] = __ldcg(&a.rec_ml[at + row]);
+      x[i] = __ldcg(reinterpret_cast<const float4*>(a.rec + (at + row) * kD + dim));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float m = __shfl_sync(0xFFFFFFFFu, M, 4 * i + (lane >> 3)), f = ml[i].x == -INFINITY ? 0.f : exp2_fast(ml[i].x - m);
+      den[i] = fmaf(f, ml[i].y, den[i]);
+      o[i].x = fmaf(f, x[i].x, o[i].x), o[i].y = fmaf(f, x[i].y, o[i].y);
+      o[i].z = fmaf(f, x[i].z, o[i].z), o[i].w = fmaf(f, x[i].w, o[i].w);
     }
   }
 #pragma unroll
-  for (int s = 16; s; s >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, s);
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  const int rr = w.r0 + row, tok = rr / a.G;
-  uint16_t* y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
-  // (stored order 0, 2, 1, 3)
-  *reinterpret_cast<uint2*>(y + 4 * lane) = make_uint2(bf16x2_rn(o.x * inv, o.z * inv), bf16x2_rn(o.y * inv, o.w * inv));
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 4 * i + (lane >> 3), rr = w.r0 + row, tok = rr / a.G;
+    const float inv = den[i] > 0.f ? 1.f / den[i] : 0.f;
+    if (row < w.rows)  // (stored order 0, 2, 1, 3)
+      *reinterpret_cast<uint2*>(a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD + dim) =
+          make_uint2(bf16x2_rn(o[i].x * inv, o[i].z * inv), bf16x2_rn(o[i].y * inv, o[i].w * inv));
+  }
 }
 
 __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_constant__ ChunkArgs a) {
@@ -179,7 +193,6 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
       ctl->grown[i] = 0u;
     }
     mbar_init(&ctl->q_full, kSoftWarps);
-    mbar_init(&ctl->group, kSoftWarps);
     ctl->stop = 0u;
     mbar_fence_init();
   }
@@ -291,7 +304,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
     const float scale = a.scale_log2;
     // the key's probabilities in a tile's buffer: 16-byte pieces 2 h and 2 h + 1
     const uint32_t prow = L::p + key * 64 + ((2 * h ^ ((key >> 1) & 3)) << 4);
-    uint32_t n = 0, votes = 0, g_phase = 0;  // pairs of key tiles, votes so far
+    uint32_t n = 0, votes = 0;  // pairs of key tiles, votes so far
     auto queries = [&](int slot) {
       const Item& w = ctl->item[slot];
       if (w.t0 == w.t1) return;
@@ -314,12 +327,6 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
     auto meet = [&]() -> bool {  // the warps of a row
       warp_arrive(&ctl->vote[h], lane);
       return wait(c, &ctl->vote[h], votes++ & 1u, 11u);
-    };
-    auto meet_all = [&]() -> bool {
-      warp_arrive(&ctl->group, lane);
-      const bool r = wait(c, &ctl->group, g_phase, 13u);
-      g_phase ^= 1u;
-      return r;
     };
     Ring<2> it;
     int turn = 0;  // which of the scales is in use
@@ -490,7 +497,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
         const float m = ctl->scale[turn][r];
         const float f = whole ? (sum > 0.f ? 1.f / sum : 0.f) : m == kNone ? 0.f : 1.f;
         const size_t rec = whole ? 0 : static_cast<size_t>(w.slot) * a.slot_rows;
-        if (!whole && wl == 0 && lane < 16 && r < w.rows)
+        if (!whole && lane < 16 && r < w.rows)  // (all four warps write the same)
           a.rec_ml[rec + r] = make_float2(m == kNone ? -INFINITY : m, sum);
         const int dim = (key & ~3) | ((key & 1) << 1) | ((key >> 1) & 1);  // stored order 0, 2, 1, 3
         const int rr = w.r0 + 16 * h, left = w.rows - 16 * h;
@@ -517,22 +524,18 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
         }
         tc_fence_before();
       }
-      if (!whole) {
-        // the last part to arrive adds them up, in the blocks' order
+      if (!whole && h < groups) {
+        // Of each warp, the last part's to arrive adds the parts up: it needs
+        // what the same warps of the other blocks wrote, no more.
         __threadfence();
-        ok = meet_all();
-        if (!ok) break;
-        if (t == 0) {
-          uint32_t* count = a.count + 2 * w.first;
-          const bool last = atomicAdd(count, 1u) == static_cast<uint32_t>(w.parts) - 1u;
-          if (last) *count = 0u;
-          ctl->last = last;
+        __syncwarp();
+        uint32_t* count = a.count + kChunkCounters * w.first + warp;
+        const uint32_t before = __shfl_sync(0xFFFFFFFFu, lane == 0 ? atomicAdd(count, 1u) : 0u, 0);
+        if (before == static_cast<uint32_t>(w.parts) - 1u) {
+          if (lane == 0) *count = 0u;
           __threadfence();
+          merge_share(a, w, ctl->ranges, 16 * h, 32 * wl, lane);
         }
-        ok = meet_all();
-        if (!ok) break;
-        if (ctl->last)
-          for (int row = warp; row < w.rows; row += kSoftWarps) merge_row(a, w, ctl->ranges, row, lane);
       }
       warp_arrive(&ctl->it_empty[slot], lane);
     }

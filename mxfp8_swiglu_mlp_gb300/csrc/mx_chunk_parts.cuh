@@ -244,7 +244,16 @@ __device__ __forceinline__ void load_items(const Ctx& c, Ctl* ctl, uint8_t* k, u
     Item& w = ctl->item[it.slot];
     if (!ld.v) {
       Item next;
-      if (!walk.next(a, lane, next)) next.t0 = next.t1 = 0;
+      if (!walk.next(a, lane, next)) {
+        next.t0 = next.t1 = 0;
+      } else {  // its queries on their way to L2
+        for (int r = lane; r < next.rows; r += 32) {
+          const int rr = next.r0 + r, tok = rr / a.G;
+          const uint16_t* q = a.q + static_cast<long long>(next.c0 + tok) * a.ldq + (next.hk * a.G + rr - tok * a.G) * kD;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+        }
+      }
       if (!wait(c, &ctl->it_empty[it.slot], it.phase ^ 1u, 2u)) break;
       if (lane == 0) w = next;
       __syncwarp();
