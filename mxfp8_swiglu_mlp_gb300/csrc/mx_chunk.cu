@@ -55,6 +55,7 @@ constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 2;  // 
 constexpr int kBlock = 32 * (kLoadWarp + 2);
 constexpr int NK = 4, NV = 3;                         // tiles of K and of V's codes in flight
 constexpr int kSlots = 2;                             // bf16 V tiles
+constexpr int kPartCost = 55;                         // units that a part costs to write and merge
 constexpr uint32_t kQCodes = 128 * kD;                // bytes of one term of a query tile's half
 constexpr int kFirst = 64;                            // keys of a tile's first section
 // Columns of tensor memory: scores and (in their place) probabilities of the
@@ -72,7 +73,7 @@ struct Ctl {
   uint64_t it_full[2], it_empty[2];
   Item item[2];
   float2 ml[128];                    // maxima and sums of the second stream's rows
-  long long red[kBlock / 32];
+  long long red[kBlock / 32][3];
   chunk::Ranges ranges;
   uint32_t tmem, stop, last[2];
 };
@@ -230,9 +231,16 @@ __device__ __forceinline__ void merge_rows(const ChunkArgs& a, const Item& w, co
     return __shfl_sync(0xFFFFFFFFu, slots, p & 31);
   };
   float M = -INFINITY;
-  for (int p = 0; p < blocks; ++p) {
-    const int sl = slot_of(p);
-    if (sl >= 0) M = fmaxf(M, __ldcg(&a.rec_ml[static_cast<size_t>(sl) * a.slot_rows + own].x));
+#pragma unroll 1
+  for (int p = 0; p < blocks; p += 4) {  // four loads on their way together
+    int sl[4];
+    float m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sl[i] = p + i < blocks ? slot_of(p + i) : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = __ldcg(&a.rec_ml[static_cast<size_t>(max(sl[i], 0)) * a.slot_rows + own].x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) M = fmaxf(M, sl[i] < 0 ? -INFINITY : m[i]);
   }
   const int rr = w.r0 + own, tok = rr / a.G;
   uint16_t* y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
@@ -307,8 +315,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
-  const long long units = chunk::all_units(a, qs, rs, ctl->red);  // a block-wide barrier inside
-  if (t == 0) ctl->ranges.make(units, a.grid);
+  chunk::make_ranges(a, qs, rs, kPartCost, ctl->red, ctl->ranges);  // a block-wide barrier inside
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

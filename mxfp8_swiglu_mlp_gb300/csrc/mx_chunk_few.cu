@@ -38,6 +38,7 @@ constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 2;  // 
 constexpr int kBlock = 32 * (kLoadWarp + 2);
 constexpr int NK = 4, NV = 3, kSlots = 3;       // tiles of K and of V's codes in flight, of V as bf16
 constexpr int kRows = kChunkFewRows;
+constexpr int kPartCost = 25;                 // units that a part costs to write and merge
 constexpr uint32_t kProbs = kKeys * kRows * 2;  // a tile's probabilities
 static_assert(kRows == 32, "64 bytes of probabilities a key, one swizzle atom wide");
 constexpr uint32_t kSwizzle64B = 4;
@@ -57,7 +58,7 @@ struct Ctl {
   float peak[2][4][16];      // a group's maxima, of each warp
   float sums[4][kRows];
   uint32_t grown[2];         // the last vote that found a larger score
-  long long red[kBlock / 32];
+  long long red[kBlock / 32][3];
   chunk::Ranges ranges;
   uint32_t tmem, stop;
 };
@@ -109,43 +110,63 @@ __device__ __forceinline__ float across(float (&v)[16], int lane) {
 __device__ __forceinline__ void merge_share(const ChunkArgs& a, const Item& w, const chunk::Ranges& rg, int row0, int dim0,
                                             int lane) {
   const int blocks = w.last - w.first + 1, dim = dim0 + 4 * (lane & 7);
-  int slots = -1, from = -32;  // slots of the parts from .. from + 31, one a lane
-  auto slot_of = [&](int p) -> size_t {
-    if (p >= from + 32 || p < from) {
-      from = p & ~31;
-      slots = from + lane < blocks ? chunk::part_slot(w, rg, w.first + from + lane) : -1;
-    }
-    return static_cast<size_t>(static_cast<long long>(__shfl_sync(0xFFFFFFFFu, slots, p & 31)) * a.slot_rows);
+  // the first row of each part's results, 32 parts at a time, a lane each (parts
+  // without a key tile read the first slot, with no weight; no branches, so that
+  // several parts' loads are on their way together)
+  auto rows_of = [&](int base) {
+    const int sl = base + lane < blocks ? chunk::part_slot(w, rg, w.first + base + lane) : -1;
+    return sl < 0 ? -1 : sl * a.slot_rows;
   };
-  const size_t none = static_cast<size_t>(-static_cast<long long>(a.slot_rows));
   float M = -INFINITY;  // of row lane % 16
 #pragma unroll 1
-  for (int p = 0; p < blocks; ++p) {
-    const size_t at = slot_of(p);
-    if (at != none) M = fmaxf(M, __ldcg(&a.rec_ml[at + min(row0 + (lane & 15), w.rows - 1)].x));
+  for (int base = 0; base < blocks; base += 32) {
+    const int mine = rows_of(base), n = min(32, blocks - base);
+#pragma unroll 1
+    for (int p = 0; p < n; p += 8) {  // (lanes past the last part have none)
+      int at[8];
+      float m[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) at[i] = __shfl_sync(0xFFFFFFFFu, mine, p + i);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[i] = __ldcg(&a.rec_ml[max(at[i], 0) + min(row0 + (lane & 15), w.rows - 1)].x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) M = fmaxf(M, at[i] < 0 ? -INFINITY : m[i]);
+    }
   }
   float den[4];
   float4 o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) den[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int p = 0; p < blocks; ++p) {
-    const size_t at = slot_of(p);
-    if (at == none) continue;
-    float2 ml[4];
-    float4 x[4];
+  for (int base = 0; base < blocks; base += 32) {
+    const int mine = rows_of(base), n = min(32, blocks - base);
+#pragma unroll 1
+    for (int p = 0; p < n; p += 2) {
+      int at[2];
+      float2 ml[2][4];
+      float4 x[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = min(row0 + 4 * i + (lane >> 3), w.rows - 1);
-      ml[i] = __ldcg(&a.rec_ml[at + row]);
-      x[i] = __ldcg(reinterpret_cast<const float4*>(a.rec + (at + row) * kD + dim));
-    }
+      for (int q = 0; q < 2; ++q) at[q] = __shfl_sync(0xFFFFFFFFu, mine, p + q);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float m = __shfl_sync(0xFFFFFFFFu, M, 4 * i + (lane >> 3)), f = ml[i].x == -INFINITY ? 0.f : exp2_fast(ml[i].x - m);
-      den[i] = fmaf(f, ml[i].y, den[i]);
-      o[i].x = fmaf(f, x[i].x, o[i].x), o[i].y = fmaf(f, x[i].y, o[i].y);
-      o[i].z = fmaf(f, x[i].z, o[i].z), o[i].w = fmaf(f, x[i].w, o[i].w);
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = max(at[q], 0) + min(row0 + 4 * i + (lane >> 3), w.rows - 1);
+          ml[q][i] = __ldcg(&a.rec_ml[row]);
+          x[q][i] = __ldcg(reinterpret_cast<const float4*>(a.rec + static_cast<size_t>(row) * kD + dim));
+        }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float m = __shfl_sync(0xFFFFFFFFu, M, 4 * i + (lane >> 3));
+          const bool none = at[q] < 0 || ml[q][i].x == -INFINITY;
+          const float f = none ? 0.f : exp2_fast(ml[q][i].x - m);
+          const float4 v = none ? make_float4(0.f, 0.f, 0.f, 0.f) : x[q][i];
+          den[i] = fmaf(f, none ? 0.f : ml[q][i].y, den[i]);
+          o[i].x = fmaf(f, v.x, o[i].x), o[i].y = fmaf(f, v.y, o[i].y);
+          o[i].z = fmaf(f, v.z, o[i].z), o[i].w = fmaf(f, v.w, o[i].w);
+        }
     }
   }
 #pragma unroll
@@ -200,8 +221,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
-  const long long units = chunk::all_units(a, qs, rs, ctl->red);  // a block-wide barrier inside
-  if (t == 0) ctl->ranges.make(units, a.grid);
+  chunk::make_ranges(a, qs, rs, kPartCost, ctl->red, ctl->ranges);  // a block-wide barrier inside
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -384,6 +404,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
             float2 add[8];
 #pragma unroll 1
             for (bool again = false;; again = true) {
+             if (again || k0 > w.t0) {  // (there is no scale before the first tiles)
               const float4* ms = reinterpret_cast<const float4*>(ctl->scale[turn] + 16 * h);
               float top = -INFINITY;
 #pragma unroll
@@ -418,6 +439,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
               if (__any_sync(0xFFFFFFFFu, live && top > kGrow) && lane == 0) *grown = votes + 1u;
               ok = meet();
               if (!ok || *grown != votes) break;
+             }
               // the rows' maxima, and what has been added up so far in the new unit
               float x[16];
 #pragma unroll

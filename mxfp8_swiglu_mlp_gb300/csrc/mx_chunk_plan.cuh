@@ -10,7 +10,9 @@
 // does the end of one query tile, some whole ones and the beginning of
 // another: the work is even whatever the lengths are, a long cache with few
 // rows spreads over the whole GPU, and a block leaves at most two partial
-// results, however many rows there are.
+// results, however many rows there are.  (Where the query tiles are not more
+// than the blocks, and the longest is not much longer than an equal share, each
+// is one block's instead, and worth one unit: nothing has to be merged then.)
 #pragma once
 #include "mx_chunk.h"
 #include "mx_device.cuh"
@@ -72,19 +74,26 @@ struct Tiles {
   }
 };
 __device__ __forceinline__ int key_cost(int rows) { return rows > 128 ? kPairCost : kHalfCost; }
-// Units of one KV head of a sequence.
-__device__ __forceinline__ long long seq_units(const ChunkArgs& a, const Seq& s, int qs, int rs) {
+__device__ __forceinline__ long long tile_units(int nt, int rows, bool one) {
+  return one ? 1 : kTileCost + static_cast<long long>(nt) * key_cost(rows);
+}
+// Units of one KV head of a sequence (one: a unit a query tile); the most that a
+// query tile has joins `most`.
+__device__ __forceinline__ long long seq_units(const ChunkArgs& a, const Seq& s, int qs, int rs, bool one, long long& most) {
   long long u = 0;
   Tiles t;
   for (t.start(a, s, qs, rs); t.more(a); t.next(a)) {
     int lo, hi, tb, nt, rows;
     t.get(a, lo, hi, tb, nt, rows);
-    u += kTileCost + static_cast<long long>(nt) * key_cost(rows);
+    const long long v = tile_units(nt, rows, one);
+    u += v;
+    most = max(most, v);
   }
   return u;
 }
 // Key tiles of a query tile (nt of them, cost w each) that lie before unit y of it.
-__device__ __forceinline__ int tiles_before(long long y, int nt, int w) {
+__device__ __forceinline__ int tiles_before(long long y, int nt, int w, bool one) {
+  if (one) return y > 0 ? nt : 0;
   if (y <= kTileCost) return 0;
   y += w - 1 - kTileCost;
   const long long t = w == kPairCost ? y / kPairCost : y / kHalfCost;
@@ -95,8 +104,12 @@ __device__ __forceinline__ int tiles_before(long long y, int nt, int w) {
 struct Ranges {
   long long each;
   int more, blocks;  // the first `more` blocks have one unit more
-  __device__ __forceinline__ void make(long long units, int grid) {
+  int one;           // a query tile is one unit
+  // for `tiles` query tiles of `most` units at most
+  __device__ __forceinline__ void make(long long units, long long tiles, long long most, int grid, int part_cost) {
     long long b = units / kLeastUnits;
+    one = tiles <= grid && tiles > 0 && most <= units / max(min(b, static_cast<long long>(grid)), 1LL) + 2 * part_cost;
+    if (one) b = units = tiles;
     blocks = b < 1 ? 1 : b < grid ? static_cast<int>(b) : grid;
     each = units / blocks;
     more = static_cast<int>(units - each * blocks);
@@ -125,26 +138,33 @@ struct Item {
 __device__ __forceinline__ int part_slot(const Item& w, const Ranges& r, int c) {
   const long long s = r.start(c), e = r.start(c + 1);
   const int kc = key_cost(w.rows);
-  if (tiles_before(e - w.x, w.nt, kc) <= tiles_before(s - w.x, w.nt, kc)) return -1;
+  if (tiles_before(e - w.x, w.nt, kc, r.one) <= tiles_before(s - w.x, w.nt, kc, r.one)) return -1;
   return 2 * c + (s >= w.x ? 0 : 1);  // the tile that a block begins with, else the one it ends with
 }
 
-// Block-wide: all units; reports sequences that are not valid.
-__device__ inline long long all_units(const ChunkArgs& a, int qs, int rs, long long* red) {
+// Block-wide: the ranges; reports sequences that are not valid.  red: three values a warp.
+__device__ inline void make_ranges(const ChunkArgs& a, int qs, int rs, int part_cost, long long (*red)[3], Ranges& ranges) {
   const int t = threadIdx.x;
-  long long u = 0;
+  long long u = 0, n = 0, most = 0;
   for (int b = t; b < a.B; b += blockDim.x) {
     const Seq s = load_seq(a, b);
-    u += seq_units(a, s, qs, rs);
+    u += seq_units(a, s, qs, rs, false, most);
+    n += (static_cast<long long>(s.n) * a.G + a.tile_rows - 1) / a.tile_rows;
     if (s.bad) atomicCAS(a.status, 0u, (1u << 24) | (1u << 16) | (static_cast<uint32_t>(b) & 0xFFFFu));
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
-  if ((t & 31) == 0) red[t >> 5] = u;
+  for (int o = 16; o; o >>= 1) {
+    u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+    n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+  }
+  if ((t & 31) == 0) red[t >> 5][0] = u, red[t >> 5][1] = n, red[t >> 5][2] = most;
   __syncthreads();
-  long long s = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) s += red[w];
-  return s * a.Hkv;
+  if (t == 0) {
+    for (int w = 1; w < static_cast<int>(blockDim.x) / 32; ++w)
+      u += red[w][0], n += red[w][1], most = max(most, red[w][2]);
+    ranges.make(u * a.Hkv, n * a.Hkv, most, a.grid, part_cost);
+  }
 }
 
 // A warp's way through its block's range.
@@ -171,7 +191,8 @@ struct Walk {
       Seq ls;
       ls.n = ls.len = 0;
       if (base + lane < a.B) ls = load_seq(a, base + lane);
-      const long long mine = seq_units(a, ls, qs, rs);
+      long long most = 0;
+      const long long mine = seq_units(a, ls, qs, rs, r.one, most);
       long long incl = mine * a.Hkv;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -211,13 +232,13 @@ struct Walk {
       }
       t.get(a, w.lo, w.hi, w.tb, w.nt, w.rows);
       const int kc = key_cost(w.rows), j = t.j;
-      const long long stop = at + kTileCost + static_cast<long long>(w.nt) * kc;
+      const long long stop = at + tile_units(w.nt, w.rows, r.one);
       t.next(a);
       w.x = at;
       at = stop;
       if (stop <= x) continue;  // before the range
       const long long to = min(stop, end);
-      const int p0 = tiles_before(x - w.x, w.nt, kc), p1 = tiles_before(to - w.x, w.nt, kc);
+      const int p0 = tiles_before(x - w.x, w.nt, kc, r.one), p1 = tiles_before(to - w.x, w.nt, kc, r.one);
       x = to;
       if (p0 == p1) continue;
       w.b = b, w.hk = hk, w.n = s.n, w.len = s.len, w.c0 = c0;
