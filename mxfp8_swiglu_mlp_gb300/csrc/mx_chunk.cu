@@ -56,6 +56,7 @@ constexpr int kBlock = 32 * (kLoadWarp + 2);
 constexpr int NK = 4, NV = 3;                         // tiles of K and of V's codes in flight
 constexpr int kSlots = 2;                             // bf16 V tiles
 constexpr int kPartCost = 55;                         // units that a part costs to write and merge
+constexpr int kLeastUnits = 80;                      // of a block
 constexpr uint32_t kQCodes = 128 * kD;                // bytes of one term of a query tile's half
 constexpr int kFirst = 64;                            // keys of a tile's first section
 // Columns of tensor memory: scores and (in their place) probabilities of the
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
-  chunk::make_ranges(a, qs, rs, kPartCost, ctl->red, ctl->ranges);  // a block-wide barrier inside
+  chunk::make_ranges(a, qs, rs, kPartCost, kLeastUnits, ctl->red, ctl->ranges);  // a block-wide barrier inside
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
 }  // namespace
 
 int chunk_tile_rows(int T, int B, int G) {
-  return static_cast<long long>(T) * G > 2LL * kChunkFewRows * B ? 256 : kChunkFewRows;
+  return static_cast<long long>(T) * G > static_cast<long long>(kChunkFewRows) * B ? 256 : kChunkFewRows;
 }
 
 cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream) {

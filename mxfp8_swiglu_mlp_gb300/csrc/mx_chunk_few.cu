@@ -39,6 +39,7 @@ constexpr int kBlock = 32 * (kLoadWarp + 2);
 constexpr int NK = 4, NV = 3, kSlots = 3;       // tiles of K and of V's codes in flight, of V as bf16
 constexpr int kRows = kChunkFewRows;
 constexpr int kPartCost = 25;                 // units that a part costs to write and merge
+constexpr int kLeastUnits = 10;                // of a block
 constexpr uint32_t kProbs = kKeys * kRows * 2;  // a tile's probabilities
 static_assert(kRows == 32, "64 bytes of probabilities a key, one swizzle atom wide");
 constexpr uint32_t kSwizzle64B = 4;
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
-  chunk::make_ranges(a, qs, rs, kPartCost, ctl->red, ctl->ranges);  // a block-wide barrier inside
+  chunk::make_ranges(a, qs, rs, kPartCost, kLeastUnits, ctl->red, ctl->ranges);  // a block-wide barrier inside
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -24,7 +24,6 @@ constexpr int kKeys = 112;     // tokens of a key tile
 constexpr int kTileCost = 10;  // what a query tile costs besides its keys (queries in, outputs out)
 constexpr int kPairCost = 8;   // a key tile against two halves of 128 rows
 constexpr int kHalfCost = 5;   // a key tile against one
-constexpr int kLeastUnits = 10;  // of a block: what a part costs to merge is worth about two key tiles
 
 struct Seq {
   int n, len;  // new tokens, length with them (n = 0: nothing to do or not valid)
@@ -105,9 +104,9 @@ struct Ranges {
   long long each;
   int more, blocks;  // the first `more` blocks have one unit more
   int one;           // a query tile is one unit
-  // for `tiles` query tiles of `most` units at most
-  __device__ __forceinline__ void make(long long units, long long tiles, long long most, int grid, int part_cost) {
-    long long b = units / kLeastUnits;
+  // for `tiles` query tiles of `most` units at most; a block has at least `least`
+  __device__ __forceinline__ void make(long long units, long long tiles, long long most, int grid, int part_cost, int least) {
+    long long b = units / least;
     one = tiles <= grid && tiles > 0 && most <= units / max(min(b, static_cast<long long>(grid)), 1LL) + 2 * part_cost;
     if (one) b = units = tiles;
     blocks = b < 1 ? 1 : b < grid ? static_cast<int>(b) : grid;
@@ -143,7 +142,8 @@ __device__ __forceinline__ int part_slot(const Item& w, const Ranges& r, int c) 
 }
 
 // Block-wide: the ranges; reports sequences that are not valid.  red: three values a warp.
-__device__ inline void make_ranges(const ChunkArgs& a, int qs, int rs, int part_cost, long long (*red)[3], Ranges& ranges) {
+__device__ inline void make_ranges(const ChunkArgs& a, int qs, int rs, int part_cost, int least,
+                                   long long (*red)[3], Ranges& ranges) {
   const int t = threadIdx.x;
   long long u = 0, n = 0, most = 0;
   for (int b = t; b < a.B; b += blockDim.x) {
@@ -163,7 +163,7 @@ __device__ inline void make_ranges(const ChunkArgs& a, int qs, int rs, int part_
   if (t == 0) {
     for (int w = 1; w < static_cast<int>(blockDim.x) / 32; ++w)
       u += red[w][0], n += red[w][1], most = max(most, red[w][2]);
-    ranges.make(u * a.Hkv, n * a.Hkv, most, a.grid, part_cost);
+    ranges.make(u * a.Hkv, n * a.Hkv, most, a.grid, part_cost, least);
   }
 }
 
