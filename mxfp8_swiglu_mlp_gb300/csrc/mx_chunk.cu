@@ -55,6 +55,12 @@ constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 2;  // 
 constexpr int kBlock = 32 * (kLoadWarp + 2);
 constexpr int NK = 4, NV = 3;                         // tiles of K and of V's codes in flight
 constexpr int kSlots = 2;                             // bf16 V tiles
+// The plan's costs, in eighths of a key tile against 256 rows.  Measured: tile
+// 50 against 10: 77 to 96 us for three prompt chunks of 512 tokens among 21
+// decoding sequences; least 80 against 10: 55 to 115 us for 64 rows of one
+// sequence against 8000 tokens; a query tile a block against equal shares: 78
+// to 90 us for 128 query tiles of 39 key tiles, 142 to 137 for tiles of 77.
+constexpr int kTileCost = 50;
 constexpr int kPartCost = 55;                         // units that a part costs to write and merge
 constexpr int kLeastUnits = 80;                      // of a block
 constexpr uint32_t kQCodes = 128 * kD;                // bytes of one term of a query tile's half
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
-  chunk::make_ranges(a, qs, rs, kPartCost, kLeastUnits, ctl->red, ctl->ranges);  // a block-wide barrier inside
+  chunk::make_ranges(a, qs, rs, kTileCost, kPartCost, kLeastUnits, ctl->red, ctl->ranges);  // a block-wide barrier inside
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -38,6 +38,10 @@ constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 2;  // 
 constexpr int kBlock = 32 * (kLoadWarp + 2);
 constexpr int NK = 4, NV = 3, kSlots = 3;       // tiles of K and of V's codes in flight, of V as bf16
 constexpr int kRows = kChunkFewRows;
+// The plan's costs, in fifths of a key tile.  Measured, a query tile a block
+// against equal shares: 12 to 15 us for 8 query tiles of 5 key tiles, 16 to 23
+// for 64 of 9, 24 to 17 for 8 of 19, 31 to 26 for 64 of 27.
+constexpr int kTileCost = 10;
 constexpr int kPartCost = 25;                 // units that a part costs to write and merge
 constexpr int kLeastUnits = 10;                // of a block
 constexpr uint32_t kProbs = kKeys * kRows * 2;  // a tile's probabilities
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
-  chunk::make_ranges(a, qs, rs, kPartCost, kLeastUnits, ctl->red, ctl->ranges);  // a block-wide barrier inside
+  chunk::make_ranges(a, qs, rs, kTileCost, kPartCost, kLeastUnits, ctl->red, ctl->ranges);  // a block-wide barrier inside
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -5,8 +5,8 @@
 // (row r: token r / G, head r % G); tile_rows consecutive ones make a query
 // tile, which sees the key tiles of kKeys tokens that its mask reaches.  All
 // query tiles in a row (sequence, KV head, query tile), each worth
-//   kTileCost + its key tiles * (kPairCost above 128 rows, else kHalfCost)
-// units, are cut into `blocks` equal ranges of units, one a block.  A block so
+//   tile + its key tiles * (kPairCost above 128 rows, else kHalfCost)
+// units (tile: what it costs besides its keys, queries in and outputs out), are cut into `blocks` equal ranges of units, one a block.  A block so
 // does the end of one query tile, some whole ones and the beginning of
 // another: the work is even whatever the lengths are, a long cache with few
 // rows spreads over the whole GPU, and a block leaves at most two partial
@@ -21,7 +21,6 @@ namespace fsops {
 namespace chunk {
 
 constexpr int kKeys = 112;     // tokens of a key tile
-constexpr int kTileCost = 10;  // what a query tile costs besides its keys (queries in, outputs out)
 constexpr int kPairCost = 8;   // a key tile against two halves of 128 rows
 constexpr int kHalfCost = 5;   // a key tile against one
 
@@ -73,28 +72,32 @@ struct Tiles {
   }
 };
 __device__ __forceinline__ int key_cost(int rows) { return rows > 128 ? kPairCost : kHalfCost; }
-__device__ __forceinline__ long long tile_units(int nt, int rows, bool one) {
-  return one ? 1 : kTileCost + static_cast<long long>(nt) * key_cost(rows);
+struct Units {
+  int tile;  // of a query tile besides its keys
+  int one;   // a query tile is one unit, whatever its keys
+};
+__device__ __forceinline__ long long tile_units(int nt, int rows, const Units& v) {
+  return v.one ? 1 : v.tile + static_cast<long long>(nt) * key_cost(rows);
 }
-// Units of one KV head of a sequence (one: a unit a query tile); the most that a
-// query tile has joins `most`.
-__device__ __forceinline__ long long seq_units(const ChunkArgs& a, const Seq& s, int qs, int rs, bool one, long long& most) {
+// Units of one KV head of a sequence; the most that a query tile has joins `most`.
+__device__ __forceinline__ long long seq_units(const ChunkArgs& a, const Seq& s, int qs, int rs, const Units& v,
+                                               long long& most) {
   long long u = 0;
   Tiles t;
   for (t.start(a, s, qs, rs); t.more(a); t.next(a)) {
     int lo, hi, tb, nt, rows;
     t.get(a, lo, hi, tb, nt, rows);
-    const long long v = tile_units(nt, rows, one);
-    u += v;
-    most = max(most, v);
+    const long long x = tile_units(nt, rows, v);
+    u += x;
+    most = max(most, x);
   }
   return u;
 }
 // Key tiles of a query tile (nt of them, cost w each) that lie before unit y of it.
-__device__ __forceinline__ int tiles_before(long long y, int nt, int w, bool one) {
-  if (one) return y > 0 ? nt : 0;
-  if (y <= kTileCost) return 0;
-  y += w - 1 - kTileCost;
+__device__ __forceinline__ int tiles_before(long long y, int nt, int w, const Units& v) {
+  if (v.one) return y > 0 ? nt : 0;
+  if (y <= v.tile) return 0;
+  y += w - 1 - v.tile;
   const long long t = w == kPairCost ? y / kPairCost : y / kHalfCost;
   return t < nt ? static_cast<int>(t) : nt;
 }
@@ -103,12 +106,13 @@ __device__ __forceinline__ int tiles_before(long long y, int nt, int w, bool one
 struct Ranges {
   long long each;
   int more, blocks;  // the first `more` blocks have one unit more
-  int one;           // a query tile is one unit
-  // for `tiles` query tiles of `most` units at most; a block has at least `least`
+  Units v;
+  // for `tiles` query tiles of `most` units at most, whose parts cost `part_cost`
+  // to write and merge; a block has at least `least`
   __device__ __forceinline__ void make(long long units, long long tiles, long long most, int grid, int part_cost, int least) {
     long long b = units / least;
-    one = tiles <= grid && tiles > 0 && most <= units / max(min(b, static_cast<long long>(grid)), 1LL) + 2 * part_cost;
-    if (one) b = units = tiles;
+    v.one = tiles <= grid && tiles > 0 && most <= units / max(min(b, static_cast<long long>(grid)), 1LL) + 2 * part_cost;
+    if (v.one) b = units = tiles;
     blocks = b < 1 ? 1 : b < grid ? static_cast<int>(b) : grid;
     each = units / blocks;
     more = static_cast<int>(units - each * blocks);
@@ -137,18 +141,19 @@ struct Item {
 __device__ __forceinline__ int part_slot(const Item& w, const Ranges& r, int c) {
   const long long s = r.start(c), e = r.start(c + 1);
   const int kc = key_cost(w.rows);
-  if (tiles_before(e - w.x, w.nt, kc, r.one) <= tiles_before(s - w.x, w.nt, kc, r.one)) return -1;
+  if (tiles_before(e - w.x, w.nt, kc, r.v) <= tiles_before(s - w.x, w.nt, kc, r.v)) return -1;
   return 2 * c + (s >= w.x ? 0 : 1);  // the tile that a block begins with, else the one it ends with
 }
 
 // Block-wide: the ranges; reports sequences that are not valid.  red: three values a warp.
-__device__ inline void make_ranges(const ChunkArgs& a, int qs, int rs, int part_cost, int least,
+__device__ inline void make_ranges(const ChunkArgs& a, int qs, int rs, int tile_cost, int part_cost, int least,
                                    long long (*red)[3], Ranges& ranges) {
   const int t = threadIdx.x;
   long long u = 0, n = 0, most = 0;
+  const Units v{tile_cost, 0};
   for (int b = t; b < a.B; b += blockDim.x) {
     const Seq s = load_seq(a, b);
-    u += seq_units(a, s, qs, rs, false, most);
+    u += seq_units(a, s, qs, rs, v, most);
     n += (static_cast<long long>(s.n) * a.G + a.tile_rows - 1) / a.tile_rows;
     if (s.bad) atomicCAS(a.status, 0u, (1u << 24) | (1u << 16) | (static_cast<uint32_t>(b) & 0xFFFFu));
   }
@@ -163,6 +168,7 @@ __device__ inline void make_ranges(const ChunkArgs& a, int qs, int rs, int part_
   if (t == 0) {
     for (int w = 1; w < static_cast<int>(blockDim.x) / 32; ++w)
       u += red[w][0], n += red[w][1], most = max(most, red[w][2]);
+    ranges.v = v;
     ranges.make(u * a.Hkv, n * a.Hkv, most, a.grid, part_cost, least);
   }
 }
@@ -192,7 +198,7 @@ struct Walk {
       ls.n = ls.len = 0;
       if (base + lane < a.B) ls = load_seq(a, base + lane);
       long long most = 0;
-      const long long mine = seq_units(a, ls, qs, rs, r.one, most);
+      const long long mine = seq_units(a, ls, qs, rs, r.v, most);
       long long incl = mine * a.Hkv;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -232,13 +238,13 @@ struct Walk {
       }
       t.get(a, w.lo, w.hi, w.tb, w.nt, w.rows);
       const int kc = key_cost(w.rows), j = t.j;
-      const long long stop = at + tile_units(w.nt, w.rows, r.one);
+      const long long stop = at + tile_units(w.nt, w.rows, r.v);
       t.next(a);
       w.x = at;
       at = stop;
       if (stop <= x) continue;  // before the range
       const long long to = min(stop, end);
-      const int p0 = tiles_before(x - w.x, w.nt, kc, r.one), p1 = tiles_before(to - w.x, w.nt, kc, r.one);
+      const int p0 = tiles_before(x - w.x, w.nt, kc, r.v), p1 = tiles_before(to - w.x, w.nt, kc, r.v);
       x = to;
       if (p0 == p1) continue;
       w.b = b, w.hk = hk, w.n = s.n, w.len = s.len, w.c0 = c0;
