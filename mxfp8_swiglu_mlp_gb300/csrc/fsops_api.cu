@@ -1177,7 +1177,6 @@ fsops_status fsops_mxfp8_paged_chunk_attention(const void* q_bf16, long long ldq
   ca.slot_rows = chunk_slot_rows(T, ca.G, ca.tile_rows);
   ca.grid = di->sms;
   if (ws_bytes < chunk_ws_bytes(di->sms, ca.slot_rows)) return FSOPS_ERR_INVALID_ARG;
-  if (!encode_map(&ca.tm_k, k_codes, kChunkD, num_pages * Hkv * page_size, 16)) return FSOPS_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   ca.q = static_cast<const uint16_t*>(q_bf16);
   ca.out = static_cast<uint16_t*>(out_bf16);

@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       if (!ok) break;
     }
     if (issued && *c.stop != 0u) {  // products in flight end before tensor memory is given back
-      if (lane == 0) tc_commit(&ctl->fin[m]);
+      if (elect_one()) tc_commit(&ctl->fin[m]);
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(&ctl->fin[m], 0) && globaltimer_ns() - t0 < 20000000ull) {
       }

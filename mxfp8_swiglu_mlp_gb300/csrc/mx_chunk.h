@@ -2,7 +2,6 @@
 // paged MXFP8 cache (mx_chunk.cu).
 #pragma once
 #include <cstdint>
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace fsops {
@@ -15,7 +14,6 @@ constexpr int kChunkCounters = 8;       // of a block: parts of a query tile tha
 constexpr size_t kChunkCounterBytes = 256 * kChunkCounters * sizeof(uint32_t);  // blocks <= 256
 
 struct ChunkArgs {
-  CUtensorMap tm_k;           // K codes as [num_pages * Hkv * P, 128] bytes, boxes of 16 rows, 128-byte swizzle
   const uint16_t* q;          // row t, head h at t * ldq + h * 128
   uint16_t* out;
   long long ldq, ldo;
