@@ -377,9 +377,13 @@ fsops_status fsops_mxfp8_kv_append(const void* k_bf16, long long ldk, const void
  *   num_pages * Hkv * P < 2^31.  Pointers 16-byte aligned (block_table, cu,
  *   seq_lens 4), row distances multiples of 8 and at least Hq * D.
  *   workspace: 256-byte aligned, fsops_paged_chunk_attention_workspace_bytes()
- *   of device memory, zero before its first use (the status word and counters;
- *   each call leaves the counters zero).  One launch; graph-capture safe.
- *   Calls sharing a workspace must be ordered (one stream, or events).
+ *   of device memory, zero before its first use and after a reported timeout
+ *   (the status word and counters; each call leaves the counters zero).  One
+ *   launch; graph-capture safe.  Calls sharing a workspace must be ordered (one
+ *   stream, or events).
+ *   A NaN code or scale of K reaches the rows that see its token; one of V may
+ *   reach every row of its sequence and KV head in the call whose 256-row tile
+ *   sees it.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
 fsops_status fsops_mxfp8_paged_chunk_attention(const void* q_bf16, long long ldq, const uint8_t* k_codes,
                                                const uint8_t* k_scales, const uint8_t* v_codes,

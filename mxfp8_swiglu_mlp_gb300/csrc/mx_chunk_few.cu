@@ -27,6 +27,12 @@
 // The code that runs once an item (queries, first maximum, end) is rolled up on
 // purpose: it is fetched anew each time, and straight-line code there cost
 // 10000 cycles an item, mostly of instruction fetches.
+//
+// Measured: 64 sequences of 2k-6k tokens with 5 drafted tokens each (32 query, 8
+// KV heads, pages of 16), 558 MB, in 138 us: 4.1 TB/s, 0.60 of the copy rate.
+// Loads without widening and exponentials take 110 us, with one of them 125 and
+// 128.  Four tiles of K, three of V and three widened ones in flight: 140 us
+// against 142 for 5, 4, 2, 143 for 5, 3, 2 and 157 for 4, 2, 3.
 #include "mx_chunk_parts.cuh"
 
 namespace fsops {
