@@ -362,6 +362,7 @@ __device__ __forceinline__ void store_query(uint4 x, uint32_t flip, uint8_t* cod
     h[k] = e4m3x4_code(v0 * i0, v1 * i0, v2 * i0, v3 * i0);
     const __nv_fp8x4_e4m3* hc = reinterpret_cast<const __nv_fp8x4_e4m3*>(&h[k]);
     const float4 hv = static_cast<float4>(*hc);
+    if (e == 255) h[k] = 0x7F7F7F7Fu;  // not finite: NaN scores, not saturated ones
     l[k] = e4m3x4_code(fmaf(-hv.x, back, v0) * i1, fmaf(-hv.y, back, v1) * i1, fmaf(-hv.z, back, v2) * i1,
                        fmaf(-hv.w, back, v3) * i1);
   }

@@ -142,3 +142,33 @@ def test_append_of_many_tokens(fs, norm, R, inter):
         was = was.copy()
         was[page, :, slot] = got[page, :, slot]
         assert np.array_equal(got, was)
+
+
+@pytest.mark.parametrize("new,ctx,Hkv,G", [([6], [130], 2, 4), ([120], [130], 2, 4), ([2], [9000], 1, 4), ([70], [9000], 1, 4)])
+def test_what_is_not_finite_shows(fs, new, ctx, Hkv, G):
+    """A NaN or infinite query and a NaN key that a row sees make that row NaN,
+    never zeros; the rows that see none of it are right."""
+    import torch
+
+    bt = Batch(new, ctx, Hkv, 16, 94)
+    _finite_cache(bt)
+    n, last = new[0], int(bt.lens[0]) - 1
+    r = Run(fs, bt, G)
+    ref = r.want()
+    keys = bt.codes[0].copy()
+    keys[bt.table[0, last // 16], Hkv - 1, last % 16] = 0x7F
+    r.cache[0].copy_(torch.from_numpy(keys).cuda())
+    q = r.q.view(torch.int16)
+    q[0, 5] = 0x7FC0                # NaN in row 0, head 0
+    q[n - 2, 128 + 7] = 0x7F80      # infinity in row n - 2, head 1
+    r.call()
+    torch.cuda.synchronize()
+    assert r.status() == 0
+    bad = np.zeros((n, r.Hq), bool)
+    bad[0, 0] = bad[n - 2, 1] = True
+    bad[n - 1, (Hkv - 1) * G:] = True
+    got = bf16_bits_to_f64(r.got()[:n, :r.Hq * 128]).reshape(n, r.Hq, 128)
+    out, A, mag = ref["out"][:n], ref["absv"][:n], ref["mag"][:n, :, None]
+    tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2 * (2.0 ** -17 * mag + 2.0 ** -18)) * (A + np.abs(out))
+    assert np.isnan(got[bad]).all()
+    assert np.all(np.abs(got - out)[~bad] <= tol[~bad])
