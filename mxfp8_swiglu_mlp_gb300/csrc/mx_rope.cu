@@ -220,11 +220,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
   }
 }
 
-// The sequence that holds row t: the largest b < B with cu[b] <= t, or -1
-// when t lies before the first or behind the last sequence.  A warp narrows
-// the range 32-fold a step.
+// The sequence that holds row t, cu[0] <= t < cu[B]: the largest b < B with
+// cu[b] <= t.  A warp narrows the range 32-fold a step.
 __device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int t, int lane) {
-  if (t >= __ldg(cu + B) || t < __ldg(cu)) return -1;
   int lo = 0, hi = B;  // cu[lo] <= t < cu[hi]
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
@@ -251,7 +249,6 @@ __device__ __forceinline__ Slot find_slot(const KvAppendArgs& a, int t, int lane
   r.row = -1;
   r.pos = 0;
   const int b = find_sequence(a.cu, a.B, t, lane);
-  if (b < 0) return r;  // a padding row
   const int place = __ldg(a.lens + b) - (__ldg(a.cu + b + 1) - t);  // lens[b] - n + (t - cu[b])
   if (place < 0 || (place >> a.log2P) >= a.max_pages) {
     if (lane == 0) report(a.status, 1u, 1u, b);
@@ -281,12 +278,14 @@ __global__ void __launch_bounds__(kRopeThreads, kAppendBlocks)
   if (u >= units) return;
   const Place p = lane_place(l, D, a.rope);
   const int heads = 2 * a.Hkv, steps = (heads + HW - 1) / HW;
+  const int row0 = __ldg(a.cu), row1 = __ldg(a.cu + a.B);
   const Raw gk = load_chunks(a.gamma, p, a.gamma != nullptr);
   for (; u < units; u += warps) {
     const int t = static_cast<int>(u / parts), part = static_cast<int>(u % parts);
     const uint16_t* k = a.x[0] + t * a.ldx[0];
     const uint16_t* v0 = a.x[1] + t * a.ldx[1] - static_cast<long long>(a.Hkv) * D;
     int h = part * HW + sub;
+    if (t < row0 || t >= row1) continue;  // a padding row
     Raw w = load_chunks((h < a.Hkv ? k : v0) + h * D, p, h < heads);
     const Slot to = find_slot(a, t, lane);
     if (to.row < 0) continue;
