@@ -26,7 +26,7 @@
 // are computed once a block, whose warps go on to further tokens.
 //
 // Measured: 16384 tokens of 32 + 8 heads of 128 (336 MB) in 60 us, 5.6 TB/s; the
-// append of 11 k tokens of 8 heads (87 MB) in 22 us; one token 2.7 and 3.2 us.
+// append of 11 k tokens of 8 heads (87 MB) in 22 us; one token 2.7 and 2.8 us.
 // With fractions, sines and pair partners computed lane by lane the two took 166
 // and 104 us.
 #include <cuda_bf16.h>
