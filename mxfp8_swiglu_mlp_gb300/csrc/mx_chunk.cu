@@ -343,10 +343,9 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       ctl->stop = 9u;
     }
     __syncthreads();
-  } else if (warp >= kMmaWarp) {
-   if (warp >= kLoadWarp) {
+  } else if (warp >= kLoadWarp) {
     load_items<NK, NV>(c, ctl, smem + L::k, smem + L::raw, smem + L::sfk, smem + L::sv, qs, rs, warp > kLoadWarp, lane);
-   } else {
+  } else if (warp >= kMmaWarp) {
     // ---- products of stream m: the warp walks together, one lane issues
     const int m = warp - kMmaWarp;
     const uint64_t dk = smem_desc(smem_u32(smem + L::k), 16, 1024, kSwizzle128B);
@@ -478,7 +477,6 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       }
     }
     __syncwarp();
-   }
   } else if (warp >= kSoftWarps) {
     convert_items<NV, kSlots>(c, ctl, smem + L::raw, smem + L::sv, smem + L::v, t - 32 * kSoftWarps, lane);
   } else {

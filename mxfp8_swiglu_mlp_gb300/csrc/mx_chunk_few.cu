@@ -415,42 +415,42 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
             float2 add[8];
 #pragma unroll 1
             for (bool again = false;; again = true) {
-             if (again || k0 > w.t0) {  // (there is no scale before the first tiles)
-              const float4* ms = reinterpret_cast<const float4*>(ctl->scale[turn] + 16 * h);
-              float top = -INFINITY;
+              if (again || k0 > w.t0) {  // (there is no scale before the first tiles)
+                const float4* ms = reinterpret_cast<const float4*>(ctl->scale[turn] + 16 * h);
+                float top = -INFINITY;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) add[i] = make_float2(0.f, 0.f);
+                for (int i = 0; i < 8; ++i) add[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
-              for (int k = k0; k < k1; ++k) {
-                float2 s[8];
-                uint32_t p[8];
-                scores(k, s);
+                for (int k = k0; k < k1; ++k) {
+                  float2 s[8];
+                  uint32_t p[8];
+                  scores(k, s);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float4 m = ms[i];
-                  s[2 * i] = __ffma2_rn(s[2 * i], make_float2(scale, scale), make_float2(-m.x, -m.y));
-                  s[2 * i + 1] = __ffma2_rn(s[2 * i + 1], make_float2(scale, scale), make_float2(-m.z, -m.w));
-                }
+                  for (int i = 0; i < 4; ++i) {
+                    const float4 m = ms[i];
+                    s[2 * i] = __ffma2_rn(s[2 * i], make_float2(scale, scale), make_float2(-m.x, -m.y));
+                    s[2 * i + 1] = __ffma2_rn(s[2 * i + 1], make_float2(scale, scale), make_float2(-m.z, -m.w));
+                  }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  top = max3(top, s[i].x, s[i].y);
-                  s[i].x = exp2_fast(s[i].x), s[i].y = exp2_fast(s[i].y);
-                  add[i] = __fadd2_rn(add[i], s[i]);
-                  p[i] = bf16x2_rn(s[i].x, s[i].y);
+                  for (int i = 0; i < 8; ++i) {
+                    top = max3(top, s[i].x, s[i].y);
+                    s[i].x = exp2_fast(s[i].x), s[i].y = exp2_fast(s[i].y);
+                    add[i] = __fadd2_rn(add[i], s[i]);
+                    p[i] = bf16x2_rn(s[i].x, s[i].y);
+                  }
+                  if (live) {
+                    uint8_t* d = smem + (prow + (2 * buf + (k - k0)) * kProbs);
+                    *reinterpret_cast<uint4*>(d) = make_uint4(p[0], p[1], p[2], p[3]);
+                    *reinterpret_cast<uint4*>(smem + ((prow ^ 16u) + (2 * buf + (k - k0)) * kProbs)) =
+                        make_uint4(p[4], p[5], p[6], p[7]);
+                  }
                 }
-                if (live) {
-                  uint8_t* d = smem + (prow + (2 * buf + (k - k0)) * kProbs);
-                  *reinterpret_cast<uint4*>(d) = make_uint4(p[0], p[1], p[2], p[3]);
-                  *reinterpret_cast<uint4*>(smem + ((prow ^ 16u) + (2 * buf + (k - k0)) * kProbs)) =
-                      make_uint4(p[4], p[5], p[6], p[7]);
-                }
+                if (again) break;
+                volatile uint32_t* grown = &ctl->grown[h];
+                if (__any_sync(0xFFFFFFFFu, live && top > kGrow) && lane == 0) *grown = votes + 1u;
+                ok = meet();
+                if (!ok || *grown != votes) break;
               }
-              if (again) break;
-              volatile uint32_t* grown = &ctl->grown[h];
-              if (__any_sync(0xFFFFFFFFu, live && top > kGrow) && lane == 0) *grown = votes + 1u;
-              ok = meet();
-              if (!ok || *grown != votes) break;
-             }
               // the rows' maxima, and what has been added up so far in the new unit
               float x[16];
 #pragma unroll

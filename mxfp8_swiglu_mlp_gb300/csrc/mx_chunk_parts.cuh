@@ -112,8 +112,8 @@ struct Ring {
 // Sixteen codes times m (a bf16 power of two, twice): four bf16 words for each
 // of the two 16-byte pieces.  A code s eeee mmm moved to s 0000eeee mmm0000 is
 // the bf16 2^-120 times its value (subnormal codes included), which m takes
-// back.  Within four codes the order is 0, 2, 1, 3: the queries are stored in
-// the same order, and the outputs' columns are put back at the end.
+// back.  Within four codes the order is 0, 2, 1, 3: the outputs' columns are put
+// back at the end.
 __device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t m) {
   const uint32_t even = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u);
   const uint32_t odd = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
@@ -131,8 +131,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 
 // ---------------------------------------------------------------- load warps
 // One of them copies K's key tiles into its ring, with the 128-byte swizzle that
-// the products read, the other V's as they are, and their scales: K's in the
-// order that tcgen05.cp wants, V's token by token.  A page holds whole groups
+// the products read, the other V's (with the halves of odd rows exchanged, for
+// the warps that widen it), and their scales: K's in the order that tcgen05.cp
+// wants, V's token by token.  A page holds whole groups
 // of 16 tokens, 2 KB of codes: with 16-byte asynchronous copies (four
 // instructions of a warp a group) a tile takes its warp a third of the cycles
 // that a bulk or tensor copy a group takes, whose issue is about 100 cycles each.

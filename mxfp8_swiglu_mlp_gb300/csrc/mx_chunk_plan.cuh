@@ -6,11 +6,12 @@
 // tile, which sees the key tiles of kKeys tokens that its mask reaches.  All
 // query tiles in a row (sequence, KV head, query tile), each worth
 //   tile + its key tiles * (kPairCost above 128 rows, else kHalfCost)
-// units (tile: what it costs besides its keys, queries in and outputs out), are cut into `blocks` equal ranges of units, one a block.  A block so
-// does the end of one query tile, some whole ones and the beginning of
-// another: the work is even whatever the lengths are, a long cache with few
-// rows spreads over the whole GPU, and a block leaves at most two partial
-// results, however many rows there are.  (Where the query tiles are not more
+// units (tile: what it costs besides its keys, queries in and outputs out), are
+// cut into `blocks` equal ranges of units, one a block.  A block so does the end
+// of one query tile, some whole ones and the beginning of another: the work is
+// even whatever the lengths are, a long cache with few rows spreads over the
+// whole GPU, and a block leaves at most two partial results, however many rows
+// there are.  (Where the query tiles are not more
 // than the blocks, and the longest is not much longer than an equal share, each
 // is one block's instead, and worth one unit: nothing has to be merged then.)
 #pragma once
