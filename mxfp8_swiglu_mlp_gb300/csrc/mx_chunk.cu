@@ -85,13 +85,13 @@ struct Ctl {
   uint64_t v_full[kSlots], v_empty[kSlots];
   uint64_t s_full[2][2], p_full[2][2];  // stream, section
   uint64_t o_first[2], o_done[2], q_full, q_free, fin[2];
-  uint64_t group[2], second, taken;  // a stream's warps; the second stream's sums ready, and read
+  uint64_t second, taken;  // the second stream's sums ready, and read
   uint64_t it_full[2], it_empty[2];
   Item item[2];
   float2 ml[128];                    // maxima and sums of the second stream's rows
   long long red[kBlock / 32][3];
   chunk::Ranges ranges;
-  uint32_t tmem, stop, last[2];
+  uint32_t tmem, stop;
 };
 struct L {
   static constexpr uint32_t q = 0, v = 2 * 2 * kQCodes, k = v + kSlots * kOperand, raw = k + NK * kCodes,
@@ -231,11 +231,11 @@ __device__ __forceinline__ void put32(uint16_t* y, const float (&o)[32], float f
         make_uint4(bf16x2_rn(o[i] * f, o[i + 2] * f), bf16x2_rn(o[i + 1] * f, o[i + 3] * f),
                    bf16x2_rn(o[i + 4] * f, o[i + 6] * f), bf16x2_rn(o[i + 5] * f, o[i + 7] * f));
 }
-// Columns chunk * 32 .., chunk + step, .. of up to 32 rows of the tile (from row0
-// on, a lane a row) added up over the tile's parts, always in the blocks'
-// order.  The parts lie column by column, so that a warp reads whole lines.
+// Up to 32 rows of the tile (from row0 on, a lane a row) added up over the tile's
+// parts, always in the blocks' order.  The parts lie column by column, so that a
+// warp reads whole lines.
 __device__ __forceinline__ void merge_rows(const ChunkArgs& a, const Item& w, const chunk::Ranges& rg, int row0, int rows,
-                                           int chunk, int step, int lane) {
+                                           int lane) {
   const int own = row0 + min(lane, rows - 1);
   const int blocks = w.last - w.first + 1;
   int slots = -1, from = -32;  // slots of the parts from .. from + 31, one a lane
@@ -261,7 +261,7 @@ __device__ __forceinline__ void merge_rows(const ChunkArgs& a, const Item& w, co
   const int rr = w.r0 + own, tok = rr / a.G;
   uint16_t* y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;
 #pragma unroll 1
-  for (; chunk < kD / 32; chunk += step) {
+  for (int chunk = 0; chunk < kD / 32; ++chunk) {
     float o[32], den = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) o[i] = 0.f;
@@ -316,7 +316,6 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       mbar_init(&ctl->o_first[i], 1);
       mbar_init(&ctl->o_done[i], 1);
       mbar_init(&ctl->fin[i], 1);
-      mbar_init(&ctl->group[i], 4);
       mbar_init(&ctl->it_full[i], 32);
       mbar_init(&ctl->it_empty[i], kSoftWarps + kConvWarps + 3);
     }
@@ -495,7 +494,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       warp_arrive(&ctl->q_full, lane);
     };
     Ring<2> it;
-    uint32_t s_phase = 0, o_phase = 0, g_phase = 0, x_phase = 0, f_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0, x_phase = 0, f_phase = 0;
     bool ok = wait(c, &ctl->it_full[0], 0, 4u);
     if (ok) queries(0);
     // (what an item's end needs is read again there, to keep the loop's registers few)
@@ -617,30 +616,17 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
           }
         }
         tc_fence_before();
-        if (!whole) {
-          // the last part to arrive adds them up, in the blocks' order
+        if (!whole && busy) {
+          // Of each warp, the last part's to arrive adds the parts up: it needs
+          // what the same warps of the other blocks wrote, no more.
           __threadfence();
-          warp_arrive(&ctl->group[m], lane);
-          ok = wait(c, &ctl->group[m], g_phase, 13u);
-          if (!ok) break;
-          g_phase ^= 1u;
-          if (row == 0) {
-            uint32_t* count = a.count + kChunkCounters * w.first + m;
-            const bool last = atomicAdd(count, 1u) == static_cast<uint32_t>(w.parts) - 1u;
-            if (last) *count = 0u;
-            ctl->last[m] = last;
+          __syncwarp();
+          uint32_t* count = a.count + kChunkCounters * w.first + warp;
+          const uint32_t before = __shfl_sync(0xFFFFFFFFu, lane == 0 ? atomicAdd(count, 1u) : 0u, 0);
+          if (before == static_cast<uint32_t>(w.parts) - 1u) {
+            if (lane == 0) *count = 0u;
             __threadfence();
-          }
-          warp_arrive(&ctl->group[m], lane);
-          ok = wait(c, &ctl->group[m], g_phase, 13u);
-          if (!ok) break;
-          g_phase ^= 1u;
-          if (ctl->last[m]) {
-            // 32 rows a warp; with fewer groups of rows, the warps share their columns
-            const int base = pair ? 128 * m : 0, rows = min(128, w.rows - base), groups = (rows + 31) / 32;
-            const int g = wl % groups, step = 4 / groups;
-            if (wl / groups < step)
-              merge_rows(a, w, ctl->ranges, base + 32 * g, min(32, rows - 32 * g), wl / groups, step, lane);
+            merge_rows(a, w, ctl->ranges, tr - lane, min(32, w.rows - (tr - lane)), lane);
           }
         }
       }
