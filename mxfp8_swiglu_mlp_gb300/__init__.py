@@ -246,11 +246,11 @@ def fsops_mxfp8_paged_decode_attention(q, k_codes, k_scales, v_codes, v_scales, 
 
 def _dev_ptr(t, where: str) -> Optional[int]:
     """Pointer of a tensor of the current device (an address or None as it is)."""
-    if t is None or isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
-    if not t.is_cuda:
-        raise FsopsError(ERR_INVALID_ARG, where + " (a tensor that is not on the GPU)")
-    return t.data_ptr()
+    if t.is_cuda:
+        return t.data_ptr()
+    raise FsopsError(ERR_INVALID_ARG, where + " (a tensor that is not on the GPU)")
 
 
 def _rope(rope, where: str):
