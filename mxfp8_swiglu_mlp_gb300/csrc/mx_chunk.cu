@@ -50,6 +50,9 @@
 // V), 1900 cycles for a key tile and 256 rows; the streams' exponentials and
 // hand-offs bring that to 3200.  Measured: 2048 tokens of 32 query heads against
 // 16 k tokens (515 GFLOP) in 400 us, 1.29 PFLOP/s, 0.70 of cuBLAS's bf16 rate.
+// The roles' code is at the limit of what is fetched in time: the same roles in
+// other orders of their branches take 399 to 485 us (this order is among the
+// best), and code at an item's ends that is a little longer up to 8 % more.
 // A 112-token tile kept whole instead of two sections took 515 us (its scores
 // and probabilities at once are more registers than a thread has), 16 softmax
 // warps and eight converting ones more as well.
