@@ -43,12 +43,11 @@
 // fp32.  The maximum that scales a row is raised only when it would grow by
 // more than 2^8 (bf16 keeps its relative precision up there), which spares
 // nearly every rescaling of the outputs.
-#include <cuda_bf16.h>
 //
-// What bounds it: the products read their operands from shared memory (128
-// bytes a cycle: 60 cycles for 112 keys of 32 dimensions, 64 for 16 tokens of
-// V), 1900 cycles for a key tile and 256 rows; the streams' exponentials and
-// hand-offs bring that to 3200.  Measured: 2048 tokens of 32 query heads against
+// What bounds it: the products read their operands from shared memory at 128
+// bytes a cycle (48 cycles for 128 rows, 64 keys and 32 dimensions, 42 for 48
+// keys; 64 for 16 tokens of V), 2340 cycles for a key tile and 256 rows; the
+// streams' exponentials and hand-offs bring that to 3200.  Measured: 2048 tokens of 32 query heads against
 // 16 k tokens (515 GFLOP) in 400 us, 1.29 PFLOP/s, 0.70 of cuBLAS's bf16 rate.
 // The roles' code is at the limit of what is fetched in time: the same roles in
 // other orders of their branches take 399 to 485 us (this order is among the
