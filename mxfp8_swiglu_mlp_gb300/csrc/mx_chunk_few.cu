@@ -29,7 +29,7 @@
 // 10000 cycles an item, mostly of instruction fetches.
 //
 // Measured: 64 sequences of 2k-6k tokens with 5 drafted tokens each (32 query, 8
-// KV heads, pages of 16), 558 MB, in 138 us: 4.1 TB/s, 0.60 of the copy rate.
+// KV heads, pages of 16), 558 MB, in 136 us: 4.1 TB/s, 0.61 of the copy rate.
 // Loads without widening and exponentials take 110 us, with one of them 125 and
 // 128.  Four tiles of K, three of V and three widened ones in flight: 140 us
 // against 142 for 5, 4, 2, 143 for 5, 3, 2 and 157 for 4, 2, 3.
@@ -48,8 +48,8 @@ constexpr int kRows = kChunkFewRows;
 // against equal shares: 12 to 15 us for 8 query tiles of 5 key tiles, 16 to 23
 // for 64 of 9, 24 to 17 for 8 of 19, 31 to 26 for 64 of 27.
 constexpr int kTileCost = 10;
-constexpr int kPartCost = 25;                 // units that a part costs to write and merge
-constexpr int kLeastUnits = 10;                // of a block
+constexpr int kPartCost = 25;    // units that a part costs to write and merge
+constexpr int kLeastUnits = 10;  // of a block
 constexpr uint32_t kProbs = kKeys * kRows * 2;  // a tile's probabilities
 static_assert(kRows == 32, "64 bytes of probabilities a key, one swizzle atom wide");
 constexpr uint32_t kSwizzle64B = 4;

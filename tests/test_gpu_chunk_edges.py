@@ -172,3 +172,45 @@ def test_what_is_not_finite_shows(fs, new, ctx, Hkv, G):
     tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2 * (2.0 ** -17 * mag + 2.0 ** -18)) * (A + np.abs(out))
     assert np.isnan(got[bad]).all()
     assert np.all(np.abs(got - out)[~bad] <= tol[~bad])
+
+
+def test_few_rows_in_a_graph(fs):
+    """A captured decode step replayed with other lengths and fewer rows."""
+    import torch
+
+    bt = Batch([1, 2, 1], [700, 260, 3], 2, 16, 95, pad=2)
+    _finite_cache(bt)
+    r = Run(fs, bt, 4)
+    s = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        r.call(stream=s)
+    for new, lens in (([1, 2, 1], [701, 262, 4]), ([1, 0, 1], [650, 0, 2]), ([2, 1, 1], [449, 113, 1])):
+        bt.new, bt.lens = np.array(new), np.array(lens)
+        bt.cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        for x, y in zip(r.meta[1:], (bt.cu, bt.lens.astype(np.int32))):
+            x.copy_(torch.from_numpy(y).cuda())
+        r.out.fill_(-7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert r.status() == 0
+        _compare(r)
+
+
+def test_two_calls_at_once(fs):
+    """Calls on two streams, each with a workspace of its own."""
+    import torch
+
+    runs = []
+    for seed, (new, ctx) in enumerate((([1, 1, 3], [3000, 40, 900]), ([90, 300], [1500, 0]))):
+        bt = Batch(new, ctx, 2, 16, 96 + seed)
+        _finite_cache(bt)
+        runs.append(Run(fs, bt, 4))
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(5):
+        for r, s in zip(runs, streams):
+            r.call(stream=s)
+    torch.cuda.synchronize()
+    for r in runs:
+        assert r.status() == 0
+        _compare(r)
