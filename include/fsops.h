@@ -381,9 +381,9 @@ fsops_status fsops_mxfp8_kv_append(const void* k_bf16, long long ldk, const void
  *   (the status word and counters; each call leaves the counters zero).  One
  *   launch; graph-capture safe.  Calls sharing a workspace must be ordered (one
  *   stream, or events).
- *   A NaN code or scale of K reaches the rows that see its token; one of V may
- *   reach every row of its sequence and KV head in the call whose 256-row tile
- *   sees it.
+ *   A NaN code or scale byte makes NaN of the rows and heads that see its token
+ *   and leaves the others as they are (one of V in its own dimensions where
+ *   every row of the call sees the token, else possibly in all).
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
 fsops_status fsops_mxfp8_paged_chunk_attention(const void* q_bf16, long long ldq, const uint8_t* k_codes,
                                                const uint8_t* k_scales, const uint8_t* v_codes,

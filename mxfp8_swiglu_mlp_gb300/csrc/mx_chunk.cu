@@ -91,6 +91,7 @@ struct Ctl {
   uint64_t second, taken;  // the second stream's sums ready, and read
   uint64_t it_full[2], it_empty[2];
   Item item[2];
+  HiddenNan hidden[2];
   float2 ml[128];                    // maxima and sums of the second stream's rows
   long long red[kBlock / 32][3];
   chunk::Ranges ranges;
@@ -580,6 +581,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         }
       }
       if (pair || m == 0) {
+        if (ctl->hidden[slot].any != 0u) st.l = sum_or_nan(a, w, ctl->hidden[slot], tr, st.l);
         const bool two = !pair && w.t1 - w.t0 > 1, whole = w.whole;
         float* rec = nullptr;
         uint16_t* y = nullptr;
@@ -600,13 +602,13 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
             tmem_ld32(S + kColO + col, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = f0 != 0.f ? f0 * o[i] : 0.f;
+            for (int i = 0; i < 32; ++i) o[i] *= f0;
             if (two) {
               float o1[32];
               tmem_ld32(S + kColO + 128 + col, o1);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] += f1 != 0.f ? f1 * o1[i] : 0.f;
+              for (int i = 0; i < 32; ++i) o[i] = fmaf(f1, o1[i], o[i]);
             }
             if (write) {
               if (whole) {

@@ -64,6 +64,7 @@ struct Ctl {
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2];  // two tiles each, by turns
   uint64_t q_full, vote[2], fin[2], it_full[2], it_empty[2];
   Item item[2];
+  HiddenNan hidden[2];
   alignas(16) float scale[2][kRows];     // the rows' scales (base 2), the one in use by turns
   alignas(16) float fall[kRows];         // what the last change of scale makes of a row
   float peak[2][4][16];      // a group's maxima, of each warp
@@ -526,7 +527,8 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
         if (!ok) break;
         tc_fence_after();
         const int r = 16 * h + (lane & 15);
-        const float sum = (ctl->sums[0][r] + ctl->sums[1][r]) + (ctl->sums[2][r] + ctl->sums[3][r]);
+        float sum = (ctl->sums[0][r] + ctl->sums[1][r]) + (ctl->sums[2][r] + ctl->sums[3][r]);
+        if (ctl->hidden[slot].any != 0u) sum = sum_or_nan(a, w, ctl->hidden[slot], r, sum);
         const float m = ctl->scale[turn][r];
         const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : m == kNone ? 0.f : 1.f;  // (NaN stays)
         const size_t rec = whole ? 0 : static_cast<size_t>(w.slot) * a.slot_rows;
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float fi = __shfl_sync(0xFFFFFFFFu, f, i0 + i), v = fi != 0.f ? fi * o[i] : 0.f;
+            const float v = __shfl_sync(0xFFFFFFFFu, f, i0 + i) * o[i];
             if (i0 + i < left) {
               if (whole)
                 *y = static_cast<uint16_t>(bf16x2_rn(v, 0.f));

@@ -109,16 +109,27 @@ struct Ring {
   }
 };
 
-// Sixteen codes times m (a bf16 power of two, twice): four bf16 words for each
-// of the two 16-byte pieces.  A code s eeee mmm moved to s 0000eeee mmm0000 is
-// the bf16 2^-120 times its value (subnormal codes included), which m takes
-// back.  Within four codes the order is 0, 2, 1, 3: the outputs' columns are put
-// back at the end.
+// Tokens of an item whose values are not finite and which only some rows see
+// (noted by the convert warps).
+constexpr uint32_t kPlainScale = 134u;  // the largest scale byte s with 2^(s - 7) a bf16
+struct HiddenNan {
+  uint32_t any;
+  uint32_t bits[2][8];  // tokens from the tile's first on; from the first behind those that all rows see
+};
+
+// Four codes times m (a bf16 power of two, twice).  A code s eeee mmm moved to
+// s 0000eeee mmm0000 is the bf16 2^-120 times its value (subnormal codes
+// included), which m takes back.  Within four codes the order is 0, 2, 1, 3: the
+// outputs' columns are put back at the end.
 __device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t m) {
   const uint32_t even = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u);
   const uint32_t odd = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
   return make_uint2(mul_bf16x2(even, m), mul_bf16x2(odd, m));
 }
+// Of four codes, bits 7, 15, 23, 31 say whether one is NaN (all bits but the sign
+// set): adding one changes the bit above (a carry out of a code comes from NaN alone).
+__device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w + 0x01010101u) ^ w; }
+constexpr uint32_t kNanBits = 0x80808080u;
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -257,6 +268,7 @@ __device__ __forceinline__ void load_items(const Ctx& c, Ctl* ctl, uint8_t* k, u
       }
       if (!wait(c, &ctl->it_empty[it.slot], it.phase ^ 1u, 2u)) break;
       if (lane == 0) w = next;
+      if (lane < static_cast<int>(sizeof(HiddenNan) / 4)) reinterpret_cast<uint32_t*>(&ctl->hidden[it.slot])[lane] = 0u;
       __syncwarp();
       mbar_arrive(&ctl->it_full[it.slot]);
     } else if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) {
@@ -268,42 +280,107 @@ __device__ __forceinline__ void load_items(const Ctx& c, Ctl* ctl, uint8_t* k, u
   if (*c.stop != 0u) ld.drain();
 }
 
+// ---------------------------------------------------------------- values that are not finite
+// The second product multiplies hidden places too, by a probability of zero,
+// and zero times NaN is NaN.  So what is not finite stands in V's operand only
+// at tokens that every row of the query tile sees; at the others the operand
+// gets zeros, the token is noted, and at the item's end the rows that see
+// it become NaN.  All of it is off the path of finite values.
+// The tokens from .. upto - 1 that row r of the tile sees.
+__device__ __forceinline__ void row_sees(const ChunkArgs& a, const Item& w, int r, int& from, int& upto) {
+  upto = w.len - w.n + 1 + (w.r0 + r) / a.G;
+  from = a.window > 0 ? max(0, upto - a.window) : 0;
+}
+// A row's sum, NaN where the row sees a noted token.
+__device__ __noinline__ float sum_or_nan(const ChunkArgs& a, const Item& w, const HiddenNan& hn, int row, float sum) {
+  int from, upto, all_from, all_upto, none;
+  row_sees(a, w, min(row, w.rows - 1), from, upto);
+  row_sees(a, w, w.rows - 1, all_from, none);
+  row_sees(a, w, 0, none, all_upto);
+#pragma unroll 1
+  for (int i = 0; i < 512; ++i) {
+    const int tok = (i < 256 ? w.lo : all_upto) + (i & 255);
+    if ((hn.bits[i >> 8][(i & 255) >> 5] >> (i & 31) & 1u) != 0u && tok >= from && tok < upto) sum = __int_as_float(0x7FC00000);
+  }
+  return sum;
+}
+// A thread's share of a V tile (16 codes of every 16th token from tok on, see
+// convert_tile) once more, with what convert16 leaves out: scales from 2^8 on and
+// what is not finite.
+template <int kPasses>
+__device__ __noinline__ void convert_rest(const ChunkArgs& a, const Item& w, HiddenNan& hn, const uint8_t* raw,
+                                          const uint8_t* sc, uint8_t* row, int first, int tok) {
+  int all_from, all_upto, none;
+  row_sees(a, w, w.rows - 1, all_from, none);
+  row_sees(a, w, 0, none, all_upto);
+#pragma unroll 1
+  for (int i = 0; i < kPasses; ++i, tok += 16, raw += 16 * kD, sc += 64, row += 16 * 128) {
+    const uint32_t s = *sc;
+    if (tok < w.lo || tok >= w.hi) continue;
+    bool bad = false;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t x = reinterpret_cast<const uint32_t*>(raw)[k];
+      uint2 p = widen4(x, (min(s, kPlainScale) + 120u) * 0x00800080u);  // 2^(s - 127 + 120)
+      if (s > kPlainScale) {  // the rest of it
+        const uint32_t m = ((s - kPlainScale + 127u) << 7) * 0x10001u;
+        p = make_uint2(mul_bf16x2(p.x, m), mul_bf16x2(p.y, m));
+      }
+      const uint32_t n = s == 255u ? kNanBits : nan_bits(x);
+      p.x |= (n & 0x80u ? 0x7FFFu : 0u) | (n & 0x800000u ? 0x7FFF0000u : 0u);
+      p.y |= (n & 0x8000u ? 0x7FFFu : 0u) | (n & 0x80000000u ? 0x7FFF0000u : 0u);
+#pragma unroll
+      for (int h = 0; h < 32; h += 16) bad |= (p.x >> h & 0x7F80u) == 0x7F80u || (p.y >> h & 0x7F80u) == 0x7F80u;
+      *reinterpret_cast<uint2*>(row + (k < 2 ? first : first ^ 16) + 8 * (k & 1)) = p;
+    }
+    if (!bad || (tok >= all_from && tok < all_upto)) continue;
+    *reinterpret_cast<uint4*>(row + first) = *reinterpret_cast<uint4*>(row + (first ^ 16)) = make_uint4(0u, 0u, 0u, 0u);
+    const int at = tok < all_from ? tok - w.lo : tok - all_upto;  // below 256: a tile's rows are as many tokens at most
+    atomicOr(&hn.bits[tok < all_from ? 0 : 1][at >> 5], 1u << (at & 31));
+    hn.any = 1u;
+  }
+}
+
 // ---------------------------------------------------------------- convert warps
 // V's codes of tokens from tok0 to a bf16 tile; tokens outside [lo, hi) become
 // zeros whatever the ring holds there.  A thread has 16 codes of every 16th
 // token: eight lanes four pieces of two tokens each, which keeps their 16-byte
 // stores (and, with the ring's halves exchanged in every other row, their
-// loads) apart in the banks.
-__device__ __forceinline__ void convert16(const uint8_t* raw, uint32_t s, uint8_t* row, int first, bool on) {
+// loads) apart in the banks.  nan: nan_bits of all codes, top: the largest scale.
+__device__ __forceinline__ void convert16(const uint8_t* raw, uint32_t s, uint8_t* row, int first, bool on, uint32_t& nan,
+                                          uint32_t& top) {
   const uint4 x = *reinterpret_cast<const uint4*>(raw);
-  uint32_t m = on ? min(s, 134u) * 0x00800080u + 120u * 0x00800080u : 0u;  // 2^(s - 127 + 120), twice
-  uint2 p0 = widen4(x.x, m), p1 = widen4(x.y, m), p2 = widen4(x.z, m), p3 = widen4(x.w, m);
-  if (on && s > 134u) {  // 2^(s - 7) is beyond bf16: the rest of it
-    m = ((s - 134u + 127u) << 7) * 0x10001u;
-    p0 = make_uint2(mul_bf16x2(p0.x, m), mul_bf16x2(p0.y, m)), p1 = make_uint2(mul_bf16x2(p1.x, m), mul_bf16x2(p1.y, m));
-    p2 = make_uint2(mul_bf16x2(p2.x, m), mul_bf16x2(p2.y, m)), p3 = make_uint2(mul_bf16x2(p3.x, m), mul_bf16x2(p3.y, m));
-  }
+  const uint32_t m = on ? s * 0x00800080u + 120u * 0x00800080u : 0u;  // 2^(s - 127 + 120), twice
+  const uint2 p0 = widen4(x.x, m), p1 = widen4(x.y, m), p2 = widen4(x.z, m), p3 = widen4(x.w, m);
   *reinterpret_cast<uint4*>(row + first) = make_uint4(p0.x, p0.y, p1.x, p1.y);
   *reinterpret_cast<uint4*>(row + (first ^ 16)) = make_uint4(p2.x, p2.y, p3.x, p3.y);
+  nan |= nan_bits(x.x), nan |= nan_bits(x.y), nan |= nan_bits(x.z), nan |= nan_bits(x.w);
+  top = max(top, s);
 }
-__device__ __forceinline__ void convert_tile(const uint8_t* raw, const uint8_t* sc, uint8_t* out, int tok0, int lo, int hi,
-                                             int t) {
+__device__ __forceinline__ void convert_tile(const ChunkArgs& a, const Item& w, HiddenNan& hn, const uint8_t* raw,
+                                             const uint8_t* sc, uint8_t* out, int tok0, int lo, int hi, int t) {
   static_assert(kConvWarps == 4, "16 tokens a pass");
   constexpr int kPasses = kKeys / 16;
   const int half = (t >> 3) & 1, piece = 4 * half + (t & 3), r0 = 2 * (t >> 4) + ((t >> 2) & 1);
   const int first = ((2 * (t & 3)) ^ (r0 & 7)) << 4;
   out += half * kHalf + r0 * 128;
   raw += r0 * kD + 16 * (piece ^ (4 * (r0 & 1))), sc += 4 * r0 + (piece >> 1);
+  uint32_t nan = 0u, top = 0u;
   if (tok0 >= lo && tok0 + kKeys <= hi) {
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) convert16(raw + i * 16 * kD, sc[i * 64], out + i * 16 * 128, first, true);
+    for (int i = 0; i < kPasses; ++i) convert16(raw + i * 16 * kD, sc[i * 64], out + i * 16 * 128, first, true, nan, top);
   } else {
 #pragma unroll 1
     for (int i = 0; i < kPasses; ++i) {
       const int tok = tok0 + r0 + i * 16;
-      convert16(raw + i * 16 * kD, sc[i * 64], out + i * 16 * 128, first, tok >= lo && tok < hi);
+      const bool on = tok >= lo && tok < hi;
+      uint32_t n = 0u, s = 0u;
+      convert16(raw + i * 16 * kD, sc[i * 64], out + i * 16 * 128, first, on, n, s);
+      if (on) nan |= n, top = max(top, s);
     }
   }
+  if ((nan & kNanBits) != 0u || top > kPlainScale)
+    convert_rest<kPasses>(a, w, hn, raw, sc, out, first, tok0 + r0);
 }
 
 // The role of the convert warps, thread ct of them.
@@ -322,7 +399,8 @@ __device__ __forceinline__ void convert_items(const Ctx& c, Ctl* ctl, const uint
     for (int k = t0; k < t1; ++k) {
       ok = wait(c, &ctl->r_full[ring.slot], ring.phase, 3u) && wait(c, &ctl->v_empty[vr.slot], vr.phase ^ 1u, 6u);
       if (!ok) break;
-      convert_tile(raw + ring.slot * kCodes, sv + ring.slot * kScales,
+      // (the item stays until the softmax warps give it back, after its last product)
+      convert_tile(c.a, ctl->item[it.slot], ctl->hidden[it.slot], raw + ring.slot * kCodes, sv + ring.slot * kScales,
                    v + vr.slot * kOperand, k * kKeys, lo, hi, ct);
       fence_proxy_async_shared();
       __syncwarp();
