@@ -505,7 +505,7 @@ fsops_status fsops_set_workspace(void* ws, size_t bytes);
  * fsops_status, bits 23..16 the wait site and bits 15..0 the block index.
  * After a failure the workspace counters are reset by the kernel itself: the
  * blocks of a launch that gave up clear them once every block has left its
- * waits. */
+ * waits (but for fsops_mxfp8_paged_chunk_attention, see there). */
 fsops_status fsops_read_kernel_status(void* workspace, uint32_t* word);
 
 /* Upper bound, in nanoseconds, for every wait inside the kernels launched
@@ -514,7 +514,8 @@ fsops_status fsops_set_wait_timeout_ns(uint64_t ns);
 
 /* Test hook: kernels launched after this call wait for `n` more arrivals on
  * their cross-block readiness counters (quantised activations, finished
- * SwiGLU tiles) than any launch produces, so those waits run out and report
+ * SwiGLU tiles; the chunk attention: on the barriers of a block that say that
+ * outputs are done) than any launch produces, so those waits run out and report
  * FSOPS_ERR_TIMEOUT.  0 (the default) disables it. */
 fsops_status fsops_debug_set_extra_arrivals(uint32_t n);
 

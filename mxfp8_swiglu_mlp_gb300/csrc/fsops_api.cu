@@ -1204,6 +1204,7 @@ fsops_status fsops_mxfp8_paged_chunk_attention(const void* q_bf16, long long ldq
   // a scale of zero: so small a one that every exponent is zero, and the mask still -inf
   ca.scale_log2 = std::fmax(std::fabs(sm_scale) * 1.4426950408889634f, 1e-37f);
   ca.negate = sm_scale < 0.f ? 1 : 0;
+  ca.extra_arrivals = std::min(g_extra.load(), 1000u);  // (a barrier counts to 2^20)
   // a wait's try that fails has slept for about 4 us
   ca.tries = static_cast<uint32_t>(std::min<uint64_t>(g_timeout_ns.load() / 2000 + 1, 1u << 30));
   const cudaError_t e = launch_chunk(ca, static_cast<cudaStream_t>(stream));

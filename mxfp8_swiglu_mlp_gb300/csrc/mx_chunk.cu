@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         mbar_init(&ctl->p_full[i][u], 128);
       }
       mbar_init(&ctl->o_first[i], 1);
-      mbar_init(&ctl->o_done[i], 1);
+      mbar_init(&ctl->o_done[i], 1 + a.extra_arrivals);
       mbar_init(&ctl->fin[i], 1);
       mbar_init(&ctl->it_full[i], 32);
       mbar_init(&ctl->it_empty[i], kSoftWarps + kConvWarps + 3);
@@ -359,14 +359,12 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
     Ring<NK> kr;
     Ring<kSlots> vr;
     uint32_t q_phase = 0, p_phase = 0, odd = 0;
-    bool issued = false;
     for (;; it.step()) {
       if (!wait(c, &ctl->it_full[it.slot], it.phase, 4u)) break;
       const int tiles = __shfl_sync(0xFFFFFFFFu, ctl->item[it.slot].t1 - ctl->item[it.slot].t0, 0);
       const bool pair = __shfl_sync(0xFFFFFFFFu, ctl->item[it.slot].rows, 0) > 128;
       warp_arrive(&ctl->it_empty[it.slot], lane);
       if (tiles == 0) break;
-      issued = true;
       if (!wait(c, &ctl->q_full, q_phase, 5u)) break;
       q_phase ^= 1u;
       tc_fence_after();
@@ -473,13 +471,6 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       ok = ok && skip_k(tiles) && skip_v(tiles);
       if (!ok) break;
     }
-    if (issued && *c.stop != 0u) {  // products in flight end before tensor memory is given back
-      if (elect_one()) tc_commit(&ctl->fin[m]);
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(&ctl->fin[m], 0) && globaltimer_ns() - t0 < 20000000ull) {
-      }
-    }
-    __syncwarp();
   } else if (warp >= kSoftWarps) {
     convert_items<NV, kSlots>(c, ctl, smem + L::raw, smem + L::sv, smem + L::v, t - 32 * kSoftWarps, lane);
   } else {
@@ -648,10 +639,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
       warp_arrive(&ctl->it_empty[slot], lane);
     }
   }
-  // ---- the end: every role is here, and nothing is in flight
-  __syncthreads();
-  if (t == 0 && ctl->stop != 0u)  // FSOPS_ERR_TIMEOUT
-    atomicCAS(a.status, 0u, (5u << 24) | (ctl->stop << 16) | (blockIdx.x & 0xFFFFu));
+  finish(a, ctl, kMmaWarp, t);
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 

@@ -32,6 +32,7 @@ struct ChunkArgs {
   int tile_rows;              // rows of a query tile: 256, or kChunkFewRows for the kernel for few rows
   int grid;
   uint32_t tries;             // of a wait before it gives up
+  uint32_t extra_arrivals;    // test hook: arrivals more than any product makes when a tile's outputs are done
 };
 
 // Rows of a query tile for T rows of B sequences in groups of G heads.

@@ -228,13 +228,6 @@ struct Loader {
     }
     return true;
   }
-  // copies in flight land before the block ends (only after a wait ran out)
-  __device__ __forceinline__ void drain() {
-    const uint64_t t0 = globaltimer_ns();
-    for (int i = 0; i < stages; ++i)
-      while (!mbar_try_wait(full + i, phase ^ (i >= slot ? 1u : 0u)) && globaltimer_ns() - t0 < 20000000ull) {
-      }
-  }
 };
 
 // The role of a load warp (v: the one for V); the other one walks the plan.
@@ -277,7 +270,30 @@ __device__ __forceinline__ void load_items(const Ctx& c, Ctl* ctl, uint8_t* k, u
     if (w.t0 == w.t1 || !ld.item(c, w, lane)) break;
     if (ld.v) warp_arrive(&ctl->it_empty[it.slot], lane);
   }
-  if (*c.stop != 0u) ld.drain();
+  // the thread's copies have landed when the block ends, whatever the reason
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- the end
+// All threads, after their roles: true where a wait ran out.  The products that
+// the two product warps have issued (the same lane of each, all of them) end
+// then before tensor memory is given back; a role may give up long after the
+// product warps have left, so this is decided here and not by them.
+template <class Ctl>
+__device__ __forceinline__ void finish(const ChunkArgs& a, Ctl* ctl, int product_warp, int t) {
+  __syncthreads();
+  if (ctl->stop == 0u) return;
+  const int m = (t >> 5) - product_warp;
+  if (m == 0 || m == 1) {
+    if (elect_one()) tc_commit(&ctl->fin[m]);
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(&ctl->fin[m], 0) && globaltimer_ns() - t0 < 20000000ull) {
+    }
+    __syncwarp();
+  }
+  if (t == 0)  // FSOPS_ERR_TIMEOUT
+    atomicCAS(a.status, 0u, (5u << 24) | (ctl->stop << 16) | (blockIdx.x & 0xFFFFu));
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------- values that are not finite
