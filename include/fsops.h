@@ -298,11 +298,14 @@ size_t fsops_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int 
  *             seq_lens[b] - n_b + i.  n_b <= seq_lens[b] <= max_pages * P.
  *   block_table [B, max_pages] int32 as above.
  * All three are read on the device (a captured graph replays with new
- * contents).  Metadata outside these limits, or a page id outside
- * [0, num_pages) that would be used, is reported in the status word
- * (fsops_read_kernel_status on the pointer that holds it, site 1 for lengths
- * and offsets, 2 for a page id) and never followed; what belongs to the
- * sequence concerned is unspecified.
+ * contents).  Metadata outside these limits (the length of a sequence without
+ * new tokens may be anything), or a page id outside [0, num_pages) that would
+ * be used, is reported in the status word (fsops_read_kernel_status on the
+ * pointer that holds it, site 1 for lengths and offsets, 2 for a page id, with
+ * the sequence) and never followed.  What the attention gives for the sequence
+ * concerned is unspecified; the append leaves out its rows, or the row whose
+ * page it is.  Where offsets decrease, a row that two sequences claim may go to
+ * either.
  *
  * Rotation: the first rotary_dim dimensions of a head form pairs (u, w), the
  * pair i being elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when
@@ -350,7 +353,8 @@ fsops_status fsops_qk_norm_rope(const void* q_bf16, long long ldq, const void* k
  *   status      device word (4-byte aligned) for the report above; an
  *               attention workspace's first word serves.
  *   Limits: D = 128; P in {16, 32, 64, 128}; B, Hkv <= 65535; T >= 0;
- *   T * Hkv < 2^31; row distances as above.  Two rows of one call must not fall
+ *   T * Hkv < 2^31; max_pages * P <= 2^24; num_pages * Hkv * P < 2^31; row
+ *   distances as above.  Two rows of one call must not fall
  *   into the same slot (which of them stays is unspecified).
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
 fsops_status fsops_mxfp8_kv_append(const void* k_bf16, long long ldk, const void* v_bf16, long long ldv,

@@ -239,6 +239,20 @@ __device__ __forceinline__ void report(uint32_t* status, uint32_t code, uint32_t
   atomicCAS(status, 0u, (code << 24) | (site << 16) | (static_cast<uint32_t>(b) & 0xFFFFu));
 }
 
+// Whether a sequence's offsets and length are within the limits (the length
+// only where there are new tokens).
+__device__ __forceinline__ bool sequence_ok(const KvAppendArgs& a, int c0, int c1, int len) {
+  const bool offsets = (c0 >= 0) & (c0 <= c1) & (c1 <= a.T), length = (len >= c1 - c0) & (len <= (a.max_pages << a.log2P));
+  return offsets & (length | (c0 == c1));
+}
+// The sequences looked at by one of `blocks` blocks.  (Not by the rows: none
+// finds a sequence whose offsets decrease or lie outside the rows.)
+__device__ __forceinline__ void check_sequences(const KvAppendArgs& a, int block, int blocks) {
+#pragma unroll 1
+  for (int b = block * kRopeThreads + threadIdx.x; b < a.B; b += blocks * kRopeThreads)
+    if (!sequence_ok(a, __ldg(a.cu + b), __ldg(a.cu + b + 1), __ldg(a.lens + b))) report(a.status, 1u, 1u, b);
+}
+
 // Where a token goes: its row of head 0 in the cache (-1: nowhere).
 struct Slot {
   long long row;
@@ -249,11 +263,10 @@ __device__ __forceinline__ Slot find_slot(const KvAppendArgs& a, int t, int lane
   r.row = -1;
   r.pos = 0;
   const int b = find_sequence(a.cu, a.B, t, lane);
-  const int place = __ldg(a.lens + b) - (__ldg(a.cu + b + 1) - t);  // lens[b] - n + (t - cu[b])
-  if (place < 0 || (place >> a.log2P) >= a.max_pages) {
-    if (lane == 0) report(a.status, 1u, 1u, b);
-    return r;
-  }
+  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), len = __ldg(a.lens + b);
+  // (no short circuits: the three loads go out together)
+  if (!((t >= c0) & (t < c1) & sequence_ok(a, c0, c1, len))) return r;  // reported by check_sequences
+  const int place = len - (c1 - t);
   const int page = __ldg(a.table + static_cast<long long>(b) * a.max_pages + (place >> a.log2P));
   if (page < 0 || page >= a.num_pages) {
     if (lane == 0) report(a.status, 1u, 2u, b);
@@ -264,15 +277,21 @@ __device__ __forceinline__ Slot find_slot(const KvAppendArgs& a, int t, int lane
   return r;
 }
 
-// Unit (token, part): the KV heads of k, then of v, four a step.
+// Unit (token, part): the KV heads of k, then of v, four a step.  The last
+// `checks` blocks look at the sequences instead, beside the others.
 __global__ void __launch_bounds__(kRopeThreads, kAppendBlocks)
-    kv_append_kernel(const __grid_constant__ KvAppendArgs a, int parts, unsigned units) {
+    kv_append_kernel(const __grid_constant__ KvAppendArgs a, int parts, unsigned units, int checks) {
   constexpr int D = 128, LPH = 8, HW = 4;
   __shared__ __align__(16) float2 tab[kRopeThreads / 32][D / 2];
   __shared__ long long turns[D / 2];
   __shared__ __align__(16) float peak[kRopeThreads / 32][HW][D / 8];  // largest magnitude of each chunk
   const int lane = threadIdx.x & 31, l = lane % LPH, sub = lane / LPH, warp = threadIdx.x >> 5;
-  const unsigned warps = gridDim.x * (kRopeThreads / 32);
+  const int blocks = static_cast<int>(gridDim.x) - checks;
+  const unsigned warps = blocks * (kRopeThreads / 32);
+  if (static_cast<int>(blockIdx.x) >= blocks) {
+    check_sequences(a, blockIdx.x - blocks, checks);
+    return;
+  }
   load_turns(turns, a.rope);
   unsigned u = blockIdx.x * (kRopeThreads / 32) + warp;
   if (u >= units) return;
@@ -364,7 +383,9 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, int sms, cudaStream_t stream
 cudaError_t launch_kv_append(const KvAppendArgs& a, int sms, cudaStream_t stream) {
   const int steps = (2 * a.Hkv + 3) / 4;
   const int parts = token_parts(a.T, steps, sms * kAppendBlocks), units = a.T * parts;
-  kv_append_kernel<<<unit_blocks(units, sms * kAppendBlocks), kRopeThreads, 0, stream>>>(a, parts, units);
+  const int checks = std::min((a.B - 1) / kRopeThreads + 1, 32);
+  const unsigned blocks = unit_blocks(units, sms * kAppendBlocks - checks);  // (all of them resident at once)
+  kv_append_kernel<<<blocks + checks, kRopeThreads, 0, stream>>>(a, parts, units, checks);
   return cudaGetLastError();
 }
 
