@@ -310,9 +310,9 @@ size_t fsops_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int 
  * Rotation: the first rotary_dim dimensions of a head form pairs (u, w), the
  * pair i being elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when
  * interleaved; it becomes (u cos a - w sin a, w cos a + u sin a) with
- * a = position * inv_freq[i], the angle exact to 2^-31 turns at any int32
+ * a = position * inv_freq[i], the angle good to 2^-25 turns at any int32
  * position.  The other dimensions stay.
- *   inv_freq    device, [rotary_dim / 2] fp32, finite.
+ *   inv_freq    device, [rotary_dim / 2] fp32, of magnitude 2^40 at most.
  *   rotary_dim  0 (no rotation) .. D, a multiple of 32. */
 typedef struct {
   const float* inv_freq;

@@ -10,10 +10,12 @@
 //   x' = x * rsqrt(mean(x^2) + eps) * gamma        (without gamma: x' = x)
 //   (u, w) -> (u cos a - w sin a, w cos a + u sin a),  a = p * inv_freq[i],
 // on the R / 2 pairs of its first R dimensions.  The angle is taken modulo a
-// turn in integers: inv_freq / 2 pi as a 64-bit fraction of a turn (from fp64,
-// relative error 2^-53) times p, the overflow of the product being whole
-// turns.  So a position of any size keeps an angle good to 2^-31 turns, where
-// the fp32 product p * inv_freq is off by p * 2^-24 radians.
+// turn in integers: inv_freq / 2 pi as a 64-bit fraction of a turn (good to
+// 2^-64, from a sum of two fp64 numbers) times p, the overflow of the product
+// being whole turns.  Its top 32 bits, good to 2^-32, become an fp32 number of
+// half turns, which costs 2^-26 of a turn at most.  So a position of any size
+// keeps an angle good to 2^-25 turns, where the fp32 product p * inv_freq is off
+// by p * 2^-24 radians, and an fp64 one by p * 2^-54.
 //
 // Both kernels move each byte once and are bound by HBM (long inputs) or by
 // launch latency (a decode step).  A lane holds two chunks of 8 consecutive
@@ -47,11 +49,17 @@ constexpr int kRopeThreads = 128;
 constexpr int kRopeBlocks = 6, kAppendBlocks = 5;
 constexpr int kMaxRotary = 256;
 
-// Fraction of a turn per position, in units of 2^-64 turns.
+// Fraction of a turn per position, in units of 2^-64 turns (|inv_freq| up to 2^40).
 __device__ __forceinline__ long long turn_fraction(float inv_freq) {
-  double r = static_cast<double>(inv_freq) * 0.15915494309189533577;  // 1 / (2 pi)
-  r -= rint(r);                                                       // whole turns per position
-  return __double2ll_rn(r * 18446744073709551616.0);                  // 2^64
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / (2 pi) = kHi + kLo
+  const double f = static_cast<double>(inv_freq), r = f * kHi;
+  // what the roundings of the product and of the constant left, below 2^-15: added to a
+  // number whose last bit is 2^-64, so that it stands in the last bits
+  constexpr double kLast = 0x1.8p-12;
+  const double rest = fma(f, kLo, fma(f, kHi, -r)) + kLast;
+  // without the whole turns per position; a sum that overflows is one more
+  return static_cast<long long>(static_cast<unsigned long long>(__double2ll_rn((r - rint(r)) * 18446744073709551616.0)) +
+                                static_cast<unsigned long long>(__double_as_longlong(rest) - __double_as_longlong(kLast)));
 }
 // sine and cosine of position p's angle.
 __device__ __forceinline__ void turn_sincos(long long f, int p, float* sn, float* cs) {
