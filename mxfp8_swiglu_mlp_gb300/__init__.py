@@ -128,13 +128,13 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device: Optional[int] = None) -> Optional[int]:
     if stream is None:
         import torch
 
         # the handle itself: torch.cuda.current_stream() makes an object around
         # it, 3 us of a small call's 10
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -244,42 +244,54 @@ def fsops_mxfp8_paged_decode_attention(q, k_codes, k_scales, v_codes, v_scales, 
            "fsops_mxfp8_paged_decode_attention")
 
 
-def _dev_ptr(t, where: str) -> Optional[int]:
+def _current_device() -> int:
+    import torch
+
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):  # no GPU here: no tensor is on it
+        return -2
+
+
+def _dev_ptr(t, where: str, device: int) -> Optional[int]:
     """Pointer of a tensor of the current device (an address or None as it is)."""
     if t is None or t.__class__ is int:
         return t
-    if t.is_cuda:
+    if t.get_device() == device:
         return t.data_ptr()
-    raise FsopsError(ERR_INVALID_ARG, where + " (a tensor that is not on the GPU)")
+    raise FsopsError(ERR_INVALID_ARG, where + (" (a tensor of another GPU than the current one)" if t.is_cuda else
+                                               " (a tensor that is not on the GPU)"))
 
 
-def _rope(rope, where: str):
+def _rope(rope, where: str, device: int):
     if rope is None:
         return None
     inv_freq, rotary_dim, interleaved = rope
-    return ctypes.byref(_Rope(_dev_ptr(inv_freq, where), rotary_dim, 1 if interleaved else 0))
+    return ctypes.byref(_Rope(_dev_ptr(inv_freq, where, device), rotary_dim, 1 if interleaved else 0))
 
 
 def fsops_qk_norm_rope(q, ldq: int, k, ldk: int, gamma_q, gamma_k, eps: float, positions, rope, q_out, ldq_out: int,
                        k_out, ldk_out: int, T: int, Hq: int, Hkv: int, D: int, stream=None) -> None:
     """Per-head RMSNorm and rotation of q and k.  ``rope`` is (inv_freq,
     rotary_dim, interleaved) or None."""
-    w = "fsops_qk_norm_rope"
-    _check(lib.fsops_qk_norm_rope(_dev_ptr(q, w), ldq, _dev_ptr(k, w), ldk, _dev_ptr(gamma_q, w), _dev_ptr(gamma_k, w),
-                                  eps, _dev_ptr(positions, w), _rope(rope, w), _dev_ptr(q_out, w), ldq_out,
-                                  _dev_ptr(k_out, w), ldk_out, T, Hq, Hkv, D, _stream(stream)), w)
+    w, d = "fsops_qk_norm_rope", _current_device()
+    _check(lib.fsops_qk_norm_rope(_dev_ptr(q, w, d), ldq, _dev_ptr(k, w, d), ldk, _dev_ptr(gamma_q, w, d),
+                                  _dev_ptr(gamma_k, w, d), eps, _dev_ptr(positions, w, d), _rope(rope, w, d),
+                                  _dev_ptr(q_out, w, d), ldq_out, _dev_ptr(k_out, w, d), ldk_out, T, Hq, Hkv, D,
+                                  _stream(stream, d)), w)
 
 
 def fsops_mxfp8_kv_append(k, ldk: int, v, ldv: int, gamma_k, eps: float, positions, rope, k_codes, k_scales, v_codes,
                           v_scales, num_pages: int, block_table, max_pages: int, cu, seq_lens, T: int, B: int,
                           Hkv: int, D: int, page_size: int, status, stream=None) -> None:
     """New keys (norm, rotation) and values into the paged MXFP8 cache (see fsops.h)."""
-    w = "fsops_mxfp8_kv_append"
-    _check(lib.fsops_mxfp8_kv_append(_dev_ptr(k, w), ldk, _dev_ptr(v, w), ldv, _dev_ptr(gamma_k, w), eps,
-                                     _dev_ptr(positions, w), _rope(rope, w), _dev_ptr(k_codes, w),
-                                     _dev_ptr(k_scales, w), _dev_ptr(v_codes, w), _dev_ptr(v_scales, w), num_pages,
-                                     _dev_ptr(block_table, w), max_pages, _dev_ptr(cu, w), _dev_ptr(seq_lens, w), T, B,
-                                     Hkv, D, page_size, _dev_ptr(status, w), _stream(stream)), w)
+    w, d = "fsops_mxfp8_kv_append", _current_device()
+    _check(lib.fsops_mxfp8_kv_append(_dev_ptr(k, w, d), ldk, _dev_ptr(v, w, d), ldv, _dev_ptr(gamma_k, w, d), eps,
+                                     _dev_ptr(positions, w, d), _rope(rope, w, d), _dev_ptr(k_codes, w, d),
+                                     _dev_ptr(k_scales, w, d), _dev_ptr(v_codes, w, d), _dev_ptr(v_scales, w, d),
+                                     num_pages, _dev_ptr(block_table, w, d), max_pages, _dev_ptr(cu, w, d),
+                                     _dev_ptr(seq_lens, w, d), T, B, Hkv, D, page_size, _dev_ptr(status, w, d),
+                                     _stream(stream, d)), w)
 
 
 def fsops_paged_chunk_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int, page_size: int,
@@ -292,13 +304,14 @@ def fsops_mxfp8_paged_chunk_attention(q, ldq: int, k_codes, k_scales, v_codes, v
                                       D: int, page_size: int, window: int, sm_scale: float, workspace, ws_bytes: int,
                                       stream=None) -> None:
     """Causal attention of each sequence's new tokens over the paged MXFP8 KV cache (see fsops.h)."""
-    w = "fsops_mxfp8_paged_chunk_attention"
-    _check(lib.fsops_mxfp8_paged_chunk_attention(_dev_ptr(q, w), ldq, _dev_ptr(k_codes, w), _dev_ptr(k_scales, w),
-                                                 _dev_ptr(v_codes, w), _dev_ptr(v_scales, w), num_pages,
-                                                 _dev_ptr(block_table, w), max_pages, _dev_ptr(cu, w),
-                                                 _dev_ptr(seq_lens, w), _dev_ptr(out, w), ldo, T, B, Hq, Hkv, D,
-                                                 page_size, window, sm_scale, _dev_ptr(workspace, w), ws_bytes,
-                                                 _stream(stream)), w)
+    w, d = "fsops_mxfp8_paged_chunk_attention", _current_device()
+    _check(lib.fsops_mxfp8_paged_chunk_attention(_dev_ptr(q, w, d), ldq, _dev_ptr(k_codes, w, d),
+                                                 _dev_ptr(k_scales, w, d), _dev_ptr(v_codes, w, d),
+                                                 _dev_ptr(v_scales, w, d), num_pages,
+                                                 _dev_ptr(block_table, w, d), max_pages, _dev_ptr(cu, w, d),
+                                                 _dev_ptr(seq_lens, w, d), _dev_ptr(out, w, d), ldo, T, B, Hq, Hkv, D,
+                                                 page_size, window, sm_scale, _dev_ptr(workspace, w, d), ws_bytes,
+                                                 _stream(stream, d)), w)
 
 
 def fsops_mxfp8_swiglu_mlp_block(x_bf16, gamma_bf16, eps: float, residual: bool, w_gateup, w_down, scales, y_bf16,
