@@ -283,7 +283,7 @@ __device__ __forceinline__ void merge_rows(const ChunkArgs& a, const Item& w, co
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] = fmaf(f, v[i], o[i]);
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;  // (NaN stays)
+    const float inv = divisor(M, den);
     if (lane < rows) put32(y + 32 * chunk, o, inv);
   }
 }
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_kernel(const __grid_constant_
         float* rec = nullptr;
         uint16_t* y = nullptr;
         if (whole) {
-          const float inv = st.l == 0.f ? 0.f : 1.f / st.l;  // (NaN stays)
+          const float inv = divisor(st.m, st.l);
           f0 *= inv, f1 *= inv;
           const int rr = w.r0 + min(tr, w.rows - 1), tok = rr / a.G;
           y = a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD;

@@ -184,7 +184,7 @@ __device__ __forceinline__ void merge_share(const ChunkArgs& a, const Item& w, c
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = row0 + 4 * i + (lane >> 3), rr = w.r0 + row, tok = rr / a.G;
-    const float inv = den[i] == 0.f ? 0.f : 1.f / den[i];  // (NaN stays)
+    const float inv = divisor(__shfl_sync(0xFFFFFFFFu, M, 4 * i + (lane >> 3)), den[i]);
     if (row < w.rows)  // (stored order 0, 2, 1, 3)
       *reinterpret_cast<uint2*>(a.out + static_cast<long long>(w.c0 + tok) * a.ldo + (w.hk * a.G + rr - tok * a.G) * kD + dim) =
           make_uint2(bf16x2_rn(o[i].x * inv, o[i].z * inv), bf16x2_rn(o[i].y * inv, o[i].w * inv));
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kBlock, 1) chunk_few_kernel(const __grid_const
         float sum = (ctl->sums[0][r] + ctl->sums[1][r]) + (ctl->sums[2][r] + ctl->sums[3][r]);
         if (ctl->hidden[slot].any != 0u) sum = sum_or_nan(a, w, ctl->hidden[slot], r, sum);
         const float m = ctl->scale[turn][r];
-        const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : m == kNone ? 0.f : 1.f;  // (NaN stays)
+        const float f = whole ? divisor(m, sum) : m == kNone ? 0.f : 1.f;
         const size_t rec = whole ? 0 : static_cast<size_t>(w.slot) * a.slot_rows;
         if (!whole && lane < 16 && r < w.rows)  // (all four warps write the same)
           a.rec_ml[rec + r] = make_float2(m == kNone ? -INFINITY : m, sum);

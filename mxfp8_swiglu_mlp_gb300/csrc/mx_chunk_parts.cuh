@@ -21,6 +21,13 @@ constexpr uint32_t kScales = 512;              // bytes kept for a tile's scales
 constexpr uint32_t kOperand = kKeys * kD * 2;  // V as bf16: two halves of 64 dimensions,
 constexpr uint32_t kHalf = kOperand / 2;       // [tokens][128 bytes], 128-byte swizzle
 constexpr float kGrow = 8.f;                   // in powers of two
+// A row's maximum in fp32 is off by half its last bit, which all its probabilities
+// and their sum have as a common factor: 2^64 at most below this maximum, but
+// beyond fp32 above it.
+constexpr float kTopScore = 2147483648.f;
+__device__ __forceinline__ float divisor(float m, float l) {
+  return fabsf(m) < kTopScore ? 1.f / l : __int_as_float(0x7FC00000);
+}
 static_assert(kKeys % 16 == 0 && kCodes % 1024 == 0, "16-token groups, whole swizzle atoms");
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
