@@ -50,15 +50,21 @@ constexpr int kRopeBlocks = 6, kAppendBlocks = 5;
 constexpr int kMaxRotary = 256;
 
 // Fraction of a turn per position, in units of 2^-64 turns (|inv_freq| up to 2^40).
+// (An fp64 instruction takes an SM some 30 cycles a warp, so what integers can do
+// for them is left to integers: widening, and the product with 2^64.)
 __device__ __forceinline__ long long turn_fraction(float inv_freq) {
   constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / (2 pi) = kHi + kLo
-  const double f = static_cast<double>(inv_freq), r = f * kHi;
+  const uint32_t b = __float_as_uint(inv_freq);  // (zero and subnormal ones become 2^-127 or so)
+  const double f = __longlong_as_double((static_cast<long long>(b & 0x7FFFFFFFu) << 29) + (896LL << 52) |
+                                        static_cast<long long>(static_cast<unsigned long long>(b >> 31) << 63));
+  const double r = f * kHi;
   // what the roundings of the product and of the constant left, below 2^-15: added to a
   // number whose last bit is 2^-64, so that it stands in the last bits
   constexpr double kLast = 0x1.8p-12;
   const double rest = fma(f, kLo, fma(f, kHi, -r)) + kLast;
-  // without the whole turns per position; a sum that overflows is one more
-  return static_cast<long long>(static_cast<unsigned long long>(__double2ll_rn((r - rint(r)) * 18446744073709551616.0)) +
+  // without the whole turns per position, times 2^64; a sum that overflows is one more turn
+  const double turn = __longlong_as_double(__double_as_longlong(r - rint(r)) + (64LL << 52));
+  return static_cast<long long>(static_cast<unsigned long long>(__double2ll_rn(turn)) +
                                 static_cast<unsigned long long>(__double_as_longlong(rest) - __double_as_longlong(kLast)));
 }
 // sine and cosine of position p's angle.
