@@ -370,8 +370,9 @@ fsops_status fsops_mxfp8_kv_append(const void* k_bf16, long long ldk, const void
  *   with window > 0, t > p - window, p the row's token (see cu above),
  *   out[i, h, :] = bf16( sum_t softmax(s)[t] * V^[t, h / G, :] ).
  * Scores, maxima and sums are fp32; the probabilities enter the second product
- * rounded to bf16.  A row whose largest score times log2(e) is 2^31 or more away
- * from zero is NaN: fp32 does not tell its probabilities apart.
+ * rounded to bf16 (the decode attention keeps 22 bits of them).  A row whose
+ * largest score times log2(e) is 2^31 or more away from zero is NaN: fp32 does
+ * not tell its probabilities apart.
  *   q           bf16 [T] rows of Hq heads of D, ldq elements apart.
  *   out         bf16, rows ldo apart; must not overlap q.  Padding rows stay as
  *               they are.

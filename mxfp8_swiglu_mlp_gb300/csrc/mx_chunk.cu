@@ -48,7 +48,7 @@
 // bytes a cycle (48 cycles for 128 rows, 64 keys and 32 dimensions, 42 for 48
 // keys; 64 for 16 tokens of V), 2340 cycles for a key tile and 256 rows; the
 // streams' exponentials and hand-offs bring that to 3200.  Measured: 2048 tokens
-// of 32 query heads against 16 k tokens (515 GFLOP) in 399 us, 1.29 PFLOP/s, 0.70
+// of 32 query heads against 16 k tokens (515 GFLOP) in 403 us, 1.28 PFLOP/s, 0.69
 // of cuBLAS's bf16 rate.
 // The roles' code is at the limit of what is fetched in time: the same roles in
 // other orders of their branches take 399 to 485 us (this order is among the

@@ -282,10 +282,10 @@ __device__ __forceinline__ void load_items(const Ctx& c, Ctl* ctl, uint8_t* k, u
 }
 
 // ---------------------------------------------------------------- the end
-// All threads, after their roles: true where a wait ran out.  The products that
-// the two product warps have issued (the same lane of each, all of them) end
-// then before tensor memory is given back; a role may give up long after the
-// product warps have left, so this is decided here and not by them.
+// All threads, after their roles.  Where a wait ran out, the products that the two
+// product warps have issued (one lane of each, always the same) end before tensor
+// memory is given back; a role may give up long after the product warps have
+// left, so this is decided here and not by them.
 template <class Ctl>
 __device__ __forceinline__ void finish(const ChunkArgs& a, Ctl* ctl, int product_warp, int t) {
   __syncthreads();
@@ -323,7 +323,8 @@ __device__ __noinline__ float sum_or_nan(const ChunkArgs& a, const Item& w, cons
 #pragma unroll 1
   for (int i = 0; i < 512; ++i) {
     const int tok = (i < 256 ? w.lo : all_upto) + (i & 255);
-    if ((hn.bits[i >> 8][(i & 255) >> 5] >> (i & 31) & 1u) != 0u && tok >= from && tok < upto) sum = __int_as_float(0x7FC00000);
+    const bool noted = (hn.bits[i >> 8][(i & 255) >> 5] >> (i & 31) & 1u) != 0u;
+    if (noted && tok >= from && tok < upto) sum = __int_as_float(0x7FC00000);
   }
   return sum;
 }
@@ -370,6 +371,9 @@ __device__ __noinline__ void convert_rest(const ChunkArgs& a, const Item& w, Hid
 // token: eight lanes four pieces of two tokens each, which keeps their 16-byte
 // stores (and, with the ring's halves exchanged in every other row, their
 // loads) apart in the banks.  nan: nan_bits of all codes, top: the largest scale.
+// (Measured, the chunk of 2048 tokens against 16 k / five drafted tokens for each
+// of 64 sequences: 410 / 137 us; with NaN found by maxima of magnitudes and the
+// scales' second product here 442 / 144.)
 __device__ __forceinline__ void convert16(const uint8_t* raw, uint32_t s, uint8_t* row, int first, bool on, uint32_t& nan,
                                           uint32_t& top) {
   const uint4 x = *reinterpret_cast<const uint4*>(raw);

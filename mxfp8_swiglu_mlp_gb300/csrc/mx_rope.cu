@@ -28,7 +28,7 @@
 // are computed once a block, whose warps go on to further tokens.
 //
 // Measured: 16384 tokens of 32 + 8 heads of 128 (336 MB) in 60 us, 5.6 TB/s; the
-// append of 11 k tokens of 8 heads (87 MB) in 22 us; one token 2.7 and 2.8 us.
+// append of 14 k tokens of 8 heads (87 MB) in 22 us; one token 2.6 and 3.2 us.
 // With fractions, sines and pair partners computed lane by lane the two took 166
 // and 104 us.
 #include <cuda_bf16.h>
@@ -45,7 +45,7 @@ namespace {
 constexpr int kRopeThreads = 128;
 // Blocks an SM, at 80 and 96 registers a thread.  Measured: norm_rope with 16384
 // tokens of 32 + 8 heads of 128 takes 60 us with 6, 65 with 5, 81 with 8 (spills);
-// the append of 11k tokens of 8 heads 22 us with 5, 25 with 6 (spills).
+// the append of 14 k tokens of 8 heads 22 us with 5, 25 with 6 (spills).
 constexpr int kRopeBlocks = 6, kAppendBlocks = 5;
 constexpr int kMaxRotary = 256;
 
