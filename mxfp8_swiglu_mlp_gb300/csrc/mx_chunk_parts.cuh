@@ -134,8 +134,11 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t m) {
   return make_uint2(mul_bf16x2(even, m), mul_bf16x2(odd, m));
 }
 // Of four codes, bits 7, 15, 23, 31 say whether one is NaN (all bits but the sign
-// set): adding one changes the bit above (a carry out of a code comes from NaN alone).
+// set): adding one changes the bit above.  A negative NaN carries into the next
+// code, which may be taken for NaN then (448 is); nan_bits_exact leaves the signs
+// out.
 __device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w + 0x01010101u) ^ w; }
+__device__ __forceinline__ uint32_t nan_bits_exact(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
 constexpr uint32_t kNanBits = 0x80808080u;
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -350,7 +353,7 @@ __device__ __noinline__ void convert_rest(const ChunkArgs& a, const Item& w, Hid
         const uint32_t m = ((s - kPlainScale + 127u) << 7) * 0x10001u;
         p = make_uint2(mul_bf16x2(p.x, m), mul_bf16x2(p.y, m));
       }
-      const uint32_t n = s == 255u ? kNanBits : nan_bits(x);
+      const uint32_t n = s == 255u ? kNanBits : nan_bits_exact(x);
       p.x |= (n & 0x80u ? 0x7FFFu : 0u) | (n & 0x800000u ? 0x7FFF0000u : 0u);
       p.y |= (n & 0x8000u ? 0x7FFFu : 0u) | (n & 0x80000000u ? 0x7FFF0000u : 0u);
 #pragma unroll

@@ -146,3 +146,32 @@ def test_nan_scale_of_a_key(fs, new, ctx, Hkv, G):
     tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2 * (2.0 ** -17 * mag + 2.0 ** -18)) * (A + np.abs(out))
     assert np.isnan(got[bad]).all()
     assert np.all(np.abs(got - out)[~bad] <= tol[~bad])
+
+
+@pytest.mark.parametrize("new,ctx,G", [(1, 130, 4), (6, 130, 4), (40, 130, 1), (300, 40, 1)])
+def test_neighbours_of_a_nan_code_stay(fs, new, ctx, G):
+    """The largest codes beside NaN codes, in every place of a word of four."""
+    import torch
+
+    bt = Batch([new], [ctx], 1, 16, 260)
+    _finite_cache(bt)
+    codes, page, slot = bt.codes[1], bt.table[0, 0], 3
+    for d in range(0, 128, 2):
+        codes[page, 0, slot, d + (d >> 2 & 1)] = 0x7E if d & 8 else 0xFE
+    r = Run(fs, bt, G)
+    ref = r.want()
+    bad = np.zeros(128, bool)
+    codes = codes.copy()
+    for d in range(0, 128, 2):
+        at = d + 1 - (d >> 2 & 1)
+        codes[page, 0, slot, at] = 0xFF if d & 16 else 0x7F
+        bad[at] = True
+    r.cache[2].copy_(_dev(codes))
+    r.call()
+    torch.cuda.synchronize()
+    assert r.status() == 0
+    got = bf16_bits_to_f64(r.got()[:new, :G * 128]).reshape(new, G, 128)
+    out, A, mag = ref["out"][:new], ref["absv"][:new], ref["mag"][:new, :, None]
+    tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2 * (2.0 ** -17 * mag + 2.0 ** -18)) * (A + np.abs(out))
+    assert np.isnan(got[:, :, bad]).all()  # (all rows see the token)
+    assert np.all((np.abs(got - out) <= tol)[:, :, ~bad])
