@@ -103,17 +103,23 @@ struct Scale {
   float ch, cl;  // log2(e) / T
   int top;       // 64 times the largest logit's power of two
   float low;     // logits below it weigh nothing
-  int wide;      // powers too large for the table's way
+  int wide;      // powers that the table's way does not take (is_wide)
   float max;
+  double c;      // log2(e) / T, where wide
 };
+// Powers too large for fp32 to tell 2^-38 of one, or a log2(e) / T whose second part would have
+// too few bits left (from temperatures of 2^99 on; x c is good to 2^-39 below, as x is at most 2^11 / c).
+__device__ __forceinline__ bool is_wide(float max_power, float ch) {
+  return !(fabsf(max_power) < 2000.f && ch < 1e30f && ch > 0x1p-99f);
+}
+__device__ __noinline__ double powers_per(float T) { return 0x1.71547652b82fep+0 / static_cast<double>(T); }
 constexpr float kMagic = 12582912.f;  // 3 * 2^22: a float near it has its last bit at one
 constexpr int kUnit = 45;
 
 // The last bit is always set: what is cut off is half a unit, as often above as
 // below, so that sums of many small weights are not too small.
 __device__ __noinline__ u64 weight_wide(float x, const Scale& s) {
-  const double c = static_cast<double>(s.ch) + static_cast<double>(s.cl);
-  return static_cast<u64>(__double2ll_rd(exp2((static_cast<double>(x) - static_cast<double>(s.max)) * c + kUnit))) | 1ull;
+  return static_cast<u64>(__double2ll_rd(exp2((static_cast<double>(x) - static_cast<double>(s.max)) * s.c + kUnit))) | 1ull;
 }
 __device__ __forceinline__ u64 weight_near(float x, float ch, float cl, int top, const u64* powers) {
   const float p = x * ch;
@@ -833,13 +839,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
     return;
   }
   const float max_power = mx * ch, row_low = fmaxf(mx - span, -kMost);
-  const bool wide = !(fabsf(max_power) < 2000.f && ch < 1e30f);
+  const bool wide = is_wide(max_power, ch);
   if (mx == kInf || (plain && (wide || row_low <= -kMost))) {  // (the last: forbidden logits counted as the lowest ones, which weigh something)
     if (t == 0) a.tokens[row] = kLeft;
     return;
   }
   if (list) {
-    if (t == 0) ctl->scale = Scale{ch, cl, wide ? 0 : __float2int_rn(64.f * max_power), row_low, wide ? 1 : 0, mx};
+    if (t == 0) ctl->scale = Scale{ch, cl, wide ? 0 : __float2int_rn(64.f * max_power), row_low, wide ? 1 : 0, mx, wide ? powers_per(T) : 0.0};
     for (int i = t; i < kMaxCluster * kList; i += kThreads) ctl->list[i] = -kInf;
     const float edge = edge_of(ctl, own, k, w_full(vecs, per));
     again(__ballot_sync(0xFFFFFFFFu, own >= edge), [&](float x, int i) {
@@ -1085,10 +1091,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   constexpr float kLog2e = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0cp-26f;
   const float ch = kLog2e / T, cl = (fmaf(-ch, T, kLog2e) + kLog2eLo) / T;
   const float max_power = mx * ch, low = fmaxf(fmaf(-(kUnit + 1.5f) * 0.6931472f, T, mx), -kMost);
-  const bool wide = !(fabsf(max_power) < 2000.f && ch < 1e30f);
+  const bool wide = is_wide(max_power, ch);
   const int powers_top = wide ? 0 : __float2int_rn(64.f * max_power);
   const float unit = kMagic - ceilf(wide ? 0.f : max_power);  // for rough weights
-  if (t == 0) ctl->scale = Scale{ch, cl, powers_top, low, wide ? 1 : 0, mx};
+  if (t == 0) ctl->scale = Scale{ch, cl, powers_top, low, wide ? 1 : 0, mx, wide ? powers_per(T) : 0.0};
   __syncthreads();
   const Scale& s = ctl->scale;  // (for calls)
   const bool by_mass = p < 1.f;
