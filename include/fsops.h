@@ -467,7 +467,8 @@ fsops_status fsops_mxfp8_paged_tree_attention(const void* q_bf16, long long ldq,
  *                         no other overlap.
  *   parent      [B] or NULL (each its own);  keep, want [B].
  *   held        [num_pages] or NULL: how often something else holds a page (a
- *               cache of common beginnings); negative counts as 0.
+ *               cache of common beginnings); negative counts as 0, more than 2^30
+ *               as 2^30.
  *   refs        [num_pages]: gets how often each page is held afterwards, `held`
  *               included.
  *   copy_src, copy_dst    [B] page ids.

@@ -39,6 +39,7 @@ __device__ __forceinline__ void report(uint32_t* status, uint32_t site, int b) {
 // 7500 10.1 to 9.9, 23300 in 16000 14.7 to 10.8.
 constexpr int kMostBlocks = 16, kUpdateThreads = 1024, kUpdateWarps = kUpdateThreads / 32;
 constexpr int kEntries = 128;  // of a table row at a time
+constexpr int kMostHeld = 1 << 30;  // of what else holds a page: entries of the tables on top still fit an int
 constexpr int kOnePages = 16384, kOneEntries = 8192;  // pages and entries of the tables up to which one block does it all
 
 struct Row {
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kUpdateThreads, 1) pages_update_kernel(const _
   const int p0 = static_cast<int>(static_cast<long long>(a.num_pages) * rank / kUpdateBlocks),
             p1 = static_cast<int>(static_cast<long long>(a.num_pages) * (rank + 1) / kUpdateBlocks);
 #pragma unroll 4
-  for (int p = p0 + t; p < p1; p += kUpdateThreads) refs[p] = a.held != nullptr ? max(__ldg(a.held + p), 0) : 0;
+  for (int p = p0 + t; p < p1; p += kUpdateThreads) refs[p] = a.held != nullptr ? min(max(__ldg(a.held + p), 0), kMostHeld) : 0;
   meet();
   // what stays of the tables, and how many entries hold a page
   const bool in_place = a.table == a.new_table;
