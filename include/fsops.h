@@ -506,9 +506,10 @@ fsops_status fsops_mxfp8_kv_copy_pages(uint8_t* k_codes, uint8_t* k_scales, uint
  * j < count[b].  (Keys stay rotated for their own positions: a node on the
  * accepted path at depth j has that of token start[b] + j.)
  *   block_table [B, max_pages];  start, count [B];  path [B, max_path].
- *   A path goes up (path[b, j] > path[b, j - 1], path[b, 0] >= 0), count[b] <=
- *   max_path, and no token lies past max_pages * P; a sequence for which that does
- *   not hold is reported (site 1) and left as it is.  A token whose page id is
+ *   A path goes up (path[b, j] > path[b, j - 1], path[b, 0] >= 0), 0 <= count[b] <=
+ *   max_path, start[b] >= 0, and no token lies past max_pages * P; a sequence for
+ *   which that does not hold is reported (site 1) and left as it is.  With
+ *   count[b] = 0 its start and path may be anything.  A token whose page id is
  *   outside [0, num_pages) is not moved (site 2).  The pages from token start[b] on
  *   belong to sequence b alone.
  *   0 <= max_path <= 65535 (0: nothing to do), B * layers * Hkv < 2^31, B <= 65535;

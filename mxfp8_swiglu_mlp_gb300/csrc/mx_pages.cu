@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kCompactThreads, 8) compact_kernel(const __gri
   // the path goes up and stays within the table (its first 32 places are read with the count)
   const int p0 = lane < a.max_path ? __ldg(path + lane) : 0, left = __shfl_up_sync(0xFFFFFFFFu, p0, 1);
   auto good = [&](int p, int before) { return p > before && p >= 0 && static_cast<long long>(start) + p < tokens; };
-  bool ok = n >= 0 && n <= a.max_path && start >= 0;
+  bool ok = n >= 0 && n <= a.max_path && (start >= 0 || n == 0);  // (no early end: all three loads are on their way together)
   if (ok && lane < n) ok = good(p0, lane > 0 ? left : -1);
   for (int j = lane + 32; ok && j < n; j += 32) ok = good(__ldg(path + j), __ldg(path + j - 1));
   if (!__all_sync(0xFFFFFFFFu, ok)) {
