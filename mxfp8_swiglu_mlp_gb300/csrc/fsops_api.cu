@@ -1034,12 +1034,12 @@ size_t chunk_ws_bytes(int sms, int slot_rows) {
   const size_t rows = static_cast<size_t>(chunk_slots(sms)) * slot_rows;
   return round_up(chunk_rec_offset() + rows * (kChunkD * sizeof(float) + sizeof(float2)), 256);
 }
-// The checked arguments of the chunk attention and of the trees' (T == 0: no more than the checks).
+// The checked arguments of the chunk attention and of the trees' (mask_words > 0; T == 0: no more than the checks).
 fsops_status chunk_args(ChunkArgs& ca, const void* q_bf16, long long ldq, const uint8_t* k_codes,
                         const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales, int num_pages,
                         const int32_t* block_table, int max_pages, const int32_t* cu, const int32_t* seq_lens,
                         void* out_bf16, long long ldo, int T, int B, int Hq, int Hkv, int D, int page_size, int window,
-                        float sm_scale, void* workspace, size_t ws_bytes, bool tree) {
+                        float sm_scale, void* workspace, size_t ws_bytes, int mask_words) {
   fsops_status st = chunk_shape(T, B, Hq, Hkv, D, page_size, num_pages, max_pages);
   if (st != FSOPS_OK) return st;
   if (q_bf16 == nullptr || k_codes == nullptr || k_scales == nullptr || v_codes == nullptr || v_scales == nullptr ||
@@ -1059,8 +1059,10 @@ fsops_status chunk_args(ChunkArgs& ca, const void* q_bf16, long long ldq, const 
   if (st != FSOPS_OK) return st;
   ca = ChunkArgs();
   ca.G = Hq / Hkv;
-  ca.tile_rows = tree ? tree_tile_rows(T, B, ca.G, Hkv, static_cast<long long>(max_pages) * page_size, di->sms)
-                      : chunk_tile_rows(T, B, ca.G);
+  // the most tokens of a sequence that a tree's rows can see: what the table has room for, or the window and the nodes
+  long long tokens = static_cast<long long>(max_pages) * page_size;
+  if (window > 0) tokens = std::min(tokens, static_cast<long long>(window) + 32 * mask_words);
+  ca.tile_rows = mask_words > 0 ? tree_tile_rows(T, B, ca.G, Hkv, tokens, di->sms) : chunk_tile_rows(T, B, ca.G);
   ca.slot_rows = chunk_slot_rows(T, ca.G, ca.tile_rows);
   ca.grid = di->sms;
   if (ws_bytes < chunk_ws_bytes(di->sms, ca.slot_rows)) return FSOPS_ERR_INVALID_ARG;
@@ -1243,7 +1245,7 @@ fsops_status fsops_mxfp8_paged_chunk_attention(const void* q_bf16, long long ldq
   ChunkArgs ca;
   const fsops_status st = chunk_args(ca, q_bf16, ldq, k_codes, k_scales, v_codes, v_scales, num_pages, block_table,
                                      max_pages, cu, seq_lens, out_bf16, ldo, T, B, Hq, Hkv, D, page_size, window,
-                                     sm_scale, workspace, ws_bytes, false);
+                                     sm_scale, workspace, ws_bytes, 0);
   if (st != FSOPS_OK || T == 0) return st;
   const cudaError_t e = launch_chunk(ca, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FSOPS_OK : cuda_failed(e, "chunk_kernel launch");
@@ -1263,7 +1265,7 @@ fsops_status fsops_mxfp8_paged_tree_attention(const void* q_bf16, long long ldq,
   TreeArgs ta;
   const fsops_status st = chunk_args(ta, q_bf16, ldq, k_codes, k_scales, v_codes, v_scales, num_pages, block_table,
                                      max_pages, cu, seq_lens, out_bf16, ldo, T, B, Hq, Hkv, D, page_size, window,
-                                     sm_scale, workspace, ws_bytes, true);
+                                     sm_scale, workspace, ws_bytes, mask_words);
   if (st != FSOPS_OK || T == 0) return st;
   ta.mask = mask;
   ta.words = mask_words;

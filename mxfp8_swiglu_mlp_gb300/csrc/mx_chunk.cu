@@ -709,12 +709,15 @@ int chunk_tile_rows(int T, int B, int G) {
 
 // Trees: the kernel for few rows too where its query tiles are no more than the blocks
 // and no block has more than some 24 key tiles, by the lengths that the tables have room
-// for.  There a call's time is its longest chain, and shorter items make that shorter.
+// for or, where it is less, a window with a mask's nodes (lengths themselves are on the
+// device).  There a call's time is its longest chain, and shorter items make that shorter.
 // Measured, trees of 16 nodes, 4 heads a KV head of 8, this kernel against that one (us):
 // one tree and 500 tokens 16.4 to 14.5, 4 k 37 to 25, 16 k (15 key tiles a block) 50 to
 // 35, 64 k (62) 81 to 78; one of 64 nodes and 4 k (16) 47 to 35, 16 k (62) 66 to 76; one
 // of 128 and 4 k (31) 49 to 48; 8 trees and 2 k (15) 28.9 to 26.9, 8 k (62) 60 to 78; 16
-// trees and 500 tokens (256 query tiles) 16.7 to 33.
+// trees and 500 tokens (256 query tiles) 16.7 to 33.  With a window, 8 k tokens in tables
+// for 128 k: one tree of 16 nodes and 512 tokens 16.1 to 14.5, 2 k 28.3 to 19.9, 4 k 33.8
+// to 29.9; of 64 nodes and 512 24.7 to 16.2, 2 k 41.7 to 26.8; 8 trees and 512 16.9 to 14.8.
 int tree_tile_rows(int T, int B, int G, int Hkv, long long tokens, int blocks) {
   const long long rows = (static_cast<long long>(T) * G + B - 1) / B;  // of a sequence, on average
   const long long tiles = (rows + kChunkFewRows - 1) / kChunkFewRows * B * Hkv, keys = (tokens + kKeys - 1) / kKeys;

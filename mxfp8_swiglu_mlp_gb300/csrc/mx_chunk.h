@@ -48,7 +48,7 @@ struct TreeArgs : ChunkArgs {
 
 // Rows of a query tile for T rows of B sequences in groups of G heads.
 int chunk_tile_rows(int T, int B, int G);
-// The same of trees, whose tables have room for `tokens` tokens a sequence (as many rows or fewer).
+// The same of trees, whose rows see `tokens` tokens of a sequence at most (as many rows or fewer).
 int tree_tile_rows(int T, int B, int G, int Hkv, long long tokens, int blocks);
 // Partial-result slots of a call and their rows.
 inline int chunk_slots(int sms) { return 2 * sms; }
