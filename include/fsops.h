@@ -424,6 +424,10 @@ size_t fsops_paged_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv
  *               window only (may be NULL without), counted as base or as
  *               seq_lens[b] - 1 where they lie outside base .. seq_lens[b] - 1.
  *   A row whose mask and window leave nothing gives zeros.
+ *   Whatever masks and positions say, the page ids of the tokens max(0, base -
+ *   window + 1) .. seq_lens[b] - 1 (all of them without a window) are looked up and
+ *   have to be valid, those of nodes that no mask names among them; ids before them
+ *   may be stale.
  *   workspace: fsops_paged_chunk_attention_workspace_bytes().
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
 fsops_status fsops_mxfp8_paged_tree_attention(const void* q_bf16, long long ldq, const uint8_t* k_codes,
