@@ -428,6 +428,9 @@ size_t fsops_paged_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv
  *   window + 1) .. seq_lens[b] - 1 (all of them without a window) are looked up and
  *   have to be valid, those of nodes that no mask names among them; ids before them
  *   may be stale.
+ *   A window is over the held tokens only: where a node must not see those above it
+ *   that are `window` positions away or more, as in a model with a sliding window,
+ *   their bits are left out of its mask.
  *   workspace: fsops_paged_chunk_attention_workspace_bytes().
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
 fsops_status fsops_mxfp8_paged_tree_attention(const void* q_bf16, long long ldq, const uint8_t* k_codes,

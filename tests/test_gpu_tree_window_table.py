@@ -5,7 +5,7 @@ import pytest
 
 from tests._util import bf16_bits_to_f64
 from tests.test_gpu_chunk_attention import _compare, _finite_cache
-from tests.test_gpu_norm_rope import Batch
+from tests.test_gpu_norm_rope import Batch, _dev
 from tests.test_gpu_tree_attention import Run, _wide, fs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -85,3 +85,27 @@ def test_nan_at_the_ends_of_windows_and_many_query_tiles(fs, window):  # noqa: F
         got = bf16_bits_to_f64(r.got()).reshape(bt.T, r.Hq, 128)
         assert np.array_equal(np.isnan(got).any(axis=2), np.repeat(nan[:, None], r.Hq, 1))
         assert np.abs(got - ref)[~nan].max() <= 0.02 * np.abs(ref).max()
+
+
+# both kernels
+@pytest.mark.parametrize("Hkv", [2, 8])
+@pytest.mark.parametrize("window", [1, 7, 33])
+def test_a_chain_longer_than_a_sliding_window(fs, window, Hkv):  # noqa: F811
+    """With the bits of the nodes a window away left out it is a causal chunk with that window."""
+    import oracle
+    import torch
+
+    bt = Batch([150, 70], [90, 10], Hkv, 16, 40 + window)
+    _finite_cache(bt)
+    r = Run(fs, bt, 4, "tree", window)
+    r.masks = [np.tril(np.ones((n, n), bool)) & ~np.tril(np.ones((n, n), bool), -window) for n in (150, 70)]
+    r.pos = np.concatenate([c + np.arange(n) for n, c in ((150, 90), (70, 10))]).astype(np.int32)
+    r.mask.copy_(_dev(oracle.pack_mask(r.masks, r.words, bt.T).view(np.int32)))
+    r.dpos.copy_(_dev(r.pos))
+    chunk = oracle.paged_chunk_attention(bf16_bits_to_f64(r.qbits), bt.codes[0], bt.scales[0], bt.codes[1], bt.scales[1],
+                                         bt.table, bt.cu, bt.lens, window, r.sm)
+    assert np.abs(r.want()["out"] - chunk["out"]).max() <= 1e-12 * np.abs(chunk["out"]).max()
+    r.call()
+    torch.cuda.synchronize()
+    assert r.status() == 0
+    _compare(r)
