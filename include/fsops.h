@@ -549,9 +549,11 @@ fsops_status fsops_mxfp8_kv_compact(uint8_t* k_codes, uint8_t* k_scales, uint8_t
  *   logprobs [rows] fp32 or NULL: ln of the probability with which the token was
  *            drawn, among the kept ones (0 for the largest logit taken, -inf without
  *            any token).
- * The token is the one of exact sums of weights in units of 2^-45 of the largest: it
- * does not depend on the order of sums.  One with less than a third of a unit is never
- * drawn.  logprobs are good to 2^-19 + 2^-22 (|logprob| + 13).
+ * Weights are whole numbers of units, 2^-45 of the largest one, each good to a unit and
+ * 2^-37 of itself, and are added as such: the token does not depend on the order of
+ * sums, and is that of exact weights wherever u and top_p lie further from every border
+ * than 2^-36 + V 2^-45 (largest weight / mass) of the mass.  One with less than a third
+ * of a unit is never drawn.  logprobs are good to 2^-19 + 2^-22 (|logprob| + 13).
  *   0 <= rows < 2^27, 1 <= V <= 393216, V <= ld < 2^40, rows * ld <= 2^60.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED (a pointer that its type's size
  * does not divide), CUDA. */

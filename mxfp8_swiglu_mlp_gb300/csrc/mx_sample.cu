@@ -9,8 +9,10 @@
 //
 // A token is a whole number: it is the same whatever the order of sums only if
 // the sums are.  So weights are whole numbers, units of 2^-45 of the largest, and
-// added as such, and each is good to about its unit: u falls between a border
-// here and the same border in 64-bit floating point about once in 10^10 / V rows.
+// added as such, and each is good to a unit and 2^-37 of itself (the median is off by
+// one unit, the worst of the largest by some 160): u falls between a border here and
+// the same border in 64-bit floating point about once in 10^10 / V rows.  (Weights that
+// are alike are rounded alike, so V of a few units each can move a border by V units.)
 // (With weights good to 2^-22, as of a hardware exponential, every other row of a
 // flat distribution over 150000 tokens would be in doubt.)
 //
