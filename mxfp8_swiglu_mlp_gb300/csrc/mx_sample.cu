@@ -1476,6 +1476,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (!exact) ahead = exact_units(ahead), target = exact_units(target), all = exact_units(all);
         const bool found = there && search(true, first, end, 0u, ahead, target, exact ? 0ull : doubt_of(all));
         if (!found && exact) {
+          R.meet();  // (a search may end right behind its reading of what others write again)
           cut = by_k;
           search(true, 0u, last, 0u, 0ull, target, 0ull);  // (it lies elsewhere: the edges' weights were too rough)
         }
