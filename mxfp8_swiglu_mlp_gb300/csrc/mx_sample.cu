@@ -1028,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if constexpr (half) most = fmaxf(__low2float(most2), __high2float(most2));
   const bool plain = k <= 0 && !(p < 1.f);
   float own = plain ? kInf : R.largest();  // no element of the thread's run is larger
-  const bool listing = k > 1 && k <= kListK;
+  const bool greedy = !(T >= 1.17549435e-38f) || k == 1, listing = !greedy && k > 0 && k <= kListK;
   float mx = most;
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
@@ -1053,7 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     return;
   }
-  if (!(T >= 1.17549435e-38f) || k == 1) {  // the largest one, the first of its equals
+  if (greedy) {  // the largest one, the first of its equals
     uint32_t best = 0xFFFFFFFFu;
     if (own >= mx) {
       for (int v = R.v1 - 1; v >= R.v0; --v) {
