@@ -432,6 +432,10 @@ size_t fsops_paged_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv
  *   that are `window` positions away or more, as in a model with a sliding window,
  *   their bits are left out of its mask.
  *   workspace: fsops_paged_chunk_attention_workspace_bytes().
+ *   Lengths are on the device, so small batches are told by what the tables have room
+ *   for (max_pages * P, or window + 32 * mask_words where it is less): in a table much
+ *   wider than its sequences one tree of 16 nodes against 4 k tokens takes 33 us, in
+ *   one cut to size 20.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
 fsops_status fsops_mxfp8_paged_tree_attention(const void* q_bf16, long long ldq, const uint8_t* k_codes,
                                               const uint8_t* k_scales, const uint8_t* v_codes,
@@ -449,7 +453,8 @@ fsops_status fsops_mxfp8_paged_tree_attention(const void* q_bf16, long long ldq,
  * next two calls move the bytes, of all layers at once.  A cache of `layers`
  * layers is one allocation per array, [layers, num_pages, ...] with each layer as
  * above (a layer's part is what the attention gets); tables hold for all layers.
- * D = 128; P in {16, 32, 64, 128}; num_pages * Hkv * P < 2^31; layers 1 .. 4096.
+ * D = 128; P in {16, 32, 64, 128}; Hkv <= 65535; num_pages * Hkv * P < 2^31; layers
+ * 1 .. 4096.
  *
  * fsops_kv_pages_update -- page tables brought to new lengths, one launch: the new
  * sequence b
@@ -469,9 +474,10 @@ fsops_status fsops_mxfp8_paged_tree_attention(const void* q_bf16, long long ldq,
  * site 3).
  *   table, lens           [B, max_pages], [B]: the old ones; entries past a
  *                         sequence's last page are not read.
- *   new_table, new_lens   the new ones, written whole (-1 past the last page).
- *                         May be table and lens themselves where parent is NULL;
- *                         no other overlap.
+ *   new_table, new_lens   the new ones, written whole (-1 past the last page; 64
+ *                         sequences of up to 375 pages take 10 us in a table as wide,
+ *                         15 in one of 8192).  May be table and lens themselves
+ *                         where parent is NULL; no other overlap.
  *   parent      [B] or NULL (each its own);  keep, want [B].
  *   held        [num_pages] or NULL: how often something else holds a page (a
  *               cache of common beginnings); negative counts as 0, more than 2^30
@@ -499,7 +505,7 @@ size_t fsops_kv_pages_workspace_bytes(int B, int num_pages);
  * and scales of K and V, for i < n.  One launch.
  *   src, dst    [n] page ids on the device.  A pair with a negative id, or of a
  *               page with itself, is left out; so is one with an id >= num_pages,
- *               which is reported (site 2, with i).  No page may be dst of one
+ *               which is reported (site 2, with i mod 65536).  No page may be dst of one
  *               pair and src or dst of another.
  *   n >= 0, layers * n < 2^31;  status as fsops_mxfp8_kv_append.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */

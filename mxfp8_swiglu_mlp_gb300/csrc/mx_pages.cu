@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kUpdateThreads, 1) pages_update_kernel(const _
 // ---------------------------------------------------------------- copies
 // 16 bytes a lane, eight loads on their way together; a warp copies a piece of
 // 4 KB.  Pages and their scales are whole numbers of 64 bytes.  Bound by HBM: 769 MB
-// read and written in 117 us, 6.6 TB/s, 0.97 of the copy rate; 34 MB (mostly in L2)
+// read and written in 121 us, 6.3 TB/s, 0.93 of the copy rate; 34 MB (mostly in L2)
 // in 6 us.
 constexpr int kCopyThreads = 256, kPieceBytes = 4096;
 

@@ -50,7 +50,9 @@
 //
 // What bounds it: phases.  A row alone is 4 (top-k of few) to 25 of them, each with
 // a barrier of the block or the cluster and some hundred instructions that are
-// fetched once; many rows run two blocks an SM, which issue half of the time.
+// fetched once; many rows run two blocks an SM, which issue half of the time.  (Two
+// blocks leave a thread 64 registers; the clusters' kernel spills 60 to 68 bytes, the
+// rows' none.)
 // Measured (us): one row of 150001 bf16 logits, top-k 50 and top-p 10.6, unfiltered
 // 16, top-p alone 32 (a peaked row) to 42 (a flat one); 1024 x 32003 bf16 unfiltered
 // 48 (1.4 TB/s); 256 x 128000 fp32 with a mixture of all filters 148, with top-k 50
@@ -295,13 +297,16 @@ struct Ctl {
   Scale scale;
   int first[2];
   uint32_t nearest, farthest;
-  // written by the other blocks
-  float max[kMaxCluster], edge[kMaxCluster];
-  uint32_t index[kMaxCluster], ties[kMaxCluster], listed[kMaxCluster], from[kMaxCluster], to[kMaxCluster];
-  u64 mass[2][kMaxCluster], all[kMaxCluster];
-  Found found;
-  Cut cut;
-  uint32_t redo;
+  // Written by the other blocks (as the first one's list, list_index and hist[1] are), each
+  // before one meeting and read behind it; what is written again is not before another.
+  float max[kMaxCluster], edge[kMaxCluster];  // once
+  uint32_t index[kMaxCluster], ties[kMaxCluster];  // once
+  uint32_t listed[kMaxCluster], from[kMaxCluster], to[kMaxCluster];  // each step of a search
+  u64 mass[2][kMaxCluster];  // each pass for top-p's mass
+  u64 all[kMaxCluster];      // the counts' (read before they are shared), each pass of the draw
+  Found found;               // by the first block, when it has looked through the counts
+  Cut cut;                   // by the first block, at the end of a search over a few
+  uint32_t redo;             // set by the block itself before a meeting, cleared by the one that drew behind it, read behind the next
 };
 
 template <bool half>
@@ -1306,32 +1311,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         uint32_t count = n;
         u64 one = 0;
         if (range > 0u) {
-        const int shift = range < kBins ? 0 : 23 - __clz(static_cast<int>(range));
-        xhi = of_key(top - lo), xlo = of_key(top - hi);
-        R.clear(masses);
-        if (own >= xlo) {
-          R.between(xlo, xhi, [&](float x, int) {
-            const uint32_t d = top - key_of(x) - lo;
-            if (d > range) return;  // (a zero beside -0)
-            R.count(static_cast<int>(d >> shift), masses ? weight(x, s, ctl->powers) : 0ull, masses);
-          });
-        }
-        R.combine(masses);
-        if (R.rank == 0) R.find(masses, need, target - base);
-        const Found f = R.share();
-        if (f.bin < 0) return false;
-        need -= f.before;
-        base += f.mass_before;
-        lo += static_cast<uint32_t>(f.bin) << shift;
-        hi = min(hi, lo + ((1u << shift) - 1u));
-        if (masses ? f.count == 1u : need == f.count) {  // all of it
-          cut.least = of_key(top - hi);
-          cut.ties = 0u;
-          return !masses || sure(base, base + f.mass);
-        }
-        if (shift != 0) continue;
-        count = f.count;
-        if (masses) one = f.mass / f.count;
+          const int shift = range < kBins ? 0 : 23 - __clz(static_cast<int>(range));
+          xhi = of_key(top - lo), xlo = of_key(top - hi);
+          R.clear(masses);
+          if (own >= xlo) {
+            R.between(xlo, xhi, [&](float x, int) {
+              const uint32_t d = top - key_of(x) - lo;
+              if (d > range) return;  // (a zero beside -0)
+              R.count(static_cast<int>(d >> shift), masses ? weight(x, s, ctl->powers) : 0ull, masses);
+            });
+          }
+          R.combine(masses);
+          if (R.rank == 0) R.find(masses, need, target - base);
+          const Found f = R.share();
+          if (f.bin < 0) return false;
+          need -= f.before;
+          base += f.mass_before;
+          lo += static_cast<uint32_t>(f.bin) << shift;
+          hi = min(hi, lo + ((1u << shift) - 1u));
+          if (masses ? f.count == 1u : need == f.count) {  // all of it
+            cut.least = of_key(top - hi);
+            cut.ties = 0u;
+            return !masses || sure(base, base + f.mass);
+          }
+          if (shift != 0) continue;
+          count = f.count;
+          if (masses) one = f.mass / f.count;
         } else if (masses) {
           one = weight(of_key(top - lo), s, ctl->powers);
         }
@@ -1537,16 +1542,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             r.add(w.x + w.y);
           }
         }
-      } else
-      for (int v = R.v0; v < R.v1; ++v) {
-        float x[E];
-        unpack<half>(R.data[v], x);
+      } else {
+        for (int v = R.v0; v < R.v1; ++v) {
+          float x[E];
+          unpack<half>(R.data[v], x);
 #pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          const float2 w0 = rough2(make_float2(x[e], x[e + 1]), ch2, cl2, unit2, low),
-                       w1 = rough2(make_float2(x[e + 2], x[e + 3]), ch2, cl2, unit2, low);
-          r.add(((x[e] >= least ? w0.x : 0.f) + (x[e + 1] >= least ? w0.y : 0.f)) +
-                ((x[e + 2] >= least ? w1.x : 0.f) + (x[e + 3] >= least ? w1.y : 0.f)));
+          for (int e = 0; e < E; e += 4) {
+            const float2 w0 = rough2(make_float2(x[e], x[e + 1]), ch2, cl2, unit2, low),
+                         w1 = rough2(make_float2(x[e + 2], x[e + 3]), ch2, cl2, unit2, low);
+            r.add(((x[e] >= least ? w0.x : 0.f) + (x[e + 1] >= least ? w0.y : 0.f)) +
+                  ((x[e + 2] >= least ? w1.x : 0.f) + (x[e + 3] >= least ? w1.y : 0.f)));
+          }
         }
       }
       sum = r.units();
