@@ -51,7 +51,7 @@
 // What bounds it: phases.  A row alone is 4 (top-k of few) to 25 of them, each with
 // a barrier of the block or the cluster and some hundred instructions that are
 // fetched once; many rows run two blocks an SM, which issue half of the time.  (Two
-// blocks leave a thread 64 registers; the clusters' kernel spills 60 to 68 bytes, the
+// blocks leave a thread 64 registers; the clusters' kernel spills 52 to 76 bytes, the
 // rows' none.)
 // Measured (us): one row of 150001 bf16 logits, top-k 50 and top-p 10.6, unfiltered
 // 16, top-p alone 32 (a peaked row) to 42 (a flat one); 1024 x 32003 bf16 unfiltered
@@ -111,11 +111,13 @@ struct Scale {
   float max;
   double c;      // log2(e) / T, where wide
 };
-// Powers too large for fp32 to tell 2^-38 of one, or a log2(e) / T whose second part would have
-// too few bits left (from temperatures of 2^99 on; x c is good to 2^-39 below, as x is at most 2^11 / c).
-__device__ __forceinline__ bool is_wide(float max_power, float ch) {
-  return !(fabsf(max_power) < 2000.f && ch < 1e30f && ch > 0x1p-99f);
-}
+// Powers too large for fp32 to tell 2^-38 of one; and from temperatures of 2^99 on, where the
+// parts of log2(e) / T come near fp32's last bit, 2^-149, logits beyond kFar (up to there x c is
+// good to 2^-40; below that temperature it is whatever they are, as those that weigh anything
+// are at most 2^11 / c).  With logits as models give them such a temperature, infinity for
+// instance, is not wide: 256 x 128000 of them take 1510 us in fp64, 150 as fp32 and the table.
+constexpr float kHot = 0x1p99f, kFar = 0x1p109f;
+__device__ __forceinline__ bool is_wide(float max_power, float ch, bool far) { return !(fabsf(max_power) < 2000.f && ch < 1e30f) || far; }
 __device__ __noinline__ double powers_per(float T) { return 0x1.71547652b82fep+0 / static_cast<double>(T); }
 constexpr float kMagic = 12582912.f;  // 3 * 2^22: a float near it has its last bit at one
 constexpr int kUnit = 45;
@@ -300,7 +302,7 @@ struct Ctl {
   // Written by the other blocks (as the first one's list, list_index and hist[1] are), each
   // before one meeting and read behind it; what is written again is not before another.
   float max[kMaxCluster], edge[kMaxCluster];  // once
-  uint32_t index[kMaxCluster], ties[kMaxCluster];  // once
+  uint32_t index[kMaxCluster], ties[kMaxCluster], far[kMaxCluster];  // once
   uint32_t listed[kMaxCluster], from[kMaxCluster], to[kMaxCluster];  // each step of a search
   u64 mass[2][kMaxCluster];  // each pass for top-p's mass
   u64 all[kMaxCluster];      // the counts' (read before they are shared), each pass of the draw
@@ -594,6 +596,26 @@ __device__ __forceinline__ float log_share(float x, float max, float T, float wh
 // How many of the warps with `per` of `vecs` vectors each have all of theirs.
 __device__ __forceinline__ int w_full(int vecs, int per) { return per >= 32 ? vecs / per : 0; }
 
+// Whether a logit of the row (each thread's vectors v0 .. v1 - 1) lies beyond kFar; -inf does not.
+template <bool half>
+__device__ __noinline__ bool any_far(const uint4* data, int v0, int v1, Ctl* ctl, int C, int rank) {
+  float m = 0.f;
+  for (int v = v0; v < v1; ++v) {
+    float x[Vec<half>::n];
+    unpack<half>(data[v], x);
+#pragma unroll
+    for (int e = 0; e < Vec<half>::n; ++e) m = fmaxf(m, x[e] == -kInf ? 0.f : fabsf(x[e]));
+  }
+  uint32_t far = __syncthreads_or(m > kFar) != 0 ? 1u : 0u;
+  if (C > 1) {
+    cg::cluster_group cluster = cg::this_cluster();
+    if (static_cast<int>(threadIdx.x) < C) cluster.map_shared_rank(ctl->far, static_cast<int>(threadIdx.x))[rank] = far;
+    cluster.sync();
+    for (int r = 0; r < C; ++r) far |= ctl->far[r];
+  }
+  return far != 0u;
+}
+
 // The smallest logit that min-p leaves; by one thread.
 __device__ __noinline__ float least_of(float max, float min_p, float T) {
   const double at = static_cast<double>(max) + log(static_cast<double>(fminf(min_p, 1.f))) * static_cast<double>(T);
@@ -846,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
     return;
   }
   const float max_power = mx * ch, row_low = fmaxf(mx - span, -kMost);
-  const bool wide = is_wide(max_power, ch);
+  const bool wide = is_wide(max_power, ch, T >= kHot);  // (no look at all logits: a list's few weights are fast either way)
   if (mx == kInf || (plain && (wide || row_low <= -kMost))) {  // (the last: forbidden logits counted as the lowest ones, which weigh something)
     if (t == 0) a.tokens[row] = kLeft;
     return;
@@ -1094,11 +1116,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     edge = edge == kInf ? 0.f : -kMost;
     mx = 0.f;
   }
+  const bool far = T >= kHot && any_far<half>(part, R.v0, R.v1, ctl, C, rank);
   // log2(e) / T as two numbers
   constexpr float kLog2e = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0cp-26f;
   const float ch = kLog2e / T, cl = (fmaf(-ch, T, kLog2e) + kLog2eLo) / T;
   const float max_power = mx * ch, low = fmaxf(fmaf(-(kUnit + 1.5f) * 0.6931472f, T, mx), -kMost);
-  const bool wide = is_wide(max_power, ch);
+  const bool wide = is_wide(max_power, ch, far);
   const int powers_top = wide ? 0 : __float2int_rn(64.f * max_power);
   const float unit = kMagic - ceilf(wide ? 0.f : max_power);  // for rough weights
   if (t == 0) ctl->scale = Scale{ch, cl, powers_top, low, wide ? 1 : 0, mx, wide ? powers_per(T) : 0.0};

@@ -77,3 +77,20 @@ def test_many_long_rows_next_to_a_border(fs, k):  # noqa: F811
     r = Run(fs, x, False, u, temperature=3e38, top_k=k)
     r.call()
     r.check()
+
+
+# logits on both sides of 2^109, from where on such a temperature's weights are taken in fp64, and ordinary ones;
+# forbidden logits are none of them
+@pytest.mark.parametrize("V", [501, 40001])
+@pytest.mark.parametrize("T,size", [(6e32, 6.4e32), (6e32, 7e32), (1e35, 6.4e32), (1.2e38, 6.4e32), (3e38, 6.4e32), (np.inf, 6.4e32),
+                                    (np.inf, 1e20), (np.inf, 3.0)])
+def test_logits_smaller_than_the_temperature(fs, T, size, V):  # noqa: F811
+    rng = np.random.default_rng(8)
+    x = (rng.uniform(-1.0, 1.0, (40, V)) * size).astype(np.float32)
+    x[:, 3::5] = -np.inf
+    u, d = (np.array(v) for v in zip(*[_next_to(_borders(r, T)[:-1]) for r in x]))
+    near = d < FAR
+    assert near.sum() > 20
+    r = Run(fs, x[near], False, u[near].astype(np.float32), temperature=T)
+    r.call()
+    r.check()
